@@ -7,6 +7,7 @@ method runs in the library's CUDA kernels; there is no fallback.  Importing this
 module raises if libgdr.so has not been built.
 """
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -31,7 +32,9 @@ EXPORTS = ["gdr_version", "gdr_last_error", "gdr_prefill_workspace_bytes", "gdn_
            "gdn_prefill_varlen", "kda_prefill_varlen", "gdr_backward_workspace_bytes",
            "gdn_backward", "kda_backward", "gdn_prefill_ex", "kda_prefill_ex", "gdn_decode_ex",
            "kda_decode_ex", "gdn_verify_ex", "kda_verify_ex", "gdn_prefill_varlen_ex",
-           "kda_prefill_varlen_ex"]
+           "kda_prefill_varlen_ex", "gdr_lin_workspace_bytes", "lin_prefill", "lin_decode",
+           "lin_backward", "gdr_attn_workspace_bytes", "attn_prefill", "attn_backward",
+           "gdr_attn_decode_workspace_bytes", "attn_decode", "kv_append"]
 
 # fused prologue flags of the *_ex entry points (prologue= keyword below)
 PROLOGUE_L2NORM_QK = 1   # q, k raw: L2-normalised per (token, head) inside the kernels
@@ -97,6 +100,26 @@ def _load():
     lib.gdr_prefill_path.argtypes = [i, i, i, i]
     lib.gdr_workspace_status.restype = i
     lib.gdr_workspace_status.argtypes = [vp, sz, vp]
+    u = ctypes.c_float
+    for name, args in (
+            ("lin_prefill", [vp, vp, vp, fp, fp, vp, fp, i, i, i, i, i, i, vp, sz, vp]),
+            ("lin_decode", [vp, vp, vp, fp, fp, vp, i, i, i, i, i, vp]),
+            ("lin_backward", [vp, vp, vp, fp, fp, vp, fp, vp, vp, vp, fp, i, i, i, i, i, i, vp, sz,
+                              vp]),
+            ("attn_prefill", [vp, vp, vp, vp, vp, fp, i, i, i, i, i, i, i, i, u, i, vp, sz, vp]),
+            ("attn_backward", [vp, vp, vp, vp, vp, fp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, u,
+                               i, vp, sz, vp]),
+            ("attn_decode", [vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, i, u, i, vp,
+                             sz, vp]),
+            ("kv_append", [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, vp, sz, vp])):
+        f = getattr(lib, name)
+        f.restype = i
+        f.argtypes = args
+    for name, n in (("gdr_lin_workspace_bytes", 7), ("gdr_attn_workspace_bytes", 8),
+                    ("gdr_attn_decode_workspace_bytes", 9)):
+        f = getattr(lib, name)
+        f.restype = sz
+        f.argtypes = [i] * n
     lib.gdr_timing_start.restype = i
     lib.gdr_timing_start.argtypes = []
     lib.gdr_timing_stop.restype = i
@@ -432,6 +455,292 @@ def kda_backward(q, k, v, alpha, beta, s0, do, ds_final=None, *, workspace=None,
 
 def backward_workspace_bytes(B, T, H, dk, dv, kda):
     return lib.gdr_backward_workspace_bytes(B, T, H, dk, dv, int(kda))
+
+
+# ---- linear attention with one decay per head; sliding-window softmax attention -----------
+
+def _on(device, stream):
+    """Context in which a call on `stream` (None: the device's current one) allocates and
+    launches: outputs and workspaces belong to that stream, the launch goes to that device."""
+    if stream is not None:
+        return torch.cuda.stream(stream)
+    if device.index != torch.cuda.current_device():
+        return torch.cuda.device(device)
+    return contextlib.nullcontext()
+
+
+def _scratch(workspace, need, device, what):
+    """The call's workspace: the caller's, or one from torch's stream-ordered allocator (so a
+    captured graph owns what it uses).  Returns (tensor, nbytes)."""
+    if need == 0:
+        raise GdrError(GDR_ERR_INVALID_ARG, f"invalid {what} sizes")
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=device), need
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the inputs' device")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _cuda(t, name, dim, form):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != dim:
+        raise ValueError(f"{name} must be {form}")
+    if t.device.type != "cuda":
+        raise ValueError("inputs must be CUDA tensors (there is no CPU path)")
+    return t.device
+
+
+def _out(t, name, shape, dtype, device):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _need(t, name, shape, dtype, device)
+    return t
+
+
+def lin_workspace_bytes(B, T, H, dk, dv, dtype, backward=False):
+    """Bytes of device workspace for lin_prefill (or lin_backward) at these sizes."""
+    return lib.gdr_lin_workspace_bytes(B, T, H, dk, dv, _code(dtype), int(backward))
+
+
+def lin_prefill(q, k, v, decay, s0=None, *, o=None, s_final=None, stream=None, workspace=None):
+    """Linear attention with one decay per head over T tokens:
+    S_t = decay S_{t-1} + v_t k_t^T, o_t = S_t q_t.
+
+    q, k [B, T, H, d_k] and v [B, T, H, d_v], all float32 or all bfloat16; decay [H] float32 in
+    [0, 1]; s0 [B, H, d_v, d_k] float32 or None.  Returns (o, s_final), o in the inputs' type;
+    pass s_final=False to skip the final state, or s_final=s0 to carry in place.  workspace:
+    a zero-filled uint8 tensor of lin_workspace_bytes(...) to read with workspace_status.
+    """
+    dev = _cuda(q, "q", 4, "[B, T, H, d_k]")
+    B, T, H, dk = q.shape
+    dv = v.shape[-1]
+    dt = q.dtype
+    code = _code(dt)
+    _need(k, "k", (B, T, H, dk), dt, dev)
+    _need(q, "q", (B, T, H, dk), dt, dev)
+    _need(v, "v", (B, T, H, dv), dt, dev)
+    _need(decay, "decay", (H,), torch.float32, dev)
+    if s0 is not None:
+        _need(s0, "s0", (B, H, dv, dk), torch.float32, dev)
+    with _on(dev, stream):
+        o = _out(o, "o", (B, T, H, dv), dt, dev)
+        sf = None if s_final is False else _out(s_final, "s_final", (B, H, dv, dk), torch.float32,
+                                                dev)
+        ws, nws = _scratch(workspace, lib.gdr_lin_workspace_bytes(B, T, H, dk, dv, code, 0), dev,
+                           "lin_prefill")
+        _check(lib.lin_prefill(_ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(s0), _ptr(o), _ptr(sf),
+                               B, T, H, dk, dv, code, _ptr(ws), nws, _stream(dev, stream)))
+    return o, sf
+
+
+def lin_decode(q, k, v, decay, state, *, o=None, stream=None):
+    """One token of linear attention for N sequences: q, k [N, H, d_k], v [N, H, d_v], decay
+    [H]; ``state`` [N, H, d_v, d_k] float32 is updated in place.  Returns o [N, H, d_v]."""
+    dev = _cuda(q, "q", 3, "[N, H, d_k]")
+    N, H, dk = q.shape
+    dv = v.shape[-1]
+    dt = q.dtype
+    code = _code(dt)
+    _need(q, "q", (N, H, dk), dt, dev)
+    _need(k, "k", (N, H, dk), dt, dev)
+    _need(v, "v", (N, H, dv), dt, dev)
+    _need(decay, "decay", (H,), torch.float32, dev)
+    _need(state, "state", (N, H, dv, dk), torch.float32, dev)
+    with _on(dev, stream):
+        o = _out(o, "o", (N, H, dv), dt, dev)
+        _check(lib.lin_decode(_ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(state), _ptr(o), N, H,
+                              dk, dv, code, _stream(dev, stream)))
+    return o
+
+
+def lin_backward(q, k, v, decay, s0, do, ds_final=None, *, workspace=None, stream=None):
+    """Gradients (dq, dk, dv in the inputs' type, ds0 float32) of
+    L = sum <do, o> + <ds_final, S_T> for lin_prefill(q, k, v, decay, s0).  The decay is a
+    constant of the head and has none."""
+    dev = _cuda(q, "q", 4, "[B, T, H, d_k]")
+    B, T, H, dk = q.shape
+    dv = v.shape[-1]
+    dt = q.dtype
+    code = _code(dt)
+    _need(q, "q", (B, T, H, dk), dt, dev)
+    _need(k, "k", (B, T, H, dk), dt, dev)
+    _need(v, "v", (B, T, H, dv), dt, dev)
+    _need(decay, "decay", (H,), torch.float32, dev)
+    if s0 is not None:
+        _need(s0, "s0", (B, H, dv, dk), torch.float32, dev)
+    _need(do, "do", (B, T, H, dv), dt, dev)
+    if ds_final is not None:
+        _need(ds_final, "ds_final", (B, H, dv, dk), torch.float32, dev)
+    with _on(dev, stream):
+        dq, dk_, dv_ = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        ds0 = torch.empty((B, H, dv, dk), dtype=torch.float32, device=dev)
+        ws, nws = _scratch(workspace, lib.gdr_lin_workspace_bytes(B, T, H, dk, dv, code, 1), dev,
+                           "lin_backward")
+        _check(lib.lin_backward(_ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(s0), _ptr(do),
+                                _ptr(ds_final), _ptr(dq), _ptr(dk_), _ptr(dv_), _ptr(ds0), B, T, H,
+                                dk, dv, code, _ptr(ws), nws, _stream(dev, stream)))
+    return dq, dk_, dv_, ds0
+
+
+def attn_workspace_bytes(B, Tq, Tk, Hq, Hkv, d, dtype, backward=False):
+    """Bytes of device workspace for attn_prefill (or attn_backward) at these sizes."""
+    return lib.gdr_attn_workspace_bytes(B, Tq, Tk, Hq, Hkv, d, _code(dtype), int(backward))
+
+
+def _lengths(t, name, n, device):
+    if t is not None:
+        _need(t, name, (n,), torch.int32, device)
+    return t
+
+
+def _int32(x, name):
+    """A window or a number of sinks as the C int it becomes (None: 0)."""
+    x = 0 if x is None else int(x)
+    if x > 0x7fffffff:
+        x = 0x7fffffff
+    if x < 0 and name == "sinks":
+        raise ValueError("sinks must not be negative")
+    return max(x, 0)
+
+
+def _attn_shapes(q, k, v):
+    dev = _cuda(q, "q", 4, "[B, Tq, Hq, d]")
+    _cuda(k, "k", 4, "[B, Tk, Hkv, d]")
+    B, Tq, Hq, d = q.shape
+    Tk, Hkv = k.shape[1], k.shape[2]
+    _need(q, "q", (B, Tq, Hq, d), None, dev)
+    _need(k, "k", (B, Tk, Hkv, d), q.dtype, dev)
+    _need(v, "v", (B, Tk, Hkv, d), q.dtype, dev)
+    return dev, B, Tq, Tk, Hq, Hkv, d
+
+
+def attn_prefill(q, k, v, *, window=0, sinks=0, scale=None, lengths=None, o=None, lse=None,
+                 stream=None, workspace=None):
+    """Causal softmax attention with an optional sliding window and sinks.
+
+    q [B, Tq, Hq, d]; k, v [B, Tk, Hkv, d] (Hq a multiple of Hkv: query head h reads key head
+    h // (Hq / Hkv)); all float32 or all bfloat16.  Query i sits at position p = Tk - Tq + i
+    and sees key j when j <= p, j and p < lengths[b] (int32 [B]; None: Tk), and
+    p - j < window (0 or None: no window) or j < sinks.  scale: None for d ** -0.5.
+    Returns (o in q's type, lse [B, Hq, Tq] float32); a query that sees nothing has o = 0 and
+    lse = -inf.  Pass lse=False to skip it.
+    """
+    dev, B, Tq, Tk, Hq, Hkv, d = _attn_shapes(q, k, v)
+    code = _code(q.dtype)
+    _lengths(lengths, "lengths", B, dev)
+    with _on(dev, stream):
+        o = _out(o, "o", (B, Tq, Hq, d), q.dtype, dev)
+        lse = None if lse is False else _out(lse, "lse", (B, Hq, Tq), torch.float32, dev)
+        ws, nws = _scratch(workspace, lib.gdr_attn_workspace_bytes(B, Tq, Tk, Hq, Hkv, d, code, 0),
+                           dev, "attn_prefill")
+        _check(lib.attn_prefill(_ptr(q), _ptr(k), _ptr(v), _ptr(lengths), _ptr(o), _ptr(lse), B,
+                                Tq, Tk, Hq, Hkv, d, _int32(window, "window"),
+                                _int32(sinks, "sinks"), d ** -0.5 if scale is None else scale,
+                                code, _ptr(ws), nws, _stream(dev, stream)))
+    return o, lse
+
+
+def attn_backward(q, k, v, o, lse, do, *, window=0, sinks=0, scale=None, lengths=None,
+                  stream=None, workspace=None):
+    """Gradients (dq, dk, dv, in the inputs' type) of L = sum <do, o> for
+    attn_prefill(q, k, v, ...), from its o and lse."""
+    dev, B, Tq, Tk, Hq, Hkv, d = _attn_shapes(q, k, v)
+    code = _code(q.dtype)
+    _need(o, "o", (B, Tq, Hq, d), q.dtype, dev)
+    _need(lse, "lse", (B, Hq, Tq), torch.float32, dev)
+    _need(do, "do", (B, Tq, Hq, d), q.dtype, dev)
+    _lengths(lengths, "lengths", B, dev)
+    with _on(dev, stream):
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        ws, nws = _scratch(workspace, lib.gdr_attn_workspace_bytes(B, Tq, Tk, Hq, Hkv, d, code, 1),
+                           dev, "attn_backward")
+        _check(lib.attn_backward(_ptr(q), _ptr(k), _ptr(v), _ptr(lengths), _ptr(o), _ptr(lse),
+                                 _ptr(do), _ptr(dq), _ptr(dk), _ptr(dv), B, Tq, Tk, Hq, Hkv, d,
+                                 _int32(window, "window"), _int32(sinks, "sinks"),
+                                 d ** -0.5 if scale is None else scale, code, _ptr(ws), nws,
+                                 _stream(dev, stream)))
+    return dq, dk, dv
+
+
+def _paged(k_cache, v_cache, page_table, N, dt, dev):
+    _cuda(k_cache, "k_cache", 4, "[npages, page, Hkv, d]")
+    npages, page, Hkv, d = k_cache.shape
+    _need(k_cache, "k_cache", (npages, page, Hkv, d), dt, dev)
+    _need(v_cache, "v_cache", (npages, page, Hkv, d), dt, dev)
+    _cuda(page_table, "page_table", 2, "[N, max_pages]")
+    _need(page_table, "page_table", (N, page_table.shape[1]), torch.int32, dev)
+    return npages, page, Hkv, d, page_table.shape[1]
+
+
+def attn_decode_workspace_bytes(N, Hq, Hkv, d, page, max_pages, dtype, window=0, sinks=0):
+    """Bytes of device workspace for attn_decode at these sizes."""
+    return lib.gdr_attn_decode_workspace_bytes(N, Hq, Hkv, d, page, max_pages,
+                                               _int32(window, "window"), _int32(sinks, "sinks"),
+                                               _code(dtype))
+
+
+def attn_decode(q, k_cache, v_cache, page_table, lengths, *, k=None, v=None, window=0, sinks=0,
+                scale=None, o=None, stream=None, workspace=None):
+    """Attention of one new token for each of N sequences over a paged key-value cache.
+
+    q [N, Hq, d]; k_cache, v_cache [npages, page, Hkv, d] (page a power of two); page_table
+    [N, max_pages] int32: token t of sequence n lies in row t % page of page
+    page_table[n, t // page]; lengths [N] int32, the new token counted.  With k, v [N, Hkv, d]
+    the new token's key and value are stored at position lengths[n] - 1 by the same launch.
+    window, sinks, scale as in attn_prefill.  Returns o [N, Hq, d]; 0 for an empty sequence.
+    Lengths and table entries outside the cache are left out and recorded in the workspace's
+    status word (pass a zero-filled workspace and read it with workspace_status).
+    """
+    dev = _cuda(q, "q", 3, "[N, Hq, d]")
+    N, Hq, d = q.shape
+    dt = q.dtype
+    code = _code(dt)
+    _need(q, "q", (N, Hq, d), dt, dev)
+    npages, page, Hkv, dc, max_pages = _paged(k_cache, v_cache, page_table, N, dt, dev)
+    if dc != d:
+        raise ValueError(f"the caches' head size {dc} is not q's {d}")
+    _need(lengths, "lengths", (N,), torch.int32, dev)
+    if (k is None) != (v is None):
+        raise ValueError("k and v are given together or not at all")
+    if k is not None:
+        _need(k, "k", (N, Hkv, d), dt, dev)
+        _need(v, "v", (N, Hkv, d), dt, dev)
+    w, s = _int32(window, "window"), _int32(sinks, "sinks")
+    with _on(dev, stream):
+        o = _out(o, "o", (N, Hq, d), dt, dev)
+        ws, nws = _scratch(workspace, lib.gdr_attn_decode_workspace_bytes(
+            N, Hq, Hkv, d, page, max_pages, w, s, code), dev, "attn_decode")
+        _check(lib.attn_decode(_ptr(q), _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache),
+                               _ptr(page_table), _ptr(lengths), _ptr(o), N, Hq, Hkv, d, npages,
+                               page, max_pages, w, s, d ** -0.5 if scale is None else scale, code,
+                               _ptr(ws), nws, _stream(dev, stream)))
+    return o
+
+
+def kv_append(k, v, k_cache, v_cache, page_table, start, counts=None, *, stream=None,
+              workspace=None):
+    """Store K tokens of each of N sequences in a paged cache, in place: k, v [N, K, Hkv, d];
+    token t < counts[n] (int32 [N]; None: K) goes to position start[n] + t (int32 [N]).
+    Positions and pages outside the cache are skipped (and recorded in ``workspace``)."""
+    dev = _cuda(k, "k", 4, "[N, K, Hkv, d]")
+    N, K, Hkv, d = k.shape
+    dt = k.dtype
+    code = _code(dt)
+    _need(k, "k", (N, K, Hkv, d), dt, dev)
+    _need(v, "v", (N, K, Hkv, d), dt, dev)
+    npages, page, hc, dc, max_pages = _paged(k_cache, v_cache, page_table, N, dt, dev)
+    if (hc, dc) != (Hkv, d):
+        raise ValueError(f"the caches hold heads {hc} x {dc}, k and v {Hkv} x {d}")
+    _lengths(start, "start", N, dev)
+    _lengths(counts, "counts", N, dev)
+    if start is None:
+        raise TypeError("start must be a torch.Tensor")
+    ws, nws = (None, 0) if workspace is None else _scratch(workspace, 256, dev, "kv_append")
+    with _on(dev, stream):
+        _check(lib.kv_append(_ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(page_table),
+                             _ptr(start), _ptr(counts), N, K, Hkv, d, npages, page, max_pages,
+                             code, _ptr(ws), nws, _stream(dev, stream)))
 
 
 def prefill_path(dk, dv, dtype, kda):

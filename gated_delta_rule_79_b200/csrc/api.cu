@@ -407,6 +407,10 @@ gdr_status gdr_workspace_status(void* workspace, size_t ws_bytes, void* stream) 
     return gdr::fail(GDR_ERR_CUDA, "gdr_workspace_status: %s", cudaGetErrorString(e));
   if (word & 3u)
     return gdr::fail(GDR_ERR_TIMEOUT, "a bounded device wait gave up (status word 0x%08x)", word);
+  if (word & 8u)
+    return gdr::fail(GDR_ERR_INVALID_ARG,
+                     "a length, position or page-table entry lies outside the paged cache (status "
+                     "word 0x%08x); its tokens were left out", word);
   if (word != 0)
     return gdr::fail(GDR_ERR_INVALID_ARG,
                      "packed-sequence offsets were not a partition of the tokens (status word "

@@ -1,0 +1,75 @@
+// Softmax attention with a sliding window and sinks: what its kernels share.
+//
+// "Super Apriel: One Checkpoint, Many Speeds", §2A (Mixer Vocabulary) names full and
+// sliding-window attention beside the recurrent mixers.  Query i of Tq sits at position
+// p = Tk - Tq + i and sees key j when j <= p, j and p lie before the sequence's length, and
+// p - j < window (0: no window) or j < sinks:
+//
+//     s_ij = scale q_i.k_j,   lse_i = log sum_j e^(s_ij),   o_i = sum_j e^(s_ij - lse_i) v_j
+//
+// A query that sees nothing has o = 0 and lse = -inf.  Gradients, with D_i = do_i . o_i:
+//
+//     p_ij = e^(s_ij - lse_i),   ds_ij = scale p_ij (do_i . v_j - D_i)
+//     dv_j = sum_i p_ij do_i,    dq_i = sum_j ds_ij k_j,    dk_j = sum_i ds_ij q_i
+#pragma once
+
+#include "common.cuh"
+#include "launch.h"
+
+namespace gdr {
+namespace attn {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// The mask of one sequence.  window > 0, or 0 for none; sinks is 0 without a window.
+struct Mask {
+  int off;      // position of query 0
+  int len;      // keys and queries at and past this position do not count
+  int window, sinks;
+
+  __device__ __forceinline__ bool sees(int p, int j) const {
+    return j <= p && j < len && p < len && (window == 0 || p - j < window || j < sinks);
+  }
+};
+
+__device__ __forceinline__ Mask make_mask(const int* lengths, int b, int Tq, int Tk, int window,
+                                          int sinks) {
+  Mask m;
+  m.off = Tk - Tq;
+  m.len = lengths ? min(max(lengths[b], 0), Tk) : Tk;
+  m.window = window;
+  m.sinks = sinks;
+  return m;
+}
+
+// Key tiles of BN keys that the queries i0 .. i1 see: tiles 0 .. nsink-1 hold sinks that lie
+// before the window's first tile lo; then lo .. lo + nwin - 1.
+struct KeyTiles {
+  int nsink, lo, nwin;
+  __device__ __forceinline__ int count() const { return nsink + nwin; }
+  __device__ __forceinline__ int tile(int x) const { return x < nsink ? x : lo + x - nsink; }
+};
+template <int BN>
+__device__ __forceinline__ KeyTiles key_tiles(const Mask& m, int i0, int i1) {
+  KeyTiles t{0, 0, 0};
+  const int p0 = max(m.off + i0, 0), p1 = min(m.off + i1, m.len - 1);
+  if (p1 < p0) return t;
+  const int first = m.window ? max(0, p0 - m.window + 1) : 0;
+  t.lo = first / BN;
+  t.nwin = p1 / BN - t.lo + 1;
+  t.nsink = min((m.sinks + BN - 1) / BN, t.lo);
+  return t;
+}
+
+// Queries that see any of the keys j0 .. j1: i in [lo, hi) (empty when hi <= lo).
+__device__ __forceinline__ void query_range(const Mask& m, int j0, int j1, int Tq, int& lo,
+                                            int& hi) {
+  lo = max(0, j0 - m.off);
+  long last = (long)m.len - 1;
+  if (m.window && j0 >= m.sinks) last = min(last, (long)j1 + m.window - 1);
+  hi = j0 < m.len ? (int)min((long)Tq, last - m.off + 1) : 0;
+}
+
+}  // namespace attn
+}  // namespace gdr

@@ -1,0 +1,632 @@
+// Attention of one new token per sequence over a paged key-value cache, and the store of
+// new keys and values into the pages (sm_100a).  Mathematics and mask: attn_common.cuh, with
+// the query at position lengths[n] - 1.
+//
+// Bound by HBM: every visible token's key and value are read once for all the query heads
+// of their group, 2 d e bytes a token and key head (e bytes an element) against 4 d flops a
+// query head.  A sequence's visible tokens (the sinks, then the window) are cut into up to
+// `nsplit` equal parts, each a CTA of four warps; a warp streams its own tiles of 16 tokens
+// through a private ring of shared-memory stages with 16-byte asynchronous copies, so no
+// barrier stands between the loads and the products, and keeps its own running maximum, sum
+// and output.  The warps of a CTA join in shared memory, the parts of a sequence in a second
+// small kernel that starts while the first one drains.
+//
+// bf16 with d = 64 or 128: the products run as m16n8k16 warp matrix instructions, 16 query
+// heads as the 16 rows (fewer heads leave rows unused, which costs nothing at this ratio of
+// bytes to flops: at 6 TB/s a token of 512 bytes passes an SM every 22 cycles, and its
+// products over 16 rows take a few).  Other types run as fp32 dot products, lane = token for
+// the scores and lane = channels for the output.
+//
+// The join reads parts in order, so results do not depend on scheduling.
+
+#include "attn_common.cuh"
+
+namespace gdr {
+namespace {
+
+using namespace attn;
+
+constexpr int kWarps = 4;
+constexpr int kTile = 16;           // tokens of a warp's tile
+
+// Records a length or page outside the cache (gdr_workspace_status: GDR_ERR_INVALID_ARG).
+__device__ __forceinline__ void report(unsigned int* status) {
+  if (status) atomicOr(status, 8u);
+}
+
+// A sequence's visible tokens, numbered 0 .. count-1: the sinks, then the window.
+struct Visible {
+  int len, ns, gap, count;
+  __device__ __forceinline__ int token(int x) const { return x < ns ? x : x + gap; }
+};
+__device__ __forceinline__ Visible visible(const PagedArgs& a, int n, bool note) {
+  Visible v;
+  const int cap = (int)min((long)a.max_pages << a.page_shift, (long)0x7fffffff);
+  int len = a.lengths[n];
+  if (len < 0 || len > cap) {
+    if (note) report(a.status);
+    len = len < 0 ? 0 : cap;
+  }
+  v.len = len;
+  v.ns = v.gap = 0;
+  v.count = len;
+  if (a.window && len > a.window) {
+    v.ns = min(a.sinks, len - a.window);
+    v.gap = len - a.window - v.ns;
+    v.count = v.ns + a.window;
+  }
+  return v;
+}
+// tokens of each part: whole tiles for all four warps, so that short sequences use few parts
+__device__ __forceinline__ int part_tokens(int count, int nsplit) {
+  const int per = (count + nsplit - 1) / nsplit;
+  return max(kWarps * kTile, (per + kTile - 1) / kTile * kTile);
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take) {
+  // takes 16 bytes, or writes zeros when the row is not to be read
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+               :: "r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory");
+}
+__device__ __forceinline__ void dependents_may_launch() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_prior_grid() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+__device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                          uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, "
+               "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&p);
+}
+
+// Where this warp's tile row (a visible token) lies: the row index of the caches, or -1 when
+// there is no such token or its page is not one of the pool's; -2 for the new token itself.
+struct Rows {
+  const PagedArgs& a;
+  const Visible& v;
+  int n;
+  __device__ __forceinline__ long find(int x, int end) const {
+    if (x >= end) return -1;
+    const int t = v.token(x);
+    if (a.k_new && t == v.len - 1) return -2;
+    const int pg = a.table[(size_t)n * a.max_pages + (t >> a.page_shift)];
+    if ((unsigned)pg >= (unsigned)a.npages) {
+      report(a.status);
+      return -1;
+    }
+    return ((long)pg << a.page_shift) + (t & ((1 << a.page_shift) - 1));
+  }
+};
+
+// The part that holds the last token stores the new key and value into their page (each key
+// head's by the CTA of the group's first 16 heads).  No other CTA touches that row: the
+// tokens of a sequence lie in different rows, and sequences do not share their last page.
+template <typename T, int D>
+__device__ __forceinline__ void store_new(const PagedArgs& a, const Visible& v, int n, int hk) {
+  const int t = v.len - 1;
+  const int pg = a.table[(size_t)n * a.max_pages + (t >> a.page_shift)];
+  if ((unsigned)pg >= (unsigned)a.npages) {
+    if (threadIdx.x == 0) report(a.status);
+    return;
+  }
+  const size_t row = ((size_t)pg << a.page_shift) + (t & ((1 << a.page_shift) - 1));
+  constexpr int V = 16 / sizeof(T);
+  for (int c = threadIdx.x * V; c < 2 * D; c += kWarps * 32 * V) {
+    const bool key = c < D;
+    const T* src = (const T*)(key ? a.k_new : a.v_new) + ((size_t)n * a.Hkv + hk) * D + c % D;
+    T* dst = (T*)(key ? a.kc : a.vc) + (row * a.Hkv + hk) * D + c % D;
+    *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(src);
+  }
+}
+
+// Writes one part's result: the output itself when there is only one part, else (o, m, l) of
+// the part for the join, with o not yet divided by the sum.
+template <typename T>
+__device__ __forceinline__ void emit(const PagedArgs& a, int n, int h, int part, int parts, int D,
+                                     int c, float o, float m, float l) {
+  if (parts == 1) {
+    Elem<T>::store((T*)a.o + ((size_t)n * a.Hq + h) * D + c, l != 0.f ? o / l : 0.f);
+    return;
+  }
+  float* p = a.part + ((size_t)n * a.Hq + h) * a.nsplit * (D + 2);
+  p[(size_t)part * D + c] = o;
+  if (c == 0) {
+    p[(size_t)a.nsplit * D + 2 * part] = m;
+    p[(size_t)a.nsplit * D + 2 * part + 1] = l;
+  }
+}
+
+template <int D>
+struct TcSmem {
+  static constexpr int STAGES = 3;
+  static constexpr int ROW = D * 2;                       // bytes of a token's key or value
+  static constexpr int HALF = kTile * ROW;                // a tile's keys
+  static constexpr int WARP = STAGES * 2 * HALF;
+  static constexpr int RING = kWarps * WARP;
+  static constexpr int BYTES = RING;                      // the join of the warps reuses it
+  static_assert(kWarps * 16 * (D + 4) * 4 + kWarps * 16 * 8 <= RING, "join area");
+};
+
+template <int D>
+__global__ void __launch_bounds__(kWarps * 32)
+attn_decode_tc(const PagedArgs a) {
+  using S = TcSmem<D>;
+  using bf16 = __nv_bfloat16;
+  extern __shared__ __align__(128) unsigned char sm[];
+  dependents_may_launch();
+  const int G = a.Hq / a.Hkv, nhb = (G + 15) / 16;
+  int x = blockIdx.x;
+  const int part = x % a.nsplit;
+  x /= a.nsplit;
+  const int hb = x % nhb;
+  x /= nhb;
+  const int hk = x % a.Hkv, n = x / a.Hkv;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const Visible vis = visible(a, n, tid == 0 && part == 0);
+  const int per = part_tokens(vis.count, a.nsplit);
+  const int parts = max(1, (vis.count + per - 1) / per);
+  if (part >= parts) return;
+  const int h0 = hk * G + hb * 16, nh = min(16, G - hb * 16);
+  const int x0 = part * per, x1 = min(vis.count, x0 + per);
+  if (a.k_new && hb == 0 && part == parts - 1 && vis.len > 0) store_new<bf16, D>(a, vis, n, hk);
+
+  // query fragments, with the scale and log2 e applied to the scores later
+  const int g = lane >> 2, t4 = lane & 3;
+  uint32_t qf[D / 16][4];
+#pragma unroll
+  for (int s = 0; s < D / 16; ++s)
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int row = g + (u & 1) * 8, col = s * 16 + t4 * 2 + (u >> 1) * 8;
+      qf[s][u] = row < nh ? *reinterpret_cast<const uint32_t*>(
+                                (const bf16*)a.q + ((size_t)n * a.Hq + h0 + row) * D + col)
+                          : 0u;
+    }
+
+  // this warp's tiles: warp, warp + 4, ...
+  const int ntile = (x1 - x0 + kTile - 1) / kTile;
+  const int mine = ntile > warp ? (ntile - warp + kWarps - 1) / kWarps : 0;
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(sm) + warp * S::WARP;
+  constexpr int CH = D / 8;                 // 16-byte pieces of a row
+  constexpr int RPI = 32 / CH;              // rows a warp instruction copies
+  const Rows rows{a, vis, n};
+  // lane l < 16 looks up row l of a tile; one tile ahead of the copies
+  auto look = [&](int i) -> long {
+    return i < mine && lane < kTile ? rows.find(x0 + (warp + i * kWarps) * kTile + lane, x1) : -1;
+  };
+  auto issue = [&](int i, long mrow) {
+    const uint32_t st = ring + (i % S::STAGES) * 2 * S::HALF;
+#pragma unroll
+    for (int r0 = 0; r0 < kTile; r0 += RPI) {
+      const int r = r0 + lane / CH, c = lane % CH;
+      const long row = __shfl_sync(0xffffffffu, mrow, r);
+      const size_t at = row >= 0 ? ((size_t)row * a.Hkv + hk) * D + c * 8
+                                 : ((size_t)n * a.Hkv + hk) * D + c * 8;
+      const bool take = row != -1;
+      const bf16* kp = (const bf16*)(row == -2 ? a.k_new : a.kc) + (take ? at : 0);
+      const bf16* vp = (const bf16*)(row == -2 ? a.v_new : a.vc) + (take ? at : 0);
+      const uint32_t dst = st + r * S::ROW + ((c ^ (r & 7)) << 4);
+      cp_async16(dst, kp, take);
+      cp_async16(dst + S::HALF, vp, take);
+    }
+  };
+  // rows without a token score -inf; the stage's rows are kept as a bit mask of their lanes
+  uint32_t live[S::STAGES];
+  long ahead = look(0);
+#pragma unroll
+  for (int i = 0; i < S::STAGES - 1; ++i) {
+    live[i] = __ballot_sync(0xffffffffu, ahead != -1);
+    if (i < mine) issue(i, ahead);
+    cp_commit();
+    ahead = look(i + 1);
+  }
+  float o[D / 8][4];
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+    for (int u = 0; u < 4; ++u) o[i][u] = 0.f;
+  float mx[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+  const float c = a.scale * kLog2e;
+
+  // unrolled by the number of stages so that `live` stays in registers
+  for (int i0 = 0; i0 < mine; i0 += S::STAGES) {
+#pragma unroll
+    for (int s = 0; s < S::STAGES; ++s) {
+      const int i = i0 + s;
+      if (i < mine) {
+        const int fill = i + S::STAGES - 1;
+        live[(s + S::STAGES - 1) % S::STAGES] = __ballot_sync(0xffffffffu, ahead != -1);
+        if (fill < mine) issue(fill, ahead);
+        cp_commit();
+        ahead = look(fill + 1);
+        cp_wait<S::STAGES - 1>();
+        __syncwarp();
+        const uint32_t st = ring + s * 2 * S::HALF;
+        float sc[2][4] = {};
+        // scores: B fragments of both 8-token halves from one ldmatrix per 16 channels
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const int r = (lane & 7) + ((lane >> 4) << 3), ch = ks * 2 + ((lane >> 3) & 1);
+          uint32_t b[4];
+          ldsm4(st + r * S::ROW + ((ch ^ (r & 7)) << 4), b);
+          mma_16816(sc[0], qf[ks], b[0], b[1]);
+          mma_16816(sc[1], qf[ks], b[2], b[3]);
+        }
+        float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const bool on = (live[s] >> (hf * 8 + t4 * 2 + (u & 1))) & 1u;
+            sc[hf][u] = on ? sc[hf][u] * c : -INFINITY;
+            top[u >> 1] = fmaxf(top[u >> 1], sc[hf][u]);
+          }
+        float f[2];
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          top[w] = fmaxf(top[w], __shfl_xor_sync(0xffffffffu, top[w], 1));
+          top[w] = fmaxf(top[w], __shfl_xor_sync(0xffffffffu, top[w], 2));
+          const float now = fmaxf(mx[w], top[w]);
+          const float base = now == -INFINITY ? 0.f : now;
+          f[w] = exp2f(mx[w] - base);
+          mx[w] = now;
+          sum[w] *= f[w];
+          top[w] = base;
+        }
+        uint32_t pa[4];
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            const float p0 = exp2f(sc[hf][2 * w] - top[w]), p1 = exp2f(sc[hf][2 * w + 1] - top[w]);
+            sum[w] += p0 + p1;
+            pa[hf * 2 + w] = pack_bf16(p0, p1);   // bf16, as the values they weigh
+          }
+        if (__any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f)) {
+#pragma unroll
+          for (int e = 0; e < D / 8; ++e) {
+            o[e][0] *= f[0];
+            o[e][1] *= f[0];
+            o[e][2] *= f[1];
+            o[e][3] *= f[1];
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < D / 16; ++e) {
+          const int r = lane & 15, ch = e * 2 + (lane >> 4);
+          uint32_t b[4];
+          ldsm4_t(st + S::HALF + r * S::ROW + ((ch ^ (r & 7)) << 4), b);
+          mma_16816(o[2 * e], pa, b[0], b[1]);
+          mma_16816(o[2 * e + 1], pa, b[2], b[3]);
+        }
+        __syncwarp();     // the stage is refilled in the next step
+      }
+    }
+  }
+  cp_wait<0>();
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    sum[w] += __shfl_xor_sync(0xffffffffu, sum[w], 1);
+    sum[w] += __shfl_xor_sync(0xffffffffu, sum[w], 2);
+  }
+  __syncthreads();
+  float* jo = reinterpret_cast<float*>(sm);                 // [warp][16][D + 4]
+  float* jm = jo + kWarps * 16 * (D + 4);                   // [warp][16] m, then l
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const int row = g + 8 * w;
+#pragma unroll
+    for (int e = 0; e < D / 8; ++e) {
+      float2 p = make_float2(o[e][2 * w], o[e][2 * w + 1]);
+      *reinterpret_cast<float2*>(jo + (warp * 16 + row) * (D + 4) + e * 8 + t4 * 2) = p;
+    }
+    if (t4 == 0) {
+      jm[warp * 16 + row] = mx[w];
+      jm[kWarps * 16 + warp * 16 + row] = sum[w];
+    }
+  }
+  __syncthreads();
+  for (int e = tid; e < nh * D; e += kWarps * 32) {
+    const int row = e / D, ch = e % D;
+    float m = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, jm[w * 16 + row]);
+    const float base = m == -INFINITY ? 0.f : m;
+    float l = 0.f, v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float f = exp2f(jm[w * 16 + row] - base);
+      l = fmaf(f, jm[kWarps * 16 + w * 16 + row], l);
+      v = fmaf(f, jo[(w * 16 + row) * (D + 4) + ch], v);
+    }
+    emit<bf16>(a, n, h0 + row, part, parts, D, ch, v, m, l);
+  }
+}
+
+// fp32 arithmetic: a warp's tile is 32 tokens; 8 query heads at a time.
+constexpr int kSTile = 32, kSHeads = 8;
+
+template <typename T, int D>
+struct SimtSmem {
+  float kv[kWarps][kSTile][D + 4];     // keys, then values; then the warps' outputs
+  float q[kSHeads][D];
+  float p[kWarps][kSHeads][kSTile];
+  float m[kWarps][kSHeads], l[kWarps][kSHeads];
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kWarps * 32)
+attn_decode_simt(const PagedArgs a) {
+  extern __shared__ __align__(128) unsigned char raw[];
+  SimtSmem<T, D>& sm = *reinterpret_cast<SimtSmem<T, D>*>(raw);
+  dependents_may_launch();
+  const int G = a.Hq / a.Hkv, nhb = (G + kSHeads - 1) / kSHeads;
+  int x = blockIdx.x;
+  const int part = x % a.nsplit;
+  x /= a.nsplit;
+  const int hb = x % nhb;
+  x /= nhb;
+  const int hk = x % a.Hkv, n = x / a.Hkv;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const Visible vis = visible(a, n, tid == 0 && part == 0);
+  const int per = part_tokens(vis.count, a.nsplit);
+  const int parts = max(1, (vis.count + per - 1) / per);
+  if (part >= parts) return;
+  const int h0 = hk * G + hb * kSHeads, nh = min(kSHeads, G - hb * kSHeads);
+  const int x0 = part * per, x1 = min(vis.count, x0 + per);
+  if (a.k_new && hb == 0 && part == parts - 1 && vis.len > 0) store_new<T, D>(a, vis, n, hk);
+  for (int e = tid; e < kSHeads * D; e += kWarps * 32)
+    sm.q[e / D][e % D] =
+        e / D < nh ? Elem<T>::load((const T*)a.q + ((size_t)n * a.Hq + h0 + e / D) * D + e % D)
+                   : 0.f;
+  __syncthreads();
+  constexpr int CPL = D / 32;            // channels of a lane in the output: lane + 32 e
+  float o[kSHeads][CPL] = {}, mx[kSHeads], sum[kSHeads];
+#pragma unroll
+  for (int h = 0; h < kSHeads; ++h) mx[h] = -INFINITY, sum[h] = 0.f;
+  const float c = a.scale * kLog2e;
+  const Rows rows{a, vis, n};
+  float (*kv)[D + 4] = sm.kv[warp];
+  for (int b = x0 + warp * kSTile; b < x1; b += kWarps * kSTile) {
+    const long mrow = rows.find(b + lane, x1);
+    auto load = [&](const void* cache, const void* fresh) {
+      constexpr int CH = D / 4;
+      for (int e = lane; e < kSTile * CH; e += 32) {
+        const int r = e / CH, cc = (e % CH) * 4;
+        const long row = __shfl_sync(0xffffffffu, mrow, r);
+        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (row >= 0) f = Elem<T>::load4((const T*)cache + ((size_t)row * a.Hkv + hk) * D + cc);
+        if (row == -2) f = Elem<T>::load4((const T*)fresh + ((size_t)n * a.Hkv + hk) * D + cc);
+        *reinterpret_cast<float4*>(&kv[r][cc]) = f;
+      }
+    };
+    load(a.kc, a.k_new);
+    __syncwarp();
+    float s[kSHeads] = {};
+#pragma unroll 4
+    for (int cc = 0; cc < D; cc += 4) {
+      const float4 f = *reinterpret_cast<const float4*>(&kv[lane][cc]);
+#pragma unroll
+      for (int h = 0; h < kSHeads; ++h) {
+        const float4 w = *reinterpret_cast<const float4*>(&sm.q[h][cc]);
+        s[h] = fmaf(f.x, w.x, fmaf(f.y, w.y, fmaf(f.z, w.z, fmaf(f.w, w.w, s[h]))));
+      }
+    }
+    __syncwarp();
+    load(a.vc, a.v_new);
+#pragma unroll
+    for (int h = 0; h < kSHeads; ++h) {
+      s[h] = mrow != -1 ? s[h] * c : -INFINITY;
+      float top = s[h];
+#pragma unroll
+      for (int f = 16; f; f >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, f));
+      const float now = fmaxf(mx[h], top), base = now == -INFINITY ? 0.f : now;
+      const float f = exp2f(mx[h] - base), p = exp2f(s[h] - base);
+      mx[h] = now;
+      sum[h] = fmaf(sum[h], f, p);       // this lane's tokens only, until the end
+      sm.p[warp][h][lane] = p;
+#pragma unroll
+      for (int e = 0; e < CPL; ++e) o[h][e] *= f;
+    }
+    __syncwarp();
+#pragma unroll 4
+    for (int r = 0; r < kSTile; ++r) {
+      float v[CPL];
+#pragma unroll
+      for (int e = 0; e < CPL; ++e) v[e] = kv[r][lane + 32 * e];
+#pragma unroll
+      for (int h = 0; h < kSHeads; ++h) {
+        const float p = sm.p[warp][h][r];
+#pragma unroll
+        for (int e = 0; e < CPL; ++e) o[h][e] = fmaf(p, v[e], o[h][e]);
+      }
+    }
+    __syncwarp();
+  }
+#pragma unroll
+  for (int h = 0; h < kSHeads; ++h) {
+#pragma unroll
+    for (int f = 16; f; f >>= 1) sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], f);
+#pragma unroll
+    for (int e = 0; e < CPL; ++e) kv[h][lane + 32 * e] = o[h][e];
+    if (lane == 0) {
+      sm.m[warp][h] = mx[h];
+      sm.l[warp][h] = sum[h];
+    }
+  }
+  __syncthreads();
+  for (int e = tid; e < nh * D; e += kWarps * 32) {
+    const int h = e / D, ch = e % D;
+    float m = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sm.m[w][h]);
+    const float base = m == -INFINITY ? 0.f : m;
+    float l = 0.f, v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float f = exp2f(sm.m[w][h] - base);
+      l = fmaf(f, sm.l[w][h], l);
+      v = fmaf(f, sm.kv[w][h][ch], v);
+    }
+    emit<T>(a, n, h0 + h, part, parts, D, ch, v, m, l);
+  }
+}
+
+// Joins the parts of each (sequence, query head): a warp each.
+template <typename T, int D>
+__global__ void __launch_bounds__(128)
+attn_decode_join(const PagedArgs a) {
+  const size_t nh = (size_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  wait_for_prior_grid();
+  if (nh >= (size_t)a.N * a.Hq) return;
+  const Visible vis = visible(a, (int)(nh / a.Hq), false);
+  const int per = part_tokens(vis.count, a.nsplit);
+  const int parts = (vis.count + per - 1) / per;
+  if (parts <= 1) return;
+  const float* p = a.part + nh * a.nsplit * (D + 2);
+  const float* ml = p + (size_t)a.nsplit * D;
+  float m = -INFINITY;
+  for (int s = lane; s < parts; s += 32) m = fmaxf(m, ml[2 * s]);
+#pragma unroll
+  for (int f = 16; f; f >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, f));
+  const float base = m == -INFINITY ? 0.f : m;
+  constexpr int CPL = D / 32;
+  float l = 0.f, o[CPL] = {};
+#pragma unroll 4
+  for (int s = 0; s < parts; ++s) {
+    const float2 x = *reinterpret_cast<const float2*>(ml + 2 * s);
+    const float f = exp2f(x.x - base);
+    l = fmaf(f, x.y, l);
+#pragma unroll
+    for (int e = 0; e < CPL; ++e) o[e] = fmaf(f, p[(size_t)s * D + lane + 32 * e], o[e]);
+  }
+  const float inv = l != 0.f ? 1.f / l : 0.f;
+#pragma unroll
+  for (int e = 0; e < CPL; ++e)
+    Elem<T>::store((T*)a.o + nh * D + lane + 32 * e, o[e] * inv);
+}
+
+// Token t of sequence n (t < counts[n]) goes to position start[n] + t of its pages: a thread
+// for each 16 bytes of keys and values.
+__global__ void __launch_bounds__(256)
+kv_append_kernel(const AppendArgs a) {
+  const size_t total = (size_t)a.N * a.K * a.Hkv * a.pieces;
+  const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= total) return;
+  const size_t row = (size_t)a.Hkv * a.pieces;         // 16-byte pieces of a token
+  const int n = (int)(i / (row * a.K));
+  const int t = (int)(i / row % a.K);
+  const int count = a.counts ? min(a.counts[n], a.K) : a.K;
+  if (t >= count) return;
+  const long pos = (long)a.start[n] + t;
+  if (pos < 0 || pos >= ((long)a.max_pages << a.page_shift)) {
+    report(a.status);
+    return;
+  }
+  const int pg = a.table[(size_t)n * a.max_pages + (pos >> a.page_shift)];
+  if ((unsigned)pg >= (unsigned)a.npages) {
+    report(a.status);
+    return;
+  }
+  const size_t slot = ((size_t)pg << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
+  const size_t dst = slot * row + i % row;
+  reinterpret_cast<uint4*>(a.kc)[dst] = reinterpret_cast<const uint4*>(a.k)[i];
+  reinterpret_cast<uint4*>(a.vc)[dst] = reinterpret_cast<const uint4*>(a.v)[i];
+}
+
+template <typename K>
+cudaError_t launch_main(K kern, int smem, const PagedArgs& a, unsigned grid, cudaStream_t st) {
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kern<<<grid, kWarps * 32, smem, st>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t launch_t(const PagedArgs& a, cudaStream_t st) {
+  const int G = a.Hq / a.Hkv;
+  cudaError_t e;
+  if constexpr (sizeof(T) == 2 && D >= 64) {
+    const unsigned grid = (unsigned)((size_t)a.N * a.Hkv * ((G + 15) / 16) * a.nsplit);
+    e = launch_main(attn_decode_tc<D>, TcSmem<D>::BYTES, a, grid, st);
+  } else {
+    const unsigned grid =
+        (unsigned)((size_t)a.N * a.Hkv * ((G + kSHeads - 1) / kSHeads) * a.nsplit);
+    e = launch_main(attn_decode_simt<T, D>, (int)sizeof(SimtSmem<T, D>), a, grid, st);
+  }
+  if (e != cudaSuccess || a.nsplit == 1) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(((size_t)a.N * a.Hq + 3) / 4), 1, 1);
+  cfg.blockDim = dim3(128, 1, 1);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attn_decode_join<T, D>, a);
+}
+
+template <typename T>
+cudaError_t launch_d(const PagedArgs& a, cudaStream_t st) {
+  switch (a.d) {
+    case 32: return launch_t<T, 32>(a, st);
+    case 64: return launch_t<T, 64>(a, st);
+    case 128: return launch_t<T, 128>(a, st);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+// How many parts a sequence's tokens may be cut into.  The grid is the same for every
+// length (the lengths are on the device), and parts past a short sequence's end leave at
+// once, so it is chosen from what the page table can hold: enough CTAs for eight on each
+// SM, which also evens out sequences of different lengths, and no part below 64 tokens.
+int attn_decode_splits(int N, int Hq, int Hkv, int d, int dtype, long capacity, int window,
+                       int sinks) {
+  const int G = Hq / Hkv;
+  const int hb = dtype == GDR_BF16 && d >= 64 ? (G + 15) / 16 : (G + kSHeads - 1) / kSHeads;
+  const long base = (long)N * Hkv * hb;
+  long most = capacity;
+  if (window && most > (long)window + sinks) most = (long)window + sinks;
+  const long by_tokens = (most + kWarps * kTile - 1) / (kWarps * kTile);
+  const long by_ctas = (148L * 8 + base - 1) / base;
+  long s = by_tokens < by_ctas ? by_tokens : by_ctas;
+  if (s < 1) s = 1;
+  return (int)(s > 256 ? 256 : s);
+}
+
+cudaError_t launch_attn_decode(const PagedArgs& a, cudaStream_t st) {
+  return a.dtype == GDR_F32 ? launch_d<float>(a, st) : launch_d<__nv_bfloat16>(a, st);
+}
+
+cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t st) {
+  const size_t total = (size_t)a.N * a.K * a.Hkv * a.pieces;
+  kv_append_kernel<<<(unsigned)((total + 255) / 256), 256, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace gdr

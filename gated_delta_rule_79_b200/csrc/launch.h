@@ -102,6 +102,99 @@ struct BackwardArgs {
 size_t backward_workspace_bytes(int B, int T, int H, int dk, int dv);
 cudaError_t launch_backward(const BackwardArgs& a, cudaStream_t stream);
 
+// ---- linear attention with one decay per head (lin_common.cuh) -------------------------
+// One scan over the tokens: the prefill, or one of the three that the gradients are.
+struct LinJob {
+  const void* q;        // [B, T, H, dk]
+  const void* k;        // [B, T, H, dk]
+  const void* v;        // [B, T, H, dv]
+  void* o;              // [B, T, H, dv]
+  const float* s_in;    // [B, H, dv, dk] entering state ([B, H, dk, dv] with s_trans), or null
+  float* s_out;         // [B, H, dv, dk], or null
+  int rev;              // 1: from the last token to the first
+  int e0;               // decay steps between the entering state and the first output (0 or 1)
+  int s_trans;
+};
+constexpr int kLinMaxJobs = 3;
+struct LinScan {
+  LinJob job[kLinMaxJobs];
+  const float* decay;   // [H]
+  float* part;          // [njobs, B, H, nseg - 1, dv, dk]: what each segment left
+  unsigned int* status;
+  int njobs, B, T, H, dk, dv, dtype;
+  int seg_len, nseg;
+};
+cudaError_t launch_lin_simt(const LinScan& sc, cudaStream_t stream);
+
+struct LinDecodeArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* decay;
+  float* state;
+  void* o;
+  int N, H, dk, dv, dtype;
+};
+cudaError_t launch_lin_decode(const LinDecodeArgs& a, cudaStream_t stream);
+
+// ---- softmax attention with a sliding window and sinks (attn_common.cuh) ----------------
+struct AttnArgs {
+  const void* q;        // [B, Tq, Hq, d]
+  const void* k;        // [B, Tk, Hkv, d]
+  const void* v;
+  const int* lengths;   // [B] or null
+  void* o;              // [B, Tq, Hq, d]
+  float* lse;           // [B, Hq, Tq] or null (forward only)
+  unsigned int* status;
+  int B, Tq, Tk, Hq, Hkv, d;
+  int window, sinks;    // window 0: none (and then no sinks)
+  float scale;
+  int dtype;
+};
+struct AttnGradArgs {
+  AttnArgs f;           // the forward's arguments and results
+  const void* dO;
+  float* delta;         // [B, Hq, Tq] workspace: do . o of every row
+  void* dq;
+  void* dk;
+  void* dv;
+};
+cudaError_t launch_attn_forward_simt(const AttnArgs& a, cudaStream_t stream);
+cudaError_t launch_attn_delta(const AttnGradArgs& a, cudaStream_t stream);
+cudaError_t launch_attn_backward_simt(const AttnGradArgs& a, cudaStream_t stream);
+
+struct PagedArgs {
+  const void* q;        // [N, Hq, d]
+  const void* k_new;    // [N, Hkv, d] or null
+  const void* v_new;
+  void* kc;             // [npages, 1 << page_shift, Hkv, d]
+  void* vc;
+  const int* table;     // [N, max_pages]
+  const int* lengths;   // [N]
+  void* o;              // [N, Hq, d]
+  float* part;          // [N, Hq] x (nsplit x d outputs, nsplit x (max, sum))
+  unsigned int* status;
+  int N, Hq, Hkv, d, npages, page_shift, max_pages, window, sinks, nsplit;
+  float scale;
+  int dtype;
+};
+int attn_decode_splits(int N, int Hq, int Hkv, int d, int dtype, long capacity, int window,
+                       int sinks);
+cudaError_t launch_attn_decode(const PagedArgs& a, cudaStream_t stream);
+
+struct AppendArgs {
+  const void* k;        // [N, K, Hkv, d]
+  const void* v;
+  void* kc;
+  void* vc;
+  const int* table;
+  const int* start;     // [N]
+  const int* counts;    // [N] or null
+  unsigned int* status; // may be null
+  int N, K, Hkv, pieces, npages, page_shift, max_pages;   // pieces: 16-byte pieces of a row
+};
+cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t stream);
+
 // Records `msg` as the calling thread's gdr_last_error() text and returns `s`.
 int report_error(int s, const char* msg);
 

@@ -1,0 +1,288 @@
+// Linear attention with one decay per head on the CUDA cores, all in fp32: fp32 tensors,
+// and head sizes the tensor-core kernels do not take (lin_tc.cu).  The algebra and the two
+// passes over the segments are in lin_common.cuh.
+//
+// Chunks of 32 tokens.  A thread of the 16 x 16 grid keeps (d_v / 16) x (d_k / 16) elements
+// of the state in registers, so the rank-32 update of a chunk costs one shared-memory read
+// per 4 to 8 multiply-adds; the outputs' kernel mirrors the state in shared memory for
+// S q.  Bound: fp32 multiply-adds, 2 (2 d_k d_v + 16 (d_k + d_v)) flops a token.
+
+#include "lin_common.cuh"
+
+namespace gdr {
+namespace {
+
+using namespace lin;
+
+constexpr int kC = 32;
+constexpr int kThreads = 256;
+
+// The sum over the segment's tokens of a^(n-1-i) v_i k_i^T.
+template <typename T, int DK, int DV>
+__global__ void __launch_bounds__(kThreads)
+lin_segment_simt(const LinScan sc) {
+  const LinJob& jb = sc.job[blockIdx.y];
+  __shared__ float ks[kC][DK + 4], vs[kC][DV + 4], w[kC];
+  const int p = blockIdx.x % (sc.nseg - 1), bh = blockIdx.x / (sc.nseg - 1);
+  const int b = bh / sc.H, h = bh % sc.H;
+  const Segment sg = segment(p, jb.rev, sc.T, sc.seg_len, sc.nseg);
+  const double l2 = log2_decay(sc.decay[h]);
+  const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+  float acc[DV / 16][DK / 16] = {};
+  const T* kb = (const T*)jb.k + (((size_t)b * sc.T + sg.a) * sc.H + h) * DK;
+  const T* vb = (const T*)jb.v + (((size_t)b * sc.T + sg.a) * sc.H + h) * DV;
+  for (int x0 = 0; x0 < sg.n; x0 += kC) {
+    __syncthreads();
+    if (tid < kC) {
+      const int x = x0 + tid;
+      w[tid] = x < sg.n ? (float)decay_pow(l2, jb.rev ? x : sg.n - 1 - x) : 0.f;
+    }
+    for (int e = tid; e < kC * (DK / 4); e += kThreads) {
+      const int r = e / (DK / 4), c = (e % (DK / 4)) * 4;
+      float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (x0 + r < sg.n) f = Elem<T>::load4(kb + (size_t)(x0 + r) * sc.H * DK + c);
+      *reinterpret_cast<float4*>(&ks[r][c]) = f;
+    }
+    for (int e = tid; e < kC * (DV / 4); e += kThreads) {
+      const int r = e / (DV / 4), c = (e % (DV / 4)) * 4;
+      float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (x0 + r < sg.n) f = Elem<T>::load4(vb + (size_t)(x0 + r) * sc.H * DV + c);
+      *reinterpret_cast<float4*>(&vs[r][c]) = f;
+    }
+    __syncthreads();
+    for (int r = 0; r < kC; ++r) {
+      float kk[DK / 16], wr = w[r];
+#pragma unroll
+      for (int j = 0; j < DK / 16; ++j) kk[j] = ks[r][tx + 16 * j] * wr;
+#pragma unroll
+      for (int i = 0; i < DV / 16; ++i) {
+        const float vv = vs[r][ty + 16 * i];
+#pragma unroll
+        for (int j = 0; j < DK / 16; ++j) acc[i][j] = fmaf(vv, kk[j], acc[i][j]);
+      }
+    }
+  }
+  float* dst = sc.part + (((size_t)blockIdx.y * sc.B * sc.H + bh) * (sc.nseg - 1) + p) * DV * DK;
+#pragma unroll
+  for (int i = 0; i < DV / 16; ++i)
+#pragma unroll
+    for (int j = 0; j < DK / 16; ++j) dst[(ty + 16 * i) * DK + tx + 16 * j] = acc[i][j];
+}
+
+template <int DK, int DV>
+struct OutSmem {
+  float st[DK][DV + 4];          // the state entering the chunk, transposed
+  float q[kC][DK + 4], k[kC][DK + 4], v[kC][DV + 4];
+  float p[kC][kC + 1];
+  float pw[kC + 1];              // a^n, n = 0 .. 32
+};
+
+template <typename T, int DK, int DV>
+__global__ void __launch_bounds__(kThreads)
+lin_out_simt(const LinScan sc) {
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  OutSmem<DK, DV>& sm = *reinterpret_cast<OutSmem<DK, DV>*>(smem_raw);
+  constexpr int VPT = DV / 16, W = VPT < 4 ? VPT : 4, NG = VPT / W;
+  const LinJob& jb = sc.job[blockIdx.y];
+  const int p = blockIdx.x % sc.nseg, bh = blockIdx.x / sc.nseg;
+  const int b = bh / sc.H, h = bh % sc.H;
+  const Segment sg = segment(p, jb.rev, sc.T, sc.seg_len, sc.nseg);
+  const double l2 = log2_decay(sc.decay[h]);
+  const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+  if (tid <= kC) sm.pw[tid] = (float)decay_pow(l2, tid);
+
+  // state entering the segment: the call's own, decayed over the tokens before, and what
+  // the earlier segments left.  For p = 0 it is used as it is, with e0 below.
+  float S[DV / 16][DK / 16] = {};
+  if (jb.s_in) {
+    const float f = p == 0 ? 1.f : (float)decay_pow(l2, (long)sg.before + jb.e0 - 1);
+    const float* s = jb.s_in + (size_t)bh * DV * DK;
+#pragma unroll
+    for (int i = 0; i < DV / 16; ++i)
+#pragma unroll
+      for (int j = 0; j < DK / 16; ++j) {
+        const int r = ty + 16 * i, c = tx + 16 * j;
+        S[i][j] = f * s[jb.s_trans ? c * DV + r : r * DK + c];
+      }
+  }
+  for (int m = 0; m < p; ++m) {
+    const Segment pm = segment(m, jb.rev, sc.T, sc.seg_len, sc.nseg);
+    const float f = (float)decay_pow(l2, (long)sg.before - pm.before - pm.n);
+    const float* s =
+        sc.part + (((size_t)blockIdx.y * sc.B * sc.H + bh) * (sc.nseg - 1) + m) * DV * DK;
+#pragma unroll
+    for (int i = 0; i < DV / 16; ++i)
+#pragma unroll
+      for (int j = 0; j < DK / 16; ++j)
+        S[i][j] = fmaf(f, s[(ty + 16 * i) * DK + tx + 16 * j], S[i][j]);
+  }
+
+  const size_t row0 = ((size_t)b * sc.T + sg.a) * sc.H + h;
+  const T* qb = (const T*)jb.q + row0 * DK;
+  const T* kb = (const T*)jb.k + row0 * DK;
+  const T* vb = (const T*)jb.v + row0 * DV;
+  T* ob = (T*)jb.o + row0 * DV;
+  const int nch = (sg.n + kC - 1) / kC;
+  for (int ci = 0; ci < nch; ++ci) {
+    const int x0 = (jb.rev ? nch - 1 - ci : ci) * kC;
+    const int L = min(kC, sg.n - x0);
+    const int E = (p == 0 && ci == 0) ? jb.e0 : 1;
+    __syncthreads();
+    for (int e = tid; e < kC * (DK / 4); e += kThreads) {
+      const int r = e / (DK / 4), c = (e % (DK / 4)) * 4;
+      float4 fq = make_float4(0.f, 0.f, 0.f, 0.f), fk = fq;
+      if (r < L) {
+        fq = Elem<T>::load4(qb + (size_t)(x0 + r) * sc.H * DK + c);
+        fk = Elem<T>::load4(kb + (size_t)(x0 + r) * sc.H * DK + c);
+      }
+      *reinterpret_cast<float4*>(&sm.q[r][c]) = fq;
+      *reinterpret_cast<float4*>(&sm.k[r][c]) = fk;
+    }
+    for (int e = tid; e < kC * (DV / 4); e += kThreads) {
+      const int r = e / (DV / 4), c = (e % (DV / 4)) * 4;
+      float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < L) f = Elem<T>::load4(vb + (size_t)(x0 + r) * sc.H * DV + c);
+      *reinterpret_cast<float4*>(&sm.v[r][c]) = f;
+    }
+#pragma unroll
+    for (int i = 0; i < DV / 16; ++i)
+#pragma unroll
+      for (int j = 0; j < DK / 16; ++j) sm.st[tx + 16 * j][ty + 16 * i] = S[i][j];
+    __syncthreads();
+    {
+      const int t = tid >> 3, j0 = tid & 7;
+      float g[4] = {};
+      for (int c = 0; c < DK; c += 4) {
+        const float4 a = *reinterpret_cast<const float4*>(&sm.q[t][c]);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          const float4 d = *reinterpret_cast<const float4*>(&sm.k[j0 + 8 * m][c]);
+          g[m] = fmaf(a.x, d.x, fmaf(a.y, d.y, fmaf(a.z, d.z, fmaf(a.w, d.w, g[m]))));
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const int gap = jb.rev ? j0 + 8 * m - t : t - (j0 + 8 * m);
+        sm.p[t][j0 + 8 * m] = gap >= 0 ? g[m] * sm.pw[gap] : 0.f;
+      }
+    }
+    __syncthreads();
+    {
+      float o[2][NG][W] = {};
+      const int t0 = 2 * ty;
+      for (int c = 0; c < DK; ++c) {
+        const float qa = sm.q[t0][c], qc = sm.q[t0 + 1][c];
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+#pragma unroll
+          for (int e = 0; e < W; ++e) {
+            const float s = sm.st[c][tx * W + 16 * W * g + e];
+            o[0][g][e] = fmaf(qa, s, o[0][g][e]);
+            o[1][g][e] = fmaf(qc, s, o[1][g][e]);
+          }
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int i = jb.rev ? L - 1 - (t0 + u) : t0 + u;
+        const float f = t0 + u < L ? sm.pw[i + E] : 0.f;
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+#pragma unroll
+          for (int e = 0; e < W; ++e) o[u][g][e] *= f;
+      }
+      for (int j = 0; j < L; ++j) {
+        const float pa = sm.p[t0][j], pc = sm.p[t0 + 1][j];
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+#pragma unroll
+          for (int e = 0; e < W; ++e) {
+            const float s = sm.v[j][tx * W + 16 * W * g + e];
+            o[0][g][e] = fmaf(pa, s, o[0][g][e]);
+            o[1][g][e] = fmaf(pc, s, o[1][g][e]);
+          }
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        if (t0 + u < L) {
+          T* dst = ob + (size_t)(x0 + t0 + u) * sc.H * DV;
+#pragma unroll
+          for (int g = 0; g < NG; ++g)
+#pragma unroll
+            for (int e = 0; e < W; ++e)
+              Elem<T>::store(dst + tx * W + 16 * W * g + e, o[u][g][e]);
+        }
+    }
+    // the chunk's decay as a pair of floats: its rounding would otherwise be the same in
+    // every chunk and add up over a long prompt
+    const double fd = decay_pow(l2, (long)L - 1 + E);
+    const float fh = (float)fd, fl = (float)(fd - (double)fh);
+#pragma unroll
+    for (int i = 0; i < DV / 16; ++i)
+#pragma unroll
+      for (int j = 0; j < DK / 16; ++j) S[i][j] = fmaf(fh, S[i][j], fl * S[i][j]);
+    for (int r = 0; r < L; ++r) {
+      const float wr = sm.pw[jb.rev ? r : L - 1 - r];
+      float kk[DK / 16];
+#pragma unroll
+      for (int j = 0; j < DK / 16; ++j) kk[j] = sm.k[r][tx + 16 * j] * wr;
+#pragma unroll
+      for (int i = 0; i < DV / 16; ++i) {
+        const float vv = sm.v[r][ty + 16 * i];
+#pragma unroll
+        for (int j = 0; j < DK / 16; ++j) S[i][j] = fmaf(vv, kk[j], S[i][j]);
+      }
+    }
+  }
+  if (jb.s_out && p == sc.nseg - 1) {
+    const float f = (float)decay_pow(l2, 1 - jb.e0);
+    float* s = jb.s_out + (size_t)bh * DV * DK;
+#pragma unroll
+    for (int i = 0; i < DV / 16; ++i)
+#pragma unroll
+      for (int j = 0; j < DK / 16; ++j) s[(ty + 16 * i) * DK + tx + 16 * j] = f * S[i][j];
+  }
+}
+
+template <typename T, int DK, int DV>
+cudaError_t launch_t(const LinScan& sc, cudaStream_t st) {
+  if (sc.nseg > 1) {
+    lin_segment_simt<T, DK, DV>
+        <<<dim3((unsigned)(sc.B * sc.H * (sc.nseg - 1)), sc.njobs), kThreads, 0, st>>>(sc);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  constexpr int smem = (int)sizeof(OutSmem<DK, DV>);
+  auto kern = lin_out_simt<T, DK, DV>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kern<<<dim3((unsigned)(sc.B * sc.H * sc.nseg), sc.njobs), kThreads, smem, st>>>(sc);
+  return cudaGetLastError();
+}
+
+template <typename T, int DK>
+cudaError_t launch_dv(const LinScan& sc, cudaStream_t st) {
+  switch (sc.dv) {
+    case 32: return launch_t<T, DK, 32>(sc, st);
+    case 64: return launch_t<T, DK, 64>(sc, st);
+    case 128: return launch_t<T, DK, 128>(sc, st);
+  }
+  return cudaErrorInvalidValue;
+}
+
+template <typename T>
+cudaError_t launch_dk(const LinScan& sc, cudaStream_t st) {
+  switch (sc.dk) {
+    case 32: return launch_dv<T, 32>(sc, st);
+    case 64: return launch_dv<T, 64>(sc, st);
+    case 128: return launch_dv<T, 128>(sc, st);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t launch_lin_simt(const LinScan& sc, cudaStream_t st) {
+  return sc.dtype == GDR_F32 ? launch_dk<float>(sc, st) : launch_dk<__nv_bfloat16>(sc, st);
+}
+
+}  // namespace gdr

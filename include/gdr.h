@@ -1,6 +1,7 @@
 /*
- * gdr.h - C ABI of libgdr: the gated delta rule token mixers (GDN and KDA) on
- * NVIDIA B200 (sm_100a).
+ * gdr.h - C ABI of libgdr: the gated delta rule token mixers (GDN and KDA), linear
+ * attention with a decay per head, and sliding-window softmax attention, on NVIDIA B200
+ * (sm_100a).
  *
  * The operation.  "Super Apriel: One Checkpoint, Many Speeds", §2A (Mixer
  * Vocabulary) names two recurrent mixers: Gated DeltaNet (GDN), the delta rule
@@ -364,6 +365,108 @@ GDR_API gdr_status kda_backward(const void* q, const void* k, const void* v,
                         int in_dtype, int do_dtype,
                         void* workspace, size_t ws_bytes, void* stream);
 
+/* ---- Linear attention with one decay per head ------------------------------------------
+ *
+ * A third recurrent mixer beside GDN and KDA, without the delta rule's correction:
+ *
+ *     S_t = decay_h S_{t-1} + v_t k_t^T,      o_t = S_t q_t
+ *
+ * decay [H] fp32 in [0, 1] is a constant of each head (0 is an exact 0: o_t sees its own
+ * token only).  States are [B, H, d_v, d_k] fp32 as above; q, k, v, o and the gradients of
+ * q, k, v all have the type `dtype`; head sizes {32, 64, 128}; q is used as given.
+ *
+ * lin_prefill: any T >= 0; s0 NULL for zeros; s_final NULL to skip, or s0 itself.
+ * lin_decode: one token for each of N sequences, the state updated in place.
+ * lin_backward: gradients of L = sum <dO, o> + <ds_final, S_T> with respect to q, k, v and
+ *   s0 (ds0 is written whether s0 was given or not; the decay has none); ds_final NULL for
+ *   zeros.  No output may overlap another argument.  Deterministic.
+ * Workspaces: gdr_lin_workspace_bytes(...) bytes (at least 256), 256-byte aligned.  The
+ * first 256 bytes hold the status word that gdr_workspace_status reads: zero them once
+ * before the first use to use that call; nothing else needs a fill.  Sizes for which it
+ * returns 0 are refused. */
+GDR_API size_t gdr_lin_workspace_bytes(int B, int T, int H, int dk, int dv, int dtype,
+                                       int backward);
+GDR_API gdr_status lin_prefill(const void* q, const void* k, const void* v, const float* decay,
+                       const float* s0, void* o, float* s_final,
+                       int B, int T, int H, int dk, int dv, int dtype,
+                       void* workspace, size_t ws_bytes, void* stream);
+GDR_API gdr_status lin_decode(const void* q, const void* k, const void* v, const float* decay,
+                      float* state, void* o, int N, int H, int dk, int dv, int dtype,
+                      void* stream);
+GDR_API gdr_status lin_backward(const void* q, const void* k, const void* v, const float* decay,
+                        const float* s0, const void* dO, const float* ds_final,
+                        void* dq, void* dk_out, void* dv_out, float* ds0,
+                        int B, int T, int H, int dk, int dv, int dtype,
+                        void* workspace, size_t ws_bytes, void* stream);
+
+/* ---- Softmax attention with a sliding window and sinks ----------------------------------
+ *
+ * The full- and sliding-window-attention mixers.  q, o are [B, Tq, Hq, d] and k, v
+ * [B, Tk, Hkv, d] of one type; query head h reads key head h / (Hq / Hkv); d in
+ * {32, 64, 128}.  Query i sits at position p = Tk - Tq + i (Tq < Tk continues a prompt) and
+ * sees key j when
+ *
+ *     j <= p,  j < lengths[b],  p < lengths[b],  and  p - j < window or j < sinks
+ *
+ * window <= 0 means no window (every j <= p); lengths (int32 device array [B], clamped to
+ * 0 .. Tk) may be NULL for Tk.  o_i = sum_j softmax_j(scale q_i.k_j) v_j and lse_i, the
+ * natural logarithm of the softmax's sum ([B, Hq, Tq] fp32, may be NULL).  A query that sees
+ * nothing gets o = 0 and lse = -inf.  scale > 0.  Keys, values and queries at and past a
+ * sequence's length may hold anything, NaN included; elsewhere they are finite.
+ * With bf16 tensors the softmax weights (and, in the gradients, the weights' gradients) are
+ * rounded to bf16 before they meet the values; sums and statistics are fp32.
+ *
+ * attn_backward: the gradients of q, k, v in the tensors' type for dO [B, Tq, Hq, d], from
+ * the forward's o and lse; zero for what no query sees.  Deterministic.  No output may
+ * overlap another argument.
+ * Workspaces as for the linear mixer, with gdr_attn_workspace_bytes(...) bytes. */
+GDR_API size_t gdr_attn_workspace_bytes(int B, int Tq, int Tk, int Hq, int Hkv, int d, int dtype,
+                                        int backward);
+GDR_API gdr_status attn_prefill(const void* q, const void* k, const void* v, const int* lengths,
+                        void* o, float* lse, int B, int Tq, int Tk, int Hq, int Hkv, int d,
+                        int window, int sinks, float scale, int dtype,
+                        void* workspace, size_t ws_bytes, void* stream);
+GDR_API gdr_status attn_backward(const void* q, const void* k, const void* v, const int* lengths,
+                         const void* o, const float* lse, const void* dO,
+                         void* dq, void* dk, void* dv,
+                         int B, int Tq, int Tk, int Hq, int Hkv, int d,
+                         int window, int sinks, float scale, int dtype,
+                         void* workspace, size_t ws_bytes, void* stream);
+
+/* One new token for each of N sequences over a paged cache.
+ *
+ *   q            [N, Hq, d]
+ *   k, v         [N, Hkv, d] the new token's key and value, or both NULL when they are in the
+ *                cache already.  Given, the call stores them at position lengths[n] - 1
+ *   k_cache,     [npages, page, Hkv, d]; page is a power of two up to 4096
+ *   v_cache
+ *   page_table   [N, max_pages] int32: token t of sequence n lies in row t % page of page
+ *                page_table[n, t / page]
+ *   lengths      [N] int32: tokens of each sequence, the new one included; 0 gives o = 0
+ *   o            [N, Hq, d]
+ *
+ * The query sits at position lengths[n] - 1; window, sinks, scale as above.  Only pages that
+ * hold visible tokens are read (those before a window may have been given away).  Lengths and
+ * table entries are read on the device: lengths are clamped to 0 .. max_pages * page, tokens
+ * whose table entry is outside the pool are left out, and either is recorded in the status
+ * word (GDR_ERR_INVALID_ARG from gdr_workspace_status).  Sequences must not share the page of
+ * their new token.  The workspace must hold gdr_attn_decode_workspace_bytes(...) bytes.
+ *
+ * kv_append stores K tokens of each sequence: k, v [N, K, Hkv, d]; token t < counts[n] (NULL:
+ * K) goes to position start[n] + t.  A position or page outside the cache is skipped and, with
+ * a workspace of at least 256 bytes (may be NULL), recorded there. */
+GDR_API size_t gdr_attn_decode_workspace_bytes(int N, int Hq, int Hkv, int d, int page,
+                                               int max_pages, int window, int sinks, int dtype);
+GDR_API gdr_status attn_decode(const void* q, const void* k, const void* v, void* k_cache,
+                       void* v_cache, const int* page_table, const int* lengths, void* o,
+                       int N, int Hq, int Hkv, int d, int npages, int page, int max_pages,
+                       int window, int sinks, float scale, int dtype,
+                       void* workspace, size_t ws_bytes, void* stream);
+GDR_API gdr_status kv_append(const void* k, const void* v, void* k_cache, void* v_cache,
+                     const int* page_table, const int* start, const int* counts,
+                     int N, int K, int Hkv, int d, int npages, int page, int max_pages,
+                     int dtype, void* workspace, size_t ws_bytes, void* stream);
+
 /* Which prefill kernel a call with these parameters runs: 1 = the bf16
  * tensor-core (tcgen05) kernel, 0 = the fp32 CUDA-core kernel, -1 = the
  * parameters are not supported.  Pure host query, no CUDA call. */
@@ -371,9 +474,10 @@ GDR_API int gdr_prefill_path(int dk, int dv, int in_dtype, int kda);
 
 /* Synchronises `stream`, reads the device status word in `workspace` and clears
  * it.  Returns GDR_OK, GDR_ERR_TIMEOUT if a bounded device-side wait of a
- * prefill kernel gave up since the last check (the outputs of that call are
+ * kernel gave up since the last check (the outputs of that call are
  * then undefined), GDR_ERR_INVALID_ARG if a packed-sequence call found its offsets
- * inconsistent (nothing was processed), or GDR_ERR_CUDA. */
+ * inconsistent (nothing was processed) or a call on a paged cache met a length or page
+ * outside it (those tokens were left out), or GDR_ERR_CUDA. */
 GDR_API gdr_status gdr_workspace_status(void* workspace, size_t ws_bytes, void* stream);
 
 /* Debug aid; the paper has no counterpart.  The library also comes as a debug build,

@@ -30,6 +30,8 @@ chunked_backward
             the same gradients from the chunk algebra (the state gradient chained
             through the chunks in reverse), pinned against backward
 prologue    L2-normalised q, k and the gate from its logit (the fused prologue)
+linear      linear attention with one decay per head, and its gradients
+attention   causal softmax attention with a sliding window and sinks, and its gradients
 """
 
 from .recurrent import gated_delta_rule, decode_step, verify_steps, prefill_varlen  # noqa: F401
@@ -37,3 +39,5 @@ from .chunked import chunked_gated_delta_rule  # noqa: F401
 from .backward import gated_delta_rule_backward  # noqa: F401
 from .chunked_backward import chunked_gated_delta_rule_backward  # noqa: F401
 from .prologue import apply_prologue, gate_from_logit, l2_normalise  # noqa: F401
+from .linear import linear_attention, linear_attention_backward  # noqa: F401
+from .attention import attention, attention_backward, visible  # noqa: F401
