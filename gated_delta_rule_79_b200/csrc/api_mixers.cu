@@ -295,7 +295,9 @@ gdr_status attn_prefill(const void* q, const void* k, const void* v, const int* 
   normalise_window(Tk, window, sinks);
   AttnArgs a{q, k, v, lengths, o, lse, (unsigned int*)workspace, B, Tq, Tk, Hq, Hkv, d,
              window, sinks, scale, dtype};
-  return done(fn, launch_attn_forward_simt(a, (cudaStream_t)stream));
+  const bool tc = dtype == GDR_BF16 && d >= 64 && Tk > 0;
+  return done(fn, tc ? launch_attn_forward_tc(a, (cudaStream_t)stream)
+                     : launch_attn_forward_simt(a, (cudaStream_t)stream));
 }
 
 gdr_status attn_backward(const void* q, const void* k, const void* v, const int* lengths,

@@ -49,6 +49,9 @@ struct KeyTiles {
   int nsink, lo, nwin;
   __device__ __forceinline__ int count() const { return nsink + nwin; }
   __device__ __forceinline__ int tile(int x) const { return x < nsink ? x : lo + x - nsink; }
+  __device__ __forceinline__ bool has(int tl) const {
+    return tl < nsink || (tl >= lo && tl < lo + nwin);
+  }
 };
 template <int BN>
 __device__ __forceinline__ KeyTiles key_tiles(const Mask& m, int i0, int i1) {

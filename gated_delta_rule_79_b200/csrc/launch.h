@@ -160,6 +160,7 @@ struct AttnGradArgs {
   void* dv;
 };
 cudaError_t launch_attn_forward_simt(const AttnArgs& a, cudaStream_t stream);
+cudaError_t launch_attn_forward_tc(const AttnArgs& a, cudaStream_t stream);   // bf16, d >= 64
 cudaError_t launch_attn_delta(const AttnGradArgs& a, cudaStream_t stream);
 cudaError_t launch_attn_backward_simt(const AttnGradArgs& a, cudaStream_t stream);
 
