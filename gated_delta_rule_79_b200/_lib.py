@@ -115,7 +115,7 @@ def _load():
         f = getattr(lib, name)
         f.restype = i
         f.argtypes = args
-    for name, n in (("gdr_lin_workspace_bytes", 7), ("gdr_attn_workspace_bytes", 8),
+    for name, n in (("gdr_lin_workspace_bytes", 7), ("gdr_attn_workspace_bytes", 10),
                     ("gdr_attn_decode_workspace_bytes", 9)):
         f = getattr(lib, name)
         f.restype = sz
@@ -583,9 +583,10 @@ def lin_backward(q, k, v, decay, s0, do, ds_final=None, *, workspace=None, strea
     return dq, dk_, dv_, ds0
 
 
-def attn_workspace_bytes(B, Tq, Tk, Hq, Hkv, d, dtype, backward=False):
+def attn_workspace_bytes(B, Tq, Tk, Hq, Hkv, d, dtype, backward=False, window=0, sinks=0):
     """Bytes of device workspace for attn_prefill (or attn_backward) at these sizes."""
-    return lib.gdr_attn_workspace_bytes(B, Tq, Tk, Hq, Hkv, d, _code(dtype), int(backward))
+    return lib.gdr_attn_workspace_bytes(B, Tq, Tk, Hq, Hkv, d, _int32(window, "window"),
+                                        _int32(sinks, "sinks"), _code(dtype), int(backward))
 
 
 def _lengths(t, name, n, device):
@@ -629,14 +630,13 @@ def attn_prefill(q, k, v, *, window=0, sinks=0, scale=None, lengths=None, o=None
     dev, B, Tq, Tk, Hq, Hkv, d = _attn_shapes(q, k, v)
     code = _code(q.dtype)
     _lengths(lengths, "lengths", B, dev)
+    w, n = _int32(window, "window"), _int32(sinks, "sinks")
     with _on(dev, stream):
         o = _out(o, "o", (B, Tq, Hq, d), q.dtype, dev)
         lse = None if lse is False else _out(lse, "lse", (B, Hq, Tq), torch.float32, dev)
-        ws, nws = _scratch(workspace, lib.gdr_attn_workspace_bytes(B, Tq, Tk, Hq, Hkv, d, code, 0),
-                           dev, "attn_prefill")
+        ws, nws = _scratch(workspace, 256, dev, "attn_prefill")
         _check(lib.attn_prefill(_ptr(q), _ptr(k), _ptr(v), _ptr(lengths), _ptr(o), _ptr(lse), B,
-                                Tq, Tk, Hq, Hkv, d, _int32(window, "window"),
-                                _int32(sinks, "sinks"), d ** -0.5 if scale is None else scale,
+                                Tq, Tk, Hq, Hkv, d, w, n, d ** -0.5 if scale is None else scale,
                                 code, _ptr(ws), nws, _stream(dev, stream)))
     return o, lse
 
@@ -651,14 +651,14 @@ def attn_backward(q, k, v, o, lse, do, *, window=0, sinks=0, scale=None, lengths
     _need(lse, "lse", (B, Hq, Tq), torch.float32, dev)
     _need(do, "do", (B, Tq, Hq, d), q.dtype, dev)
     _lengths(lengths, "lengths", B, dev)
+    w, n = _int32(window, "window"), _int32(sinks, "sinks")
     with _on(dev, stream):
         dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-        ws, nws = _scratch(workspace, lib.gdr_attn_workspace_bytes(B, Tq, Tk, Hq, Hkv, d, code, 1),
-                           dev, "attn_backward")
+        ws, nws = _scratch(workspace, lib.gdr_attn_workspace_bytes(B, Tq, Tk, Hq, Hkv, d, w, n,
+                                                                   code, 1), dev, "attn_backward")
         _check(lib.attn_backward(_ptr(q), _ptr(k), _ptr(v), _ptr(lengths), _ptr(o), _ptr(lse),
-                                 _ptr(do), _ptr(dq), _ptr(dk), _ptr(dv), B, Tq, Tk, Hq, Hkv, d,
-                                 _int32(window, "window"), _int32(sinks, "sinks"),
-                                 d ** -0.5 if scale is None else scale, code, _ptr(ws), nws,
+                                 _ptr(do), _ptr(dq), _ptr(dk), _ptr(dv), B, Tq, Tk, Hq, Hkv, d, w,
+                                 n, d ** -0.5 if scale is None else scale, code, _ptr(ws), nws,
                                  _stream(dev, stream)))
     return dq, dk, dv
 

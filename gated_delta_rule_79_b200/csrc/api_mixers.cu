@@ -138,8 +138,17 @@ gdr_status attn_common(const char* fn, int B, int Tq, int Tk, int Hq, int Hkv, i
   return GDR_OK;
 }
 
-size_t attn_need(int B, int Tq, int Hq, int backward) {
-  return kStatusBytes + (backward ? ((size_t)B * Hq * Tq * sizeof(float) + 255) / 256 * 256 : 0);
+bool attn_tc(int d, int dtype) { return dtype == GDR_BF16 && d >= 64; }
+
+// Status word, then (backward) do . o of every row, then the sums of cut key tiles.  The
+// window is normalised.
+size_t attn_delta_bytes(const AttnArgs& a) {
+  return ((size_t)a.B * a.Hq * a.Tq * sizeof(float) + 255) / 256 * 256;
+}
+size_t attn_need(const AttnArgs& a, bool backward) {
+  if (!backward || a.Tq == 0 || a.Tk == 0 || a.Hq == 0) return kStatusBytes;
+  return kStatusBytes + attn_delta_bytes(a) +
+         (attn_tc(a.d, a.dtype) ? attn_backward_tc_bytes(a) : 0);
 }
 
 int page_shift_of(int page) {
@@ -272,11 +281,15 @@ gdr_status lin_backward(const void* q, const void* k, const void* v, const float
   return done(fn, e);
 }
 
-size_t gdr_attn_workspace_bytes(int B, int Tq, int Tk, int Hq, int Hkv, int d, int dtype,
-                                int backward) {
-  if (attn_common("gdr_attn_workspace_bytes", B, Tq, Tk, Hq, Hkv, d, 0, 1.f, dtype) != GDR_OK)
+size_t gdr_attn_workspace_bytes(int B, int Tq, int Tk, int Hq, int Hkv, int d, int window,
+                                int sinks, int dtype, int backward) {
+  if (attn_common("gdr_attn_workspace_bytes", B, Tq, Tk, Hq, Hkv, d, sinks, 1.f, dtype) != GDR_OK)
     return 0;
-  return attn_need(B, Tq, Hq, backward);
+  normalise_window(Tk, window, sinks);
+  AttnArgs a{};
+  a.B = B, a.Tq = Tq, a.Tk = Tk, a.Hq = Hq, a.Hkv = Hkv, a.d = d;
+  a.window = window, a.sinks = sinks, a.dtype = dtype;
+  return attn_need(a, backward != 0);
 }
 
 gdr_status attn_prefill(const void* q, const void* k, const void* v, const int* lengths, void* o,
@@ -290,12 +303,11 @@ gdr_status attn_prefill(const void* q, const void* k, const void* v, const int* 
   const Arg args[] = {{q, "q", true, 16}, {k, "k", Tk > 0, 16}, {v, "v", Tk > 0, 16},
                       {o, "o", true, 16}, {lse, "lse", false, 16}, {lengths, "lengths", false, 4}};
   if ((s = check_pointers(fn, args)) != GDR_OK) return s;
-  s = check_workspace(fn, workspace, ws_bytes, attn_need(B, Tq, Hq, 0));
-  if (s != GDR_OK) return s;
+  if ((s = check_workspace(fn, workspace, ws_bytes, kStatusBytes)) != GDR_OK) return s;
   normalise_window(Tk, window, sinks);
   AttnArgs a{q, k, v, lengths, o, lse, (unsigned int*)workspace, B, Tq, Tk, Hq, Hkv, d,
              window, sinks, scale, dtype};
-  const bool tc = dtype == GDR_BF16 && d >= 64 && Tk > 0;
+  const bool tc = attn_tc(d, dtype) && Tk > 0;
   return done(fn, tc ? launch_attn_forward_tc(a, (cudaStream_t)stream)
                      : launch_attn_forward_simt(a, (cudaStream_t)stream));
 }
@@ -314,8 +326,12 @@ gdr_status attn_backward(const void* q, const void* k, const void* v, const int*
                       {lse, "lse", nq, 16}, {dO, "do", nq, 16}, {dq, "dq", nq, 16},
                       {dk, "dk", nk, 16}, {dv, "dv", nk, 16}, {lengths, "lengths", false, 4}};
   if ((s = check_pointers(fn, args)) != GDR_OK) return s;
-  s = check_workspace(fn, workspace, ws_bytes, attn_need(B, Tq, Hq, 1));
-  if (s != GDR_OK) return s;
+  normalise_window(Tk, window, sinks);
+  AttnGradArgs a{};
+  a.f = AttnArgs{q, k, v, lengths, const_cast<void*>(o), const_cast<float*>(lse),
+                 (unsigned int*)workspace, B, Tq, Tk, Hq, Hkv, d, window, sinks, scale, dtype};
+  a.dO = dO, a.dq = dq, a.dk = dk, a.dv = dv;
+  if ((s = check_workspace(fn, workspace, ws_bytes, attn_need(a.f, true))) != GDR_OK) return s;
   cudaStream_t st = (cudaStream_t)stream;
   const size_t e = dtype == GDR_F32 ? 4 : 2;
   if (Tq == 0 || Tk == 0) {      // nothing sees anything
@@ -325,13 +341,12 @@ gdr_status attn_backward(const void* q, const void* k, const void* v, const int*
     if (r == cudaSuccess && nk) r = cudaMemsetAsync(dv, 0, (size_t)B * Tk * Hkv * d * e, st);
     return done(fn, r);
   }
-  normalise_window(Tk, window, sinks);
-  AttnGradArgs a{AttnArgs{q, k, v, lengths, const_cast<void*>(o), const_cast<float*>(lse),
-                          (unsigned int*)workspace, B, Tq, Tk, Hq, Hkv, d, window, sinks, scale,
-                          dtype},
-                 dO, (float*)((unsigned char*)workspace + kStatusBytes), dq, dk, dv};
+  unsigned char* ws = (unsigned char*)workspace + kStatusBytes;
+  a.delta = (float*)ws;
+  a.part = (float*)(ws + attn_delta_bytes(a.f));
   cudaError_t r = launch_attn_delta(a, st);
-  if (r == cudaSuccess) r = launch_attn_backward_simt(a, st);
+  if (r == cudaSuccess)
+    r = attn_tc(d, dtype) ? launch_attn_backward_tc(a, st) : launch_attn_backward_simt(a, st);
   return done(fn, r);
 }
 

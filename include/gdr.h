@@ -420,8 +420,8 @@ GDR_API gdr_status lin_backward(const void* q, const void* k, const void* v, con
  * the forward's o and lse; zero for what no query sees.  Deterministic.  No output may
  * overlap another argument.
  * Workspaces as for the linear mixer, with gdr_attn_workspace_bytes(...) bytes. */
-GDR_API size_t gdr_attn_workspace_bytes(int B, int Tq, int Tk, int Hq, int Hkv, int d, int dtype,
-                                        int backward);
+GDR_API size_t gdr_attn_workspace_bytes(int B, int Tq, int Tk, int Hq, int Hkv, int d, int window,
+                                        int sinks, int dtype, int backward);
 GDR_API gdr_status attn_prefill(const void* q, const void* k, const void* v, const int* lengths,
                         void* o, float* lse, int B, int Tq, int Tk, int Hq, int Hkv, int d,
                         int window, int sinks, float scale, int dtype,

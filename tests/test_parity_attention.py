@@ -70,6 +70,13 @@ def test_grouped_heads(dtype, Hq, Hkv):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("window,sinks,lengths", [(100, 3, None), (0, 0, None), (50, 140, [2100])])
+def test_keys_that_many_queries_see(dtype, window, sinks, lengths):
+    """Key tiles with sinks, and early ones without a window, are cut along their queries."""
+    _check(*_inputs(1, 2600, 2600, 4, 1, 64, dtype, 5), dtype, lengths, window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("Tq,Tk", [(1, 400), (5, 131), (130, 513), (200, 70), (3, 1)])
 def test_part_of_a_prompt(dtype, Tq, Tk):
     """The last Tq positions of Tk; with more queries than keys the first ones see nothing."""
