@@ -90,7 +90,8 @@ cudaError_t run_scans(LinScan& sc, void* workspace, cudaStream_t st) {
   sc.status = (unsigned int*)workspace;
   sc.part = (float*)((unsigned char*)workspace + kStatusBytes);
   lin_cut((long)sc.B * sc.H * sc.njobs, sc.T, sc.seg_len, sc.nseg);
-  return launch_lin_simt(sc, st);
+  const bool tc = sc.dtype == GDR_BF16 && sc.dk >= 64 && sc.dv >= 64;
+  return tc ? launch_lin_tc(sc, st) : launch_lin_simt(sc, st);
 }
 
 gdr_status state_through(const char* fn, const float* in, float* out, size_t bytes,

@@ -124,6 +124,7 @@ struct LinScan {
   int njobs, B, T, H, dk, dv, dtype;
   int seg_len, nseg;
 };
+cudaError_t launch_lin_tc(const LinScan& sc, cudaStream_t stream);    // bf16, dk and dv >= 64
 cudaError_t launch_lin_simt(const LinScan& sc, cudaStream_t stream);
 
 struct LinDecodeArgs {

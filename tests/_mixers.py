@@ -42,18 +42,22 @@ def close(x, ref, bound, label=""):
                              f"{x[i]:.6g} for {ref[i]:.6g}, bound {np.broadcast_to(bound, d.shape)[i]:.3g}")
 
 
-def lin_magnitude(q, k, v, decay, s0, chunk=64):
+def lin_magnitude(q, k, v, decay, s0, chunk=64, first=None):
     """What relative errors of the weights and of the state entering each chunk can add up to
     in o (mag), what the fp32 sums behind them add up in magnitude (fine), and the sum of
     magnitudes behind S_T.  fine takes |q|.|k| where mag takes |q.k|: a dot product of n terms
-    in fp32 is off by up to n 2^-24 sum |q_c k_c|, however small the sum itself comes out."""
+    in fp32 is off by up to n 2^-24 sum |q_c k_c|, however small the sum itself comes out.
+    first: length of the first chunk.  A scan from the last token processes the chunks that
+    start at multiples of 64, the ragged one first; where a chunk starts decides which tokens
+    see a rounded state (error 2^-8 |S| |q|) rather than rounded weights (2^-8 |q.k| |v|)."""
     B, T, H, _ = q.shape
     mag, fine = np.zeros(v.shape), np.zeros(v.shape)
     S = np.zeros((B, H, v.shape[-1], q.shape[-1])) if s0 is None else s0.copy()
     tot = np.abs(S)
     a = np.asarray(decay, dtype=np.float64)
-    for c in range(0, T, chunk):
-        L = min(chunk, T - c)
+    first = min(first or chunk, T)
+    for c in [0, *range(first, T, chunk)] if T else []:
+        L = first if c == 0 else min(chunk, T - c)
         i = np.arange(L)
         for b in range(B):
             for h in range(H):

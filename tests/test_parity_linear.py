@@ -126,10 +126,10 @@ def test_backward(dtype, dk, dv, B, T, H, state):
     mq, fq_, _ = lin_magnitude(do, v, k, a, turn(s0))
     fk, fq, fv, fd = flip(k, q, v, do)
     extra = np.zeros((1, 1, 1, 1)) if dsf is None else np.abs(dsf)
-    mv, fv_, tot = lin_magnitude(fk, fq, fd, a, dsf)
-    mk, fk_, _ = lin_magnitude(fv, fd, fq, a, turn(dsf))
+    mv, fv_, tot = lin_magnitude(fk, fq, fd, a, dsf, first=T % 64 or 64)
+    mk, fk_, _ = lin_magnitude(fv, fd, fq, a, turn(dsf), first=T % 64 or 64)
     if dsf is not None:       # the first chunk's tokens meet it with a^i, not a^(i+1)
-        for i in range(min(T, 64)):
+        for i in range(min(T, T % 64 or 64)):
             w = np.asarray(a) ** i
             more = np.einsum("h,bhvk,bhk->bhv", w, extra, np.abs(fk[:, i]))
             mv[:, i] += more
