@@ -3,23 +3,26 @@
 // segments are in lin_common.cuh.
 //
 // Chunks of 64 tokens.  Everything that meets the state runs transposed, value rows in the 128
-// TMEM lanes (d_v = 64 uses its one panel twice and ignores the upper lanes), so the fp32 state
-// stays in tensor memory as an accumulator:
+// TMEM lanes (d_v = 64 uses its one panel twice and ignores the upper lanes); a thread of warps
+// 0-3 holds a row of the fp32 state in registers:
 //
 //     G  = Q K^T                        (64 x 64, bf16 operands as they are: exact products)
 //     P  = G (.) a^(i_t - i_j), lower   (bf16)
 //     O1 = S Q^T,  O2 = V^T P^T,        o = a^(i+E) O1 + O2
-//     S  = a^(L-1+E) S + V^T K~,        K~ = a^(L-1-i) k
+//     KV = V^T K~,                      K~ = a^(L-1-i) k
+//     S  = a^(L-1+E) S + KV
 //
 // A bf16 product with decayed keys would carry a rounding of 2^-9 into the fp32 state, so K~
-// enters as a sum of three bf16 terms (24 bits) whose products are exact.  S itself is rounded
-// to bf16 for O1, P for O2: one rounding of an operand each, as the output's own.
+// enters as a sum of three bf16 terms (24 bits) whose products are exact, the smallest first.
+// KV is a new accumulator for every chunk, added to S by an fp32 fma: the tensor cores truncate
+// what they accumulate, and a state kept there lost 2e-7 of itself with each chunk of its memory
+// (measured: 7e-6 after 4096 tokens at a decay of 1 - 2^-11).  S is rounded to bf16 for O1, P
+// for O2: one rounding of an operand each, as the output's own.
 //
 // Bound: HBM, 2 (d_k + d_v) 2 bytes a token and head: 64 KB a chunk at d = 128, about 2800 cycles
-// of an SM's share of 6.5 TB/s, against 1400 cycles of products and passes of 200 to 600 cycles
-// that run beside each other: warps 0-3 the state (scaling, the bf16 copy), 4-7 K~, 8-11 P and
-// the outputs, 12 issues, 13 loads up to three chunks ahead.  The chain from chunk to chunk is
-// the state's pass and its product.
+// of an SM's share of 6.5 TB/s, against 1400 cycles of products (KV 768 of them) and passes of
+// 200 to 600 cycles that run beside each other: warps 0-3 the state, 4-7 K~, 8-11 P and the
+// outputs, 12 issues, 13 loads up to three chunks ahead.
 //
 // Waits are bounded: a give-up sets the status word, drains what is in flight and ends the CTA.
 
@@ -82,36 +85,31 @@ __device__ __forceinline__ void split_keys(const unsigned char* k, unsigned char
 template <int DK, int DV>
 struct SegLayout {
   static constexpr int KT = kC * DK * 2, VT = kC * DV * 2;
-  static constexpr int STAGE = KT + VT, STAGES = 2;
-  static constexpr int SPLIT = STAGES * STAGE;
-  static constexpr int PW = SPLIT + 3 * KT;              // a^n, n = 0 .. 63
+  static constexpr int STAGE = KT + VT, STAGES = 3;
+  static constexpr int SPLIT = STAGES * STAGE;           // K~, two of them
+  static constexpr int PW = SPLIT + 2 * 3 * KT;          // a^n, n = 0 .. 63
   static constexpr int SMALL = PW + 256;
-  // two CTAs on an SM (228 KB, 1 KB of which each CTA takes itself) leave no room for padding
-  // the tiles to 1024 bytes by hand
-  static constexpr int SMEM = SMALL + 256;
-  static_assert(DK < 128 || DV < 128 || 2 * (SMEM + 1024) <= 228 * 1024, "two CTAs");
+  static constexpr int SMEM = SMALL + 256 + 1024;
+  static_assert(SMEM <= 232448, "shared memory");
 };
 struct SegSmall {
-  unsigned long long full[2], empty[2], kt_full, kt_empty, drained;
-  float far[2];                     // of each stage: a^(tokens of the segment after its chunk)
+  unsigned long long full[3], empty[3], kt_full[2], kv_done[2], kv_free[2], drained;
+  float far[3];                     // of each stage: a^(tokens of the segment after its chunk)
   uint32_t tmem;
   int abort;
 };
-constexpr int kSegWarps = 10;       // 0-7 split the keys, 8 issues, 9 loads
+constexpr int kLinWarps = 16;       // four warpgroups for the register split, 14 warps at work
 
 struct LinMaps {
   CUtensorMap q[kLinMaxJobs], k[kLinMaxJobs], v[kLinMaxJobs];
 };
 
 template <int DK, int DV>
-__global__ void __launch_bounds__(kSegWarps * 32, 2)
+__global__ void __launch_bounds__(kLinWarps * 32, 1)
 lin_segment_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin) {
   using L = SegLayout<DK, DV>;
-  extern __shared__ __align__(1024) unsigned char sm[];
-  if ((smem_u32(sm) & 1023u) != 0) {       // the tiles' swizzle needs it
-    atomicOr(sc.status, 1u);
-    return;
-  }
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   SegSmall& ss = *reinterpret_cast<SegSmall*>(sm + L::SMALL);
   float* pw = reinterpret_cast<float*>(sm + L::PW);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -123,18 +121,21 @@ lin_segment_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t 
   const int nch = (sg.n + kC - 1) / kC;
   const double l2 = log2_decay(sc.decay[h]);
   if (tid == 0) {
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < 3; ++s) {
       mbar_init(mb(ss.full[s]), 1);
       mbar_init(mb(ss.empty[s]), 1);
     }
-    mbar_init(mb(ss.kt_full), 8);
-    mbar_init(mb(ss.kt_empty), 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(mb(ss.kt_full[s]), 8);
+      mbar_init(mb(ss.kv_done[s]), 1);
+      mbar_init(mb(ss.kv_free[s]), 4);
+    }
     mbar_init(mb(ss.drained), 1);
     ss.abort = 0;
     fence_mbar_init();
   }
   if (tid < kC) pw[tid] = (float)decay_pow(l2, tid);
-  if (warp == 0) tmem_alloc(&ss.tmem, 128);
+  if (warp == 0) tmem_alloc(&ss.tmem, 256);
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
@@ -142,86 +143,107 @@ lin_segment_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t 
   const uint32_t sb = smem_u32(sm);
   const Waits wait{sc.status, &ss.abort, spin};
 
-  if (warp < 8) {
+  // (a sum: the order of the chunks does not matter, they run as they lie)
+  if (warp < 4) {
+    more_registers<208>();
+    // ---- the sum over the chunks: thread = value row ----------------------------------------
+    const int v = warp * 32 + lane;
+    const uint32_t tl = (uint32_t)(warp * 32) << 16;
+    float S[DK];
+#pragma unroll
+    for (int e = 0; e < DK; ++e) S[e] = 0.f;
     bool ok = true;
     for (int c = 0; c < nch; ++c) {
-      const int s = c & 1;
-      if (!(ok = wait(mb(ss.full[s]), (uint32_t)(c >> 1) & 1u))) break;
-      if (!(ok = wait(mb(ss.kt_empty), ((uint32_t)c & 1u) ^ 1u))) break;
-      const float far = ss.far[s];
-      const int last = min(kC, sg.n - c * kC) - 1;
-      split_keys<DK, 256>(sm + s * L::STAGE, sm + L::SPLIT, tid,
-                          [&](int r) { return far * pw[rev ? r : max(last - r, 0)]; });
-      fence_smem_to_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(mb(ss.kt_full));
-    }
-    // the last product has completed when its buffer is released
-    if (ok && nch > 0) ok = wait(mb(ss.kt_empty), (uint32_t)(nch - 1) & 1u);
-    if (ok && warp < 4) {
+      const int w = c & 1;
+      if (!(ok = wait(mb(ss.kv_done[w]), (uint32_t)(c >> 1) & 1u))) break;
       fence_after_sync();
-      const int v = warp * 32 + lane;
-      float* dst = sc.part + (((size_t)job * sc.B * sc.H + bh) * (sc.nseg - 1) + p) * DV * DK +
-                   (size_t)v * DK;
 #pragma unroll
       for (int q = 0; q < DK / 32; ++q) {
         float x[32];
-        tmem_ld32(tb + ((uint32_t)(warp * 32) << 16) + 32 * q, x);
+        tmem_ld32(tb + tl + 128 * w + 32 * q, x);
         tmem_wait_ld();
-        if (v < DV) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            reinterpret_cast<float4*>(dst + 32 * q)[e] =
-                make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
-        }
+        for (int e = 0; e < 32; ++e) S[32 * q + e] += x[e];
       }
+      fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(mb(ss.kv_free[w]));
     }
-  } else if (warp == 8) {
-    constexpr uint32_t id = idesc_a_mn(idesc_bf16_mn(128, DK));
+    if (ok && v < DV) {
+      float* dst = sc.part + (((size_t)job * sc.B * sc.H + bh) * (sc.nseg - 1) + p) * DV * DK +
+                   (size_t)v * DK;
+#pragma unroll
+      for (int e = 0; e < DK / 4; ++e)
+        reinterpret_cast<float4*>(dst)[e] =
+            make_float4(S[4 * e], S[4 * e + 1], S[4 * e + 2], S[4 * e + 3]);
+    }
+  } else if (warp < 12) {
+    fewer_registers<112>();
+    // ---- K~ ----------------------------------------------------------------------------------
     for (int c = 0; c < nch; ++c) {
-      const int s = c & 1;
-      if (!wait(mb(ss.full[s]), (uint32_t)(c >> 1) & 1u)) break;
-      if (!wait(mb(ss.kt_full), (uint32_t)c & 1u)) break;
-      fence_after_sync();
-#pragma unroll
-      for (int t = 0; t < 3; ++t)
-#pragma unroll
-        for (int ks = 0; ks < kC / 16; ++ks)
-          mma_bf16_w(tb, v_as_a<DV>(sb + s * L::STAGE + L::KT, ks),
-                     mnmajor(sb + L::SPLIT + t * L::KT, kC, ks), id, c > 0 || t > 0 || ks > 0);
-      mma_commit_w(mb(ss.empty[s]));
-      mma_commit_w(mb(ss.kt_empty));
+      const int s = c % 3, w = c & 1;
+      if (!wait(mb(ss.full[s]), (uint32_t)(c / 3) & 1u)) break;
+      // the product of chunk c - 2 has read this buffer
+      if (c >= 2 && !wait(mb(ss.kv_done[w]), (uint32_t)((c - 2) >> 1) & 1u)) break;
+      const float far = ss.far[s];
+      const int last = min(kC, sg.n - c * kC) - 1;
+      split_keys<DK, 256>(sm + s * L::STAGE, sm + L::SPLIT + w * 3 * L::KT, tid - 128,
+                          [&](int r) { return far * pw[rev ? r : max(last - r, 0)]; });
+      fence_smem_to_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(mb(ss.kt_full[w]));
     }
-    // the products issued here complete before tensor memory is freed
-    mma_commit_w(mb(ss.drained));
-    mbar_wait(mb(ss.drained), 0, kDrain);
   } else {
-    int done = 0;
-    for (int c = 0; c < nch; ++c) {
-      const int s = c & 1;
-      if (!wait(mb(ss.empty[s]), ((uint32_t)(c >> 1) & 1u) ^ 1u)) break;
-      const int t0 = sg.a + c * kC;      // a sum: the order does not matter
-      if (lane == 0) {
-        const int L0 = min(kC, sg.a + sg.n - t0);
-        const long after = rev ? t0 - sg.a : sg.a + sg.n - t0 - L0;
-        ss.far[s] = (float)decay_pow(l2, after);
-        mbar_expect_tx(mb(ss.full[s]), L::STAGE);
-        for (int pn = 0; pn < DK / 64; ++pn)
-          tma_load_4d(sb + s * L::STAGE + pn * kC * 128, &maps.k[job], 64 * pn, h, t0, b,
-                      mb(ss.full[s]));
-        for (int pn = 0; pn < DV / 64; ++pn)
-          tma_load_4d(sb + s * L::STAGE + L::KT + pn * kC * 128, &maps.v[job], 64 * pn, h, t0, b,
-                      mb(ss.full[s]));
+    fewer_registers<72>();
+    if (warp == 12) {
+      constexpr uint32_t id = idesc_a_mn(idesc_bf16_mn(128, DK));
+      for (int c = 0; c < nch; ++c) {
+        const int s = c % 3, w = c & 1;
+        if (!wait(mb(ss.full[s]), (uint32_t)(c / 3) & 1u)) break;
+        if (!wait(mb(ss.kt_full[w]), (uint32_t)(c >> 1) & 1u)) break;
+        if (c >= 2 && !wait(mb(ss.kv_free[w]), (uint32_t)((c - 2) >> 1) & 1u)) break;
+        fence_after_sync();
+#pragma unroll
+        for (int t = 2; t >= 0; --t)
+#pragma unroll
+          for (int ks = 0; ks < kC / 16; ++ks)
+            mma_bf16_w(tb + 128 * w, v_as_a<DV>(sb + s * L::STAGE + L::KT, ks),
+                       mnmajor(sb + L::SPLIT + (3 * w + t) * L::KT, kC, ks), id, t < 2 || ks > 0);
+        mma_commit_w(mb(ss.kv_done[w]));
+        mma_commit_w(mb(ss.empty[s]));
       }
-      done = c + 1;
+      // the products issued here complete before tensor memory is freed
+      mma_commit_w(mb(ss.drained));
+      mbar_wait(mb(ss.drained), 0, kDrain);
+    } else if (warp == 13) {
+      int done = 0;
+      for (int c = 0; c < nch; ++c) {
+        const int s = c % 3;
+        if (!wait(mb(ss.empty[s]), ((uint32_t)(c / 3) & 1u) ^ 1u)) break;
+        const int t0 = sg.a + c * kC;
+        if (lane == 0) {
+          const int Lc = min(kC, sg.n - c * kC);
+          const long after = rev ? c * kC : sg.n - c * kC - Lc;
+          ss.far[s] = (float)decay_pow(l2, after);
+          mbar_expect_tx(mb(ss.full[s]), L::STAGE);
+          for (int pn = 0; pn < DK / 64; ++pn)
+            tma_load_4d(sb + s * L::STAGE + pn * kC * 128, &maps.k[job], 64 * pn, h, t0, b,
+                        mb(ss.full[s]));
+          for (int pn = 0; pn < DV / 64; ++pn)
+            tma_load_4d(sb + s * L::STAGE + L::KT + pn * kC * 128, &maps.v[job], 64 * pn, h, t0,
+                        b, mb(ss.full[s]));
+        }
+        done = c + 1;
+      }
+      // copies in flight land before the CTA leaves, also when some warp gave up
+      if (lane == 0)
+        for (int c = max(0, done - 3); c < done; ++c)
+          mbar_wait(mb(ss.full[c % 3]), (uint32_t)(c / 3) & 1u, kDrain);
     }
-    if (lane == 0)
-      for (int c = max(0, done - 2); c < done; ++c)
-        mbar_wait(mb(ss.full[c & 1]), (uint32_t)(c >> 1) & 1u, kDrain);
   }
   fence_before_sync();
   __syncthreads();
-  if (warp == 0) tmem_dealloc(tb, 128);
+  if (warp == 0) tmem_dealloc(tb, 256);
 }
 
 // ---- second pass: the outputs -----------------------------------------------------------------
@@ -237,21 +259,21 @@ struct OutLayout {
   static constexpr int SMEM = SMALL + 512 + 1024;
   static_assert(SMEM <= 232448, "shared memory");
   // tensor memory
-  static constexpr uint32_t S = 0;                       // fp32 state, DK columns
-  static constexpr uint32_t SB = 128;                    // its bf16 copy, DK / 2 columns
+  static constexpr uint32_t KV = 0;                      // DK columns
+  static constexpr uint32_t SB = 128;                    // the state in bf16, DK / 2 columns
   static constexpr uint32_t G = 192;
   static constexpr uint32_t O1 = 256, O2 = 384;          // + 64 * (chunk & 1)
 };
 struct OutSmall {
   unsigned long long full[3], empty[3];
-  unsigned long long g_full, p_full[2], kt_full, s_ready, s_done, o_full[2], o_free[2], drained;
+  unsigned long long g_full, p_full[2], kt_full, kv_done, kv_free, s_ready, o1_done, o_full[2],
+      o_free[2], drained;
   uint32_t tmem;
   int abort;
 };
-constexpr int kOutWarps = 14;
 
 template <int DK, int DV>
-__global__ void __launch_bounds__(kOutWarps * 32, 1)
+__global__ void __launch_bounds__(kLinWarps * 32, 1)
 lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin) {
   using L = OutLayout<DK, DV>;
   extern __shared__ unsigned char smem_raw[];
@@ -267,7 +289,7 @@ lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin
   const int nch = (sg.n + kC - 1) / kC;
   const double l2 = log2_decay(sc.decay[h]);
   float* s_out = p == sc.nseg - 1 ? sc.job[job].s_out : nullptr;
-  const int nstate = s_out ? nch : nch - 1;        // chunks whose state product is needed
+  const int nstate = s_out ? nch : nch - 1;        // chunks whose KV is needed
   if (tid == 0) {
     for (int s = 0; s < 3; ++s) {
       mbar_init(mb(os.full[s]), 1);
@@ -281,7 +303,9 @@ lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin
     mbar_init(mb(os.g_full), 1);
     mbar_init(mb(os.kt_full), 4);
     mbar_init(mb(os.s_ready), 4);
-    mbar_init(mb(os.s_done), 1);
+    mbar_init(mb(os.kv_done), 1);
+    mbar_init(mb(os.kv_free), 4);
+    mbar_init(mb(os.o1_done), 1);
     mbar_init(mb(os.drained), 1);
     os.abort = 0;
     fence_mbar_init();
@@ -298,120 +322,104 @@ lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin
   auto chunk_at = [&](int c) { return (rev ? nch - 1 - c : c) * kC; };
 
   if (warp < 4) {
+    more_registers<208>();
     // ---- the state: thread = value row ----------------------------------------------------
     const int v = warp * 32 + lane;
     const uint32_t tl = (uint32_t)(warp * 32) << 16;
     // entering: the call's own state decayed over the tokens before, and what the earlier
     // segments left
-    {
+    float S[DK];
+#pragma unroll
+    for (int e = 0; e < DK; ++e) S[e] = 0.f;
+    if (v < DV) {
       const LinJob& jb = sc.job[job];
-      const float f0 = p == 0 ? 1.f : (float)decay_pow(l2, (long)sg.before + e0 - 1);
-      const float* part = sc.part + ((size_t)job * sc.B * sc.H + bh) * (sc.nseg - 1) * DV * DK;
-#pragma unroll 1
-      for (int q = 0; q < DK / 32; ++q) {
-        float x[32];
+      if (jb.s_in) {
+        const float f = p == 0 ? 1.f : (float)decay_pow(l2, (long)sg.before + e0 - 1);
+        const float* s = jb.s_in + (size_t)bh * DV * DK;
+        if (jb.s_trans) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) x[e] = 0.f;
-        if (v < DV) {
-          if (jb.s_in) {
-            const float* s = jb.s_in + (size_t)bh * DV * DK;
-            if (jb.s_trans) {
+          for (int e = 0; e < DK; ++e) S[e] = f * s[(size_t)e * DV + v];
+        } else {
 #pragma unroll
-              for (int e = 0; e < 32; ++e) x[e] = f0 * s[(size_t)(32 * q + e) * DV + v];
-            } else {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float4 y =
-                    *reinterpret_cast<const float4*>(s + (size_t)v * DK + 32 * q + 4 * e);
-                x[4 * e] = f0 * y.x;
-                x[4 * e + 1] = f0 * y.y;
-                x[4 * e + 2] = f0 * y.z;
-                x[4 * e + 3] = f0 * y.w;
-              }
-            }
-          }
-          for (int m = 0; m < p; ++m) {
-            const Segment pm = segment(m, rev, sc.T, sc.seg_len, sc.nseg);
-            const float f = (float)decay_pow(l2, (long)sg.before - pm.before - pm.n);
-            const float* s = part + (size_t)m * DV * DK + (size_t)v * DK + 32 * q;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float4 y = *reinterpret_cast<const float4*>(s + 4 * e);
-              x[4 * e] = fmaf(f, y.x, x[4 * e]);
-              x[4 * e + 1] = fmaf(f, y.y, x[4 * e + 1]);
-              x[4 * e + 2] = fmaf(f, y.z, x[4 * e + 2]);
-              x[4 * e + 3] = fmaf(f, y.w, x[4 * e + 3]);
-            }
+          for (int e = 0; e < DK / 4; ++e) {
+            const float4 y = *reinterpret_cast<const float4*>(s + (size_t)v * DK + 4 * e);
+            S[4 * e] = f * y.x;
+            S[4 * e + 1] = f * y.y;
+            S[4 * e + 2] = f * y.z;
+            S[4 * e + 3] = f * y.w;
           }
         }
-        tmem_st32(tb + tl + L::S + 32 * q, x);
       }
-      tmem_wait_st();
+      const float* part = sc.part +
+                          ((size_t)job * sc.B * sc.H + bh) * (sc.nseg - 1) * DV * DK +
+                          (size_t)v * DK;
+      for (int m = 0; m < p; ++m) {
+        const Segment pm = segment(m, rev, sc.T, sc.seg_len, sc.nseg);
+        const float f = (float)decay_pow(l2, (long)sg.before - pm.before - pm.n);
+        const float* s = part + (size_t)m * DV * DK;
+#pragma unroll
+        for (int e = 0; e < DK / 4; ++e) {
+          const float4 y = *reinterpret_cast<const float4*>(s + 4 * e);
+          S[4 * e] = fmaf(f, y.x, S[4 * e]);
+          S[4 * e + 1] = fmaf(f, y.y, S[4 * e + 1]);
+          S[4 * e + 2] = fmaf(f, y.z, S[4 * e + 2]);
+          S[4 * e + 3] = fmaf(f, y.w, S[4 * e + 3]);
+        }
+      }
     }
     bool ok = true;
     for (int c = 0; c < nch; ++c) {
-      if (c > 0 && !(ok = wait(mb(os.s_done), (uint32_t)(c - 1) & 1u))) break;
+      // the bf16 copy, once O1 of the chunk before has read the last one
+      if (c > 0 && !(ok = wait(mb(os.o1_done), (uint32_t)(c - 1) & 1u))) break;
       fence_after_sync();
+#pragma unroll
+      for (int q = 0; q < DK / 64; ++q) {
+        float y[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) y[e] = pack2(S[64 * q + 2 * e], S[64 * q + 2 * e + 1]);
+        tmem_st32(tb + tl + L::SB + 32 * q, y);
+      }
+      tmem_wait_st();
+      fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(mb(os.s_ready));
+      if (c >= nstate) break;
       const int E = p == 0 && c == 0 ? e0 : 1;
       const int Lc = min(kC, sg.n - chunk_at(c));
       // the chunk's decay as a pair of floats: its rounding would otherwise be the same in
       // every chunk and add up over a long prompt
       const double fd = decay_pow(l2, (long)Lc - 1 + E);
       const float fh = (float)fd, fl = (float)(fd - (double)fh);
-      const float2 fh2 = make_float2(fh, fh), fl2 = make_float2(fl, fl);
+      if (!(ok = wait(mb(os.kv_done), (uint32_t)c & 1u))) break;
+      fence_after_sync();
 #pragma unroll
-      for (int q = 0; q < DK / 64; ++q) {
-        float x[64], y[32];
-        tmem_ld32(tb + tl + L::S + 64 * q, reinterpret_cast<float(&)[32]>(x[0]));
-        tmem_ld32(tb + tl + L::S + 64 * q + 32, reinterpret_cast<float(&)[32]>(x[32]));
+      for (int q = 0; q < DK / 32; ++q) {
+        float x[32];
+        tmem_ld32(tb + tl + L::KV + 32 * q, x);
         tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 32; ++e) y[e] = pack2(x[2 * e], x[2 * e + 1]);
-        // the copy may be overwritten: the product that read it came before s_done
-        tmem_st32(tb + tl + L::SB + 32 * q, y);
-        if (c < nstate) {
-#pragma unroll
-          for (int e = 0; e < 64; e += 2) {
-            const float2 u = make_float2(x[e], x[e + 1]);
-            const float2 z = fma2(u, fh2, mul2(u, fl2));
-            x[e] = z.x;
-            x[e + 1] = z.y;
-          }
-          tmem_st32(tb + tl + L::S + 64 * q, reinterpret_cast<float(&)[32]>(x[0]));
-          tmem_st32(tb + tl + L::S + 64 * q + 32, reinterpret_cast<float(&)[32]>(x[32]));
-        }
+        for (int e = 0; e < 32; ++e)
+          S[32 * q + e] = fmaf(fh, S[32 * q + e], fmaf(fl, S[32 * q + e], x[e]));
       }
-      tmem_wait_st();
       fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(mb(os.s_ready));
+      if (lane == 0) mbar_arrive(mb(os.kv_free));
     }
-    if (s_out) {
-      if (ok) ok = wait(mb(os.s_done), (uint32_t)(nch - 1) & 1u);
-      if (ok) {
-        fence_after_sync();
-        const float f = (float)decay_pow(l2, 1 - e0);
-        float* dst = s_out + (size_t)bh * DV * DK + (size_t)v * DK;
+    if (s_out && ok && v < DV) {
+      const float f = (float)decay_pow(l2, 1 - e0);
+      float* dst = s_out + (size_t)bh * DV * DK + (size_t)v * DK;
 #pragma unroll
-        for (int q = 0; q < DK / 32; ++q) {
-          float x[32];
-          tmem_ld32(tb + tl + L::S + 32 * q, x);
-          tmem_wait_ld();
-          if (v < DV) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              reinterpret_cast<float4*>(dst + 32 * q)[e] =
-                  make_float4(f * x[4 * e], f * x[4 * e + 1], f * x[4 * e + 2], f * x[4 * e + 3]);
-          }
-        }
-      }
+      for (int e = 0; e < DK / 4; ++e)
+        reinterpret_cast<float4*>(dst)[e] = make_float4(f * S[4 * e], f * S[4 * e + 1],
+                                                        f * S[4 * e + 2], f * S[4 * e + 3]);
     }
   } else if (warp < 8) {
+    fewer_registers<112>();
     // ---- K~ ----------------------------------------------------------------------------------
     for (int c = 0; c < nstate; ++c) {
       const int s = c % 3;
       if (!wait(mb(os.full[s]), (uint32_t)(c / 3) & 1u)) break;
-      if (c > 0 && !wait(mb(os.s_done), (uint32_t)(c - 1) & 1u)) break;
+      if (c > 0 && !wait(mb(os.kv_done), (uint32_t)(c - 1) & 1u)) break;
       const int last = min(kC, sg.n - chunk_at(c)) - 1;
       split_keys<DK, 128>(sm + s * L::STAGE + L::KT, sm + L::SPLIT, tid - 128,
                           [&](int r) { return pw[rev ? r : max(last - r, 0)]; });
@@ -420,6 +428,7 @@ lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin
       if (lane == 0) mbar_arrive(mb(os.kt_full));
     }
   } else if (warp < 12) {
+    fewer_registers<112>();
     // ---- P of chunk c, then the outputs of chunk c - 1 ----------------------------------------
     const int q4 = warp & 3;
     const uint32_t tl = (uint32_t)(q4 * 32) << 16;
@@ -491,84 +500,90 @@ lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin
         if (lane == 0) mbar_arrive(mb(os.o_free[w]));
       }
     }
-  } else if (warp == 12) {
-    // ---- issuing warp --------------------------------------------------------------------------
-    constexpr uint32_t id_g = idesc_bf16(64, 64), id_o1 = idesc_bf16(128, 64),
-                       id_o2 = idesc_a_mn(idesc_bf16(128, 64)),
-                       id_s = idesc_a_mn(idesc_bf16_mn(128, DK));
-    for (int c = 0; c <= nch; ++c) {
-      const int s = c % 3, w = c & 1;
-      const uint32_t at = sb + s * L::STAGE;
-      if (c < nch) {
-        if (!wait(mb(os.full[s]), (uint32_t)(c / 3) & 1u)) break;
-        // G is free once P of the chunk before has been formed
-        if (c > 0 && !wait(mb(os.p_full[w ^ 1]), (uint32_t)((c - 1) >> 1) & 1u)) break;
-        fence_after_sync();
-#pragma unroll
-        for (int ks = 0; ks < DK / 16; ++ks)
-          mma_bf16_w(tb + L::G, kmajor(at, kC, ks), kmajor(at + L::KT, kC, ks), id_g, ks > 0);
-        mma_commit_w(mb(os.g_full));
-      }
-      if (c > 0) {
-        // O2 of chunk c - 1
-        const int d = c - 1, sd = d % 3, wd = d & 1;
-        if (c == nch && !wait(mb(os.p_full[wd]), (uint32_t)(d >> 1) & 1u)) break;
-        fence_after_sync();
-#pragma unroll
-        for (int ks = 0; ks < kC / 16; ++ks)
-          mma_bf16_w(tb + L::O2 + 64 * wd, v_as_a<DV>(sb + sd * L::STAGE + 2 * L::KT, ks),
-                     kmajor(sb + L::P + wd * 8192, kC, ks), id_o2, ks > 0);
-        mma_commit_w(mb(os.o_full[wd]));
-        mma_commit_w(mb(os.empty[sd]));
-      }
-      if (c < nch) {
-        if (!wait(mb(os.s_ready), (uint32_t)c & 1u)) break;
-        if (c >= 2 && !wait(mb(os.o_free[w]), (uint32_t)((c - 2) >> 1) & 1u)) break;
-        fence_after_sync();
-#pragma unroll
-        for (int ks = 0; ks < DK / 16; ++ks)
-          mma_bf16_ta_w(tb + L::O1 + 64 * w, tb + L::SB + 8 * ks, kmajor(at, kC, ks), id_o1,
-                        ks > 0);
-        if (c < nstate) {
-          if (!wait(mb(os.kt_full), (uint32_t)c & 1u)) break;
+  } else {
+    fewer_registers<72>();
+    if (warp == 12) {
+      // ---- issuing warp --------------------------------------------------------------------------
+      constexpr uint32_t id_g = idesc_bf16(64, 64), id_o1 = idesc_bf16(128, 64),
+                         id_o2 = idesc_a_mn(idesc_bf16(128, 64)),
+                         id_kv = idesc_a_mn(idesc_bf16_mn(128, DK));
+      for (int c = 0; c <= nch; ++c) {
+        const int s = c % 3, w = c & 1;
+        const uint32_t at = sb + s * L::STAGE;
+        if (c < nch) {
+          if (!wait(mb(os.full[s]), (uint32_t)(c / 3) & 1u)) break;
+          // G is free once P of the chunk before has been formed
+          if (c > 0 && !wait(mb(os.p_full[w ^ 1]), (uint32_t)((c - 1) >> 1) & 1u)) break;
           fence_after_sync();
 #pragma unroll
-          for (int t = 0; t < 3; ++t)
+          for (int ks = 0; ks < DK / 16; ++ks)
+            mma_bf16_w(tb + L::G, kmajor(at, kC, ks), kmajor(at + L::KT, kC, ks), id_g, ks > 0);
+          mma_commit_w(mb(os.g_full));
+        }
+        if (c > 0) {
+          // O2 of chunk c - 1
+          const int d = c - 1, sd = d % 3, wd = d & 1;
+          if (c == nch && !wait(mb(os.p_full[wd]), (uint32_t)(d >> 1) & 1u)) break;
+          fence_after_sync();
+#pragma unroll
+          for (int ks = 0; ks < kC / 16; ++ks)
+            mma_bf16_w(tb + L::O2 + 64 * wd, v_as_a<DV>(sb + sd * L::STAGE + 2 * L::KT, ks),
+                       kmajor(sb + L::P + wd * 8192, kC, ks), id_o2, ks > 0);
+          mma_commit_w(mb(os.o_full[wd]));
+          mma_commit_w(mb(os.empty[sd]));
+        }
+        if (c < nstate) {
+          // the accumulator is free once the state has taken the chunk before
+          if (!wait(mb(os.kt_full), (uint32_t)c & 1u)) break;
+          if (c > 0 && !wait(mb(os.kv_free), (uint32_t)(c - 1) & 1u)) break;
+          fence_after_sync();
+#pragma unroll
+          for (int t = 2; t >= 0; --t)
 #pragma unroll
             for (int ks = 0; ks < kC / 16; ++ks)
-              mma_bf16_w(tb + L::S, v_as_a<DV>(at + 2 * L::KT, ks),
-                         mnmajor(sb + L::SPLIT + t * L::KT, kC, ks), id_s, true);
-          mma_commit_w(mb(os.s_done));
+              mma_bf16_w(tb + L::KV, v_as_a<DV>(at + 2 * L::KT, ks),
+                         mnmajor(sb + L::SPLIT + t * L::KT, kC, ks), id_kv, t < 2 || ks > 0);
+          mma_commit_w(mb(os.kv_done));
+        }
+        if (c < nch) {
+          if (!wait(mb(os.s_ready), (uint32_t)c & 1u)) break;
+          if (c >= 2 && !wait(mb(os.o_free[w]), (uint32_t)((c - 2) >> 1) & 1u)) break;
+          fence_after_sync();
+#pragma unroll
+          for (int ks = 0; ks < DK / 16; ++ks)
+            mma_bf16_ta_w(tb + L::O1 + 64 * w, tb + L::SB + 8 * ks, kmajor(at, kC, ks), id_o1,
+                          ks > 0);
+          mma_commit_w(mb(os.o1_done));
         }
       }
-    }
-    // the products issued here complete before tensor memory is freed
-    mma_commit_w(mb(os.drained));
-    mbar_wait(mb(os.drained), 0, kDrain);
-  } else if (warp == 13) {
-    // ---- loader -----------------------------------------------------------------------------------
-    int done = 0;
-    for (int c = 0; c < nch; ++c) {
-      const int s = c % 3;
-      if (!wait(mb(os.empty[s]), ((uint32_t)(c / 3) & 1u) ^ 1u)) break;
-      if (lane == 0) {
-        const uint32_t at = sb + s * L::STAGE;
-        const int t0 = sg.a + chunk_at(c);
-        uint64_t* bar = mb(os.full[s]);
-        mbar_expect_tx(bar, L::STAGE);
-        for (int pn = 0; pn < DK / 64; ++pn) {
-          tma_load_4d(at + pn * kC * 128, &maps.q[job], 64 * pn, h, t0, b, bar);
-          tma_load_4d(at + L::KT + pn * kC * 128, &maps.k[job], 64 * pn, h, t0, b, bar);
+      // the products issued here complete before tensor memory is freed
+      mma_commit_w(mb(os.drained));
+      mbar_wait(mb(os.drained), 0, kDrain);
+    } else if (warp == 13) {
+      // ---- loader -----------------------------------------------------------------------------------
+      int done = 0;
+      for (int c = 0; c < nch; ++c) {
+        const int s = c % 3;
+        if (!wait(mb(os.empty[s]), ((uint32_t)(c / 3) & 1u) ^ 1u)) break;
+        if (lane == 0) {
+          const uint32_t at = sb + s * L::STAGE;
+          const int t0 = sg.a + chunk_at(c);
+          uint64_t* bar = mb(os.full[s]);
+          mbar_expect_tx(bar, L::STAGE);
+          for (int pn = 0; pn < DK / 64; ++pn) {
+            tma_load_4d(at + pn * kC * 128, &maps.q[job], 64 * pn, h, t0, b, bar);
+            tma_load_4d(at + L::KT + pn * kC * 128, &maps.k[job], 64 * pn, h, t0, b, bar);
+          }
+          for (int pn = 0; pn < DV / 64; ++pn)
+            tma_load_4d(at + 2 * L::KT + pn * kC * 128, &maps.v[job], 64 * pn, h, t0, b, bar);
         }
-        for (int pn = 0; pn < DV / 64; ++pn)
-          tma_load_4d(at + 2 * L::KT + pn * kC * 128, &maps.v[job], 64 * pn, h, t0, b, bar);
+        done = c + 1;
       }
-      done = c + 1;
+      // copies in flight land before the CTA leaves, also when some warp gave up
+      if (lane == 0)
+        for (int c = max(0, done - 3); c < done; ++c)
+          mbar_wait(mb(os.full[c % 3]), (uint32_t)(c / 3) & 1u, kDrain);
     }
-    // copies in flight land before the CTA leaves, also when some warp gave up
-    if (lane == 0)
-      for (int c = max(0, done - 3); c < done; ++c)
-        mbar_wait(mb(os.full[c % 3]), (uint32_t)(c / 3) & 1u, kDrain);
   }
   fence_before_sync();
   __syncthreads();
@@ -590,7 +605,7 @@ cudaError_t launch_t(const LinScan& sc, cudaStream_t st) {
     constexpr int smem = SegLayout<DK, DV>::SMEM;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kern<<<dim3((unsigned)(sc.B * sc.H * (sc.nseg - 1)), sc.njobs), kSegWarps * 32, smem, st>>>(
+    kern<<<dim3((unsigned)(sc.B * sc.H * (sc.nseg - 1)), sc.njobs), kLinWarps * 32, smem, st>>>(
         maps, sc, spin);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
@@ -598,7 +613,7 @@ cudaError_t launch_t(const LinScan& sc, cudaStream_t st) {
   constexpr int smem = OutLayout<DK, DV>::SMEM;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kern<<<dim3((unsigned)(sc.B * sc.H * sc.nseg), sc.njobs), kOutWarps * 32, smem, st>>>(maps, sc,
+  kern<<<dim3((unsigned)(sc.B * sc.H * sc.nseg), sc.njobs), kLinWarps * 32, smem, st>>>(maps, sc,
                                                                                        spin);
   return cudaGetLastError();
 }
