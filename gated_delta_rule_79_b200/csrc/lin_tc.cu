@@ -9,10 +9,10 @@
 //     G  = Q K^T                        (64 x 64, bf16 operands as they are: exact products)
 //     P  = G (.) a^(i_t - i_j), lower   (bf16)
 //     O1 = S Q^T,  O2 = V^T P^T,        o = a^(i+E) O1 + O2
-//     KV = V^T K~,                      K~ = a^(L-1-i) k
+//     KV = V~^T K,                      V~ = a^(L-1-i) v
 //     S  = a^(L-1+E) S + KV
 //
-// A bf16 product with decayed keys would carry a rounding of 2^-9 into the fp32 state, so K~
+// A bf16 product with decayed values would carry a rounding of 2^-9 into the fp32 state, so V~
 // enters as a sum of three bf16 terms (24 bits) whose products are exact, the smallest first.
 // KV is a new accumulator for every chunk, added to S by an fp32 fma: the tensor cores truncate
 // what they accumulate, and a state kept there lost 2e-7 of itself with each chunk of its memory
@@ -20,9 +20,12 @@
 // for O2: one rounding of an operand each, as the output's own.
 //
 // Bound: HBM, 2 (d_k + d_v) 2 bytes a token and head: 64 KB a chunk at d = 128, about 2800 cycles
-// of an SM's share of 6.5 TB/s, against 1400 cycles of products (KV 768 of them) and passes of
-// 200 to 600 cycles that run beside each other: warps 0-3 the state, 4-7 K~, 8-11 P and the
-// outputs, 12 issues, 13 loads up to three chunks ahead.
+// of an SM's share of 6.5 TB/s.  Next to it is shared memory: at N = 128 a product reads its two
+// operands at the full 128 bytes a cycle.  So V~^T and S are A operands from tensor memory, K is
+// read as TMA left it, and nothing but P and the outputs is written (with decayed keys as three
+// tiles in shared memory a chunk took 7600 cycles).  Passes run beside each other: warps 0-3
+// the state, 4-7 V~, 8-11 P, 12-15 the outputs, 16 and 17 issue (16 G, O1, O2; 17 KV, which waits
+// for none of them), 18 loads up to four chunks ahead.
 //
 // Waits are bounded: a give-up sets the status word, drains what is in flight and ends the CTA.
 
@@ -43,41 +46,103 @@ __device__ __forceinline__ uint64_t* mb(unsigned long long& x) {
 }
 __host__ __device__ constexpr uint32_t idesc_a_mn(uint32_t id) { return id | (1u << 15); }
 
-// V^T as an A operand with M = 128: with one panel of 64 value rows both halves read it.
-template <int DV>
-__device__ __forceinline__ uint64_t v_as_a(uint32_t tile, int ks) {
-  return sdesc(tile + (uint32_t)ks * 2048, DV == 128 ? kC * 128 : 0, 1024);
+// Descriptors of a tile's first k-step; the others lie a constant further on (16-byte units).
+__device__ __forceinline__ uint64_t k_base(uint32_t tile) { return sdesc(tile, 16, 1024); }
+__host__ __device__ constexpr uint64_t k_step(int ks) {          // K-major, 64 rows
+  return (uint64_t)((ks >> 2) * kC * 128 + (ks & 3) * 32) >> 4;
+}
+__device__ __forceinline__ uint64_t mn_base(uint32_t tile, bool two_panels) {
+  return sdesc(tile, two_panels ? kC * 128 : 0, 1024);
+}
+__host__ __device__ constexpr uint64_t mn_step(int ks) { return (uint64_t)(ks * 2048) >> 4; }
+
+// tcgen05.ld of 16 lanes x 64 columns spread over all 32 threads: x[4 n + 2 h + e] is row
+// lane / 4 + 8 h, column 8 n + 2 (lane % 4) + e.
+__device__ __forceinline__ void tmem_ld_16x64(uint32_t taddr, float (&v)[32]) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+        "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+      :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
+         "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]),
+         "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
 }
 
-// One thread's share (pieces of eight channels) of K~ = weight(row) k as three bf16 tiles.
-template <int DK, int THREADS, typename W>
-__device__ __forceinline__ void split_keys(const unsigned char* k, unsigned char* kt, int t,
-                                           W weight) {
-  constexpr int TILE = kC * DK * 2;
-#pragma unroll 2
-  for (int e = t; e < kC * (DK / 8); e += THREADS) {
-    // pieces of a panel row follow each other as stored: the swizzle only permutes them
-    const int r = (e >> 3) % kC, pn = e / (8 * kC), at = pn * kC * 128 + r * 128 + (e & 7) * 16;
-    const uint4 x = *reinterpret_cast<const uint4*>(k + at);
-    const uint32_t* xs = reinterpret_cast<const uint32_t*>(&x);
-    const float w = weight(r);
-    uint4 out[3];
+// V~^T of one chunk into tensor memory by four warps: thread = value channel (TMEM lane), two
+// tokens to a column, the three bf16 terms 32 columns apart.  wt: the rows' weights, times far.
+template <int DV>
+__device__ __forceinline__ void weigh_values(const unsigned char* v, uint32_t taddr, int lane_id,
+                                             const float* wt, float far) {
+  const int ch = lane_id % DV;
+  const unsigned char* col = v + (ch >> 6) * kC * 128 + (ch & 7) * 2;
+  const int c3 = (ch & 63) >> 3;
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      float u = __uint_as_float(xs[c] << 16) * w, v = __uint_as_float(xs[c] & 0xffff0000u) * w;
+  for (int half = 0; half < 2; ++half) {
+    uint32_t out[3][16];
 #pragma unroll
-      for (int s = 0; s < 3; ++s) {
-        const __nv_bfloat162 p = __floats2bfloat162_rn(u, v);
-        const uint32_t b = *reinterpret_cast<const uint32_t*>(&p);
-        reinterpret_cast<uint32_t*>(&out[s])[c] = b;
-        u -= __uint_as_float(b << 16);
-        v -= __uint_as_float(b & 0xffff0000u);
+    for (int q = 0; q < 8; ++q) {
+      const float4 w4 = *reinterpret_cast<const float4*>(wt + 32 * half + 4 * q);
+      const float w[4] = {w4.x * far, w4.y * far, w4.z * far, w4.w * far};
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = 32 * half + 4 * q + 2 * e;
+        const uint32_t x = *reinterpret_cast<const unsigned short*>(
+            col + r * 128 + ((c3 ^ (r & 7)) << 4));
+        const uint32_t y = *reinterpret_cast<const unsigned short*>(
+            col + (r + 1) * 128 + ((c3 ^ ((r + 1) & 7)) << 4));
+        float a = __uint_as_float(x << 16) * w[2 * e], b = __uint_as_float(y << 16) * w[2 * e + 1];
+#pragma unroll
+        for (int s = 0; s < 3; ++s) {
+          const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
+          const uint32_t u = *reinterpret_cast<const uint32_t*>(&p);
+          out[s][2 * q + e] = u;
+          a -= __uint_as_float(u << 16);
+          b -= __uint_as_float(u & 0xffff0000u);
+        }
       }
     }
-    *reinterpret_cast<uint4*>(kt + at) = out[0];
-    *reinterpret_cast<uint4*>(kt + TILE + at) = out[1];
-    *reinterpret_cast<uint4*>(kt + 2 * TILE + at) = out[2];
+#pragma unroll
+    for (int s = 0; s < 3; ++s) tmem_st16(taddr + 32 * s + 16 * half, out[s]);
   }
+}
+
+// KV = V~^T K: twelve products, the smallest terms first (A in tensor memory, B the K tile).
+template <int DK>
+__device__ __forceinline__ void issue_kv(uint32_t d, uint32_t vw, uint32_t k_tile) {
+  constexpr uint32_t id = idesc_bf16_mn(128, DK);
+  const uint64_t kb = mn_base(k_tile, DK == 128);
+#pragma unroll
+  for (int t = 2; t >= 0; --t)
+#pragma unroll
+    for (int ks = 0; ks < kC / 16; ++ks)
+      mma_bf16_ta_w(d, vw + 32 * t + 8 * ks, kb + mn_step(ks), id, t < 2 || ks > 0);
+}
+
+struct LinMaps {
+  CUtensorMap q[kLinMaxJobs], k[kLinMaxJobs], v[kLinMaxJobs], o[kLinMaxJobs];
+};
+
+// Weights of the rows of a whole chunk and of the call's ragged last one: a^(L-1-i), where row r
+// is token i = r, or L-1-r in a reversed scan.
+struct RowTables {
+  float wt[2][kC];
+};
+__device__ __forceinline__ float row_weight(double l2, int rev, int L, int r) {
+  return r < L ? (float)decay_pow(l2, rev ? r : L - 1 - r) : 0.f;
 }
 
 // ---- first pass: what a segment leaves in the state ---------------------------------------
@@ -85,33 +150,32 @@ __device__ __forceinline__ void split_keys(const unsigned char* k, unsigned char
 template <int DK, int DV>
 struct SegLayout {
   static constexpr int KT = kC * DK * 2, VT = kC * DV * 2;
-  static constexpr int STAGE = KT + VT, STAGES = 3;
-  static constexpr int SPLIT = STAGES * STAGE;           // K~, two of them
-  static constexpr int PW = SPLIT + 2 * 3 * KT;          // a^n, n = 0 .. 63
-  static constexpr int SMALL = PW + 256;
-  static constexpr int SMEM = SMALL + 256 + 1024;
+  static constexpr int STAGE = KT + VT, STAGES = 6;
+  static constexpr int TAB = STAGES * STAGE;
+  static constexpr int SMALL = TAB + (int)sizeof(RowTables);
+  static constexpr int SMEM = SMALL + 512 + 1024;
   static_assert(SMEM <= 232448, "shared memory");
+  // tensor memory: KV and V~ of buffer w
+  static constexpr uint32_t KV = 0;                      // + 128 w
+  static constexpr uint32_t VW = 256;                    // + 96 w
 };
 struct SegSmall {
-  unsigned long long full[3], empty[3], kt_full[2], kv_done[2], kv_free[2], drained;
-  float far[3];                     // of each stage: a^(tokens of the segment after its chunk)
+  unsigned long long full[6], empty[6], vw_full[2], kv_done[2], kv_free[2], drained;
+  float far[6];                     // of each stage: a^(tokens of the segment after its chunk)
   uint32_t tmem;
   int abort;
 };
-constexpr int kLinWarps = 16;       // four warpgroups for the register split, 14 warps at work
-
-struct LinMaps {
-  CUtensorMap q[kLinMaxJobs], k[kLinMaxJobs], v[kLinMaxJobs];
-};
+constexpr int kSegWarps = 16;       // 0-3 sum, 4-7 and 8-11 V~ of every other chunk, 12, 13
 
 template <int DK, int DV>
-__global__ void __launch_bounds__(kLinWarps * 32, 1)
+__global__ void __launch_bounds__(kSegWarps * 32, 1)
 lin_segment_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin) {
   using L = SegLayout<DK, DV>;
+  constexpr int NS = L::STAGES;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   SegSmall& ss = *reinterpret_cast<SegSmall*>(sm + L::SMALL);
-  float* pw = reinterpret_cast<float*>(sm + L::PW);
+  RowTables& tab = *reinterpret_cast<RowTables*>(sm + L::TAB);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int job = blockIdx.y;
   const int rev = sc.job[job].rev;
@@ -121,12 +185,12 @@ lin_segment_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t 
   const int nch = (sg.n + kC - 1) / kC;
   const double l2 = log2_decay(sc.decay[h]);
   if (tid == 0) {
-    for (int s = 0; s < 3; ++s) {
+    for (int s = 0; s < NS; ++s) {
       mbar_init(mb(ss.full[s]), 1);
       mbar_init(mb(ss.empty[s]), 1);
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(mb(ss.kt_full[s]), 8);
+      mbar_init(mb(ss.vw_full[s]), 4);
       mbar_init(mb(ss.kv_done[s]), 1);
       mbar_init(mb(ss.kv_free[s]), 4);
     }
@@ -134,8 +198,10 @@ lin_segment_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t 
     ss.abort = 0;
     fence_mbar_init();
   }
-  if (tid < kC) pw[tid] = (float)decay_pow(l2, tid);
-  if (warp == 0) tmem_alloc(&ss.tmem, 256);
+  if (tid < 2 * kC)
+    tab.wt[tid / kC][tid % kC] =
+        row_weight(l2, rev, tid < kC ? kC : sg.n - (nch - 1) * kC, tid % kC);
+  if (warp == 0) tmem_alloc(&ss.tmem, 512);
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
@@ -160,7 +226,7 @@ lin_segment_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t 
 #pragma unroll
       for (int q = 0; q < DK / 32; ++q) {
         float x[32];
-        tmem_ld32(tb + tl + 128 * w + 32 * q, x);
+        tmem_ld32(tb + tl + L::KV + 128 * w + 32 * q, x);
         tmem_wait_ld();
 #pragma unroll
         for (int e = 0; e < 32; ++e) S[32 * q + e] += x[e];
@@ -178,37 +244,33 @@ lin_segment_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t 
             make_float4(S[4 * e], S[4 * e + 1], S[4 * e + 2], S[4 * e + 3]);
     }
   } else if (warp < 12) {
-    fewer_registers<112>();
-    // ---- K~ ----------------------------------------------------------------------------------
-    for (int c = 0; c < nch; ++c) {
-      const int s = c % 3, w = c & 1;
-      if (!wait(mb(ss.full[s]), (uint32_t)(c / 3) & 1u)) break;
+    fewer_registers<104>();
+    // ---- V~ ----------------------------------------------------------------------------------
+    const int w = warp < 8 ? 0 : 1;
+    const uint32_t tl = (uint32_t)((warp & 3) * 32) << 16;
+    for (int c = w; c < nch; c += 2) {
+      const int s = c % NS;
+      if (!wait(mb(ss.full[s]), (uint32_t)(c / NS) & 1u)) break;
       // the product of chunk c - 2 has read this buffer
       if (c >= 2 && !wait(mb(ss.kv_done[w]), (uint32_t)((c - 2) >> 1) & 1u)) break;
-      const float far = ss.far[s];
-      const int last = min(kC, sg.n - c * kC) - 1;
-      split_keys<DK, 256>(sm + s * L::STAGE, sm + L::SPLIT + w * 3 * L::KT, tid - 128,
-                          [&](int r) { return far * pw[rev ? r : max(last - r, 0)]; });
-      fence_smem_to_async();
+      fence_after_sync();
+      weigh_values<DV>(sm + s * L::STAGE + L::KT, tb + tl + L::VW + 96 * w,
+                       (warp & 3) * 32 + lane, tab.wt[sg.n - c * kC < kC], ss.far[s]);
+      tmem_wait_st();
+      fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(mb(ss.kt_full[w]));
+      if (lane == 0) mbar_arrive(mb(ss.vw_full[w]));
     }
   } else {
-    fewer_registers<72>();
+    fewer_registers<80>();
     if (warp == 12) {
-      constexpr uint32_t id = idesc_a_mn(idesc_bf16_mn(128, DK));
       for (int c = 0; c < nch; ++c) {
-        const int s = c % 3, w = c & 1;
-        if (!wait(mb(ss.full[s]), (uint32_t)(c / 3) & 1u)) break;
-        if (!wait(mb(ss.kt_full[w]), (uint32_t)(c >> 1) & 1u)) break;
+        const int s = c % NS, w = c & 1;
+        if (!wait(mb(ss.full[s]), (uint32_t)(c / NS) & 1u)) break;
+        if (!wait(mb(ss.vw_full[w]), (uint32_t)(c >> 1) & 1u)) break;
         if (c >= 2 && !wait(mb(ss.kv_free[w]), (uint32_t)((c - 2) >> 1) & 1u)) break;
         fence_after_sync();
-#pragma unroll
-        for (int t = 2; t >= 0; --t)
-#pragma unroll
-          for (int ks = 0; ks < kC / 16; ++ks)
-            mma_bf16_w(tb + 128 * w, v_as_a<DV>(sb + s * L::STAGE + L::KT, ks),
-                       mnmajor(sb + L::SPLIT + (3 * w + t) * L::KT, kC, ks), id, t < 2 || ks > 0);
+        issue_kv<DK>(tb + L::KV + 128 * w, tb + L::VW + 96 * w, sb + s * L::STAGE);
         mma_commit_w(mb(ss.kv_done[w]));
         mma_commit_w(mb(ss.empty[s]));
       }
@@ -218,8 +280,8 @@ lin_segment_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t 
     } else if (warp == 13) {
       int done = 0;
       for (int c = 0; c < nch; ++c) {
-        const int s = c % 3;
-        if (!wait(mb(ss.empty[s]), ((uint32_t)(c / 3) & 1u) ^ 1u)) break;
+        const int s = c % NS;
+        if (!wait(mb(ss.empty[s]), ((uint32_t)(c / NS) & 1u) ^ 1u)) break;
         const int t0 = sg.a + c * kC;
         if (lane == 0) {
           const int Lc = min(kC, sg.n - c * kC);
@@ -237,49 +299,59 @@ lin_segment_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t 
       }
       // copies in flight land before the CTA leaves, also when some warp gave up
       if (lane == 0)
-        for (int c = max(0, done - 3); c < done; ++c)
-          mbar_wait(mb(ss.full[c % 3]), (uint32_t)(c / 3) & 1u, kDrain);
+        for (int c = max(0, done - NS); c < done; ++c)
+          mbar_wait(mb(ss.full[c % NS]), (uint32_t)(c / NS) & 1u, kDrain);
     }
   }
   fence_before_sync();
   __syncthreads();
-  if (warp == 0) tmem_dealloc(tb, 256);
+  if (warp == 0) tmem_dealloc(tb, 512);
 }
 
 // ---- second pass: the outputs -----------------------------------------------------------------
 
+struct OutTables {
+  RowTables rows;
+  float fo[4][kC];                  // a^(i+E): [E + 2 ragged]
+  float pw[kC];                     // a^n
+};
+
 template <int DK, int DV>
 struct OutLayout {
   static constexpr int KT = kC * DK * 2, VT = kC * DV * 2;
-  static constexpr int STAGE = 2 * KT + VT, STAGES = 3;  // q, k, v
-  static constexpr int SPLIT = STAGES * STAGE;
-  static constexpr int P = SPLIT + 3 * KT;               // bf16 [64 t][64 j], two of them
-  static constexpr int PW = P + 2 * 8192;                // a^n, n = 0 .. 64
-  static constexpr int SMALL = PW + 512;
-  static constexpr int SMEM = SMALL + 512 + 1024;
+  static constexpr int STAGE = 2 * KT + VT, STAGES = 4;  // q, k, v
+  static constexpr int P = STAGES * STAGE;               // bf16 [64 t][64 j], two of them
+  static constexpr int O = P + 2 * 8192;                 // outputs on their way out
+  static constexpr int TAB = O + VT;
+  static constexpr int SMALL = TAB + (int)sizeof(OutTables);
+  static constexpr int SMEM = SMALL + 256 + 1024;
   static_assert(SMEM <= 232448, "shared memory");
   // tensor memory
   static constexpr uint32_t KV = 0;                      // DK columns
   static constexpr uint32_t SB = 128;                    // the state in bf16, DK / 2 columns
   static constexpr uint32_t G = 192;
-  static constexpr uint32_t O1 = 256, O2 = 384;          // + 64 * (chunk & 1)
+  static constexpr uint32_t VW = 256;                    // 96 columns
+  static constexpr uint32_t O1 = 384, O2 = 448;
 };
 struct OutSmall {
-  unsigned long long full[3], empty[3];
-  unsigned long long g_full, p_full[2], kt_full, kv_done, kv_free, s_ready, o1_done, o_full[2],
-      o_free[2], drained;
+  unsigned long long full[4], empty[4];
+  unsigned long long g_full, p_full[2], vw_full, kv_done, kv_free, s_ready, o1_done, o_full,
+      o_free, drained[2];
   uint32_t tmem;
   int abort;
 };
+// five warpgroups: 640 threads of 96 registers at launch, then 192 + 80 + 72 + 80 + 56
+constexpr int kOutWarps = 20;
 
 template <int DK, int DV>
-__global__ void __launch_bounds__(kLinWarps * 32, 1)
+__global__ void __launch_bounds__(kOutWarps * 32, 1)
 lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin) {
   using L = OutLayout<DK, DV>;
+  constexpr int NS = L::STAGES;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   OutSmall& os = *reinterpret_cast<OutSmall*>(sm + L::SMALL);
-  float* pw = reinterpret_cast<float*>(sm + L::PW);
+  OutTables& tab = *reinterpret_cast<OutTables*>(sm + L::TAB);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int job = blockIdx.y;
   const int rev = sc.job[job].rev, e0 = sc.job[job].e0;
@@ -291,26 +363,37 @@ lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin
   float* s_out = p == sc.nseg - 1 ? sc.job[job].s_out : nullptr;
   const int nstate = s_out ? nch : nch - 1;        // chunks whose KV is needed
   if (tid == 0) {
-    for (int s = 0; s < 3; ++s) {
+    for (int s = 0; s < NS; ++s) {
       mbar_init(mb(os.full[s]), 1);
-      mbar_init(mb(os.empty[s]), 1);
+      mbar_init(mb(os.empty[s]), 2);               // both issuing warps have read the stage
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(mb(os.p_full[s]), 4);
-      mbar_init(mb(os.o_full[s]), 1);
-      mbar_init(mb(os.o_free[s]), 4);
+      mbar_init(mb(os.drained[s]), 1);
     }
     mbar_init(mb(os.g_full), 1);
-    mbar_init(mb(os.kt_full), 4);
-    mbar_init(mb(os.s_ready), 4);
+    mbar_init(mb(os.vw_full), 4);
     mbar_init(mb(os.kv_done), 1);
     mbar_init(mb(os.kv_free), 4);
+    mbar_init(mb(os.s_ready), 4);
     mbar_init(mb(os.o1_done), 1);
-    mbar_init(mb(os.drained), 1);
+    mbar_init(mb(os.o_full), 1);
+    mbar_init(mb(os.o_free), 4);
     os.abort = 0;
     fence_mbar_init();
   }
-  if (tid <= kC) pw[tid] = (float)decay_pow(l2, tid);
+  {
+    const int ragged = sg.n - (nch - 1) * kC;
+    const int r = tid % kC, x = tid / kC;          // ten rows of 64 threads
+    if (x < 2) {
+      tab.rows.wt[x][r] = row_weight(l2, rev, x ? ragged : kC, r);
+    } else if (x < 6) {
+      const int Lc = x >= 4 ? ragged : kC;
+      tab.fo[x - 2][r] = (float)decay_pow(l2, (rev ? max(Lc - 1 - r, 0) : r) + (x & 1));
+    } else if (x == 6) {
+      tab.pw[r] = (float)decay_pow(l2, r);
+    }
+  }
   if (warp == 0) tmem_alloc(&os.tmem, 512);
   fence_before_sync();
   __syncthreads();
@@ -322,7 +405,7 @@ lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin
   auto chunk_at = [&](int c) { return (rev ? nch - 1 - c : c) * kC; };
 
   if (warp < 4) {
-    more_registers<208>();
+    more_registers<192>();
     // ---- the state: thread = value row ----------------------------------------------------
     const int v = warp * 32 + lane;
     const uint32_t tl = (uint32_t)(warp * 32) << 16;
@@ -367,6 +450,10 @@ lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin
         }
       }
     }
+    // a chunk's decay as a pair of floats: its rounding would otherwise be the same in every
+    // chunk and add up over a long prompt
+    float fh = 0.f, fl = 0.f;
+    int steps = -1;
     bool ok = true;
     for (int c = 0; c < nch; ++c) {
       // the bf16 copy, once O1 of the chunk before has read the last one
@@ -384,12 +471,13 @@ lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin
       __syncwarp();
       if (lane == 0) mbar_arrive(mb(os.s_ready));
       if (c >= nstate) break;
-      const int E = p == 0 && c == 0 ? e0 : 1;
-      const int Lc = min(kC, sg.n - chunk_at(c));
-      // the chunk's decay as a pair of floats: its rounding would otherwise be the same in
-      // every chunk and add up over a long prompt
-      const double fd = decay_pow(l2, (long)Lc - 1 + E);
-      const float fh = (float)fd, fl = (float)(fd - (double)fh);
+      const int now = min(kC, sg.n - chunk_at(c)) - 1 + (p == 0 && c == 0 ? e0 : 1);
+      if (now != steps) {
+        const double f = decay_pow(l2, now);
+        fh = (float)f;
+        fl = (float)(f - (double)fh);
+        steps = now;
+      }
       if (!(ok = wait(mb(os.kv_done), (uint32_t)c & 1u))) break;
       fence_after_sync();
 #pragma unroll
@@ -397,13 +485,15 @@ lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin
         float x[32];
         tmem_ld32(tb + tl + L::KV + 32 * q, x);
         tmem_wait_ld();
+        if (q == DK / 32 - 1) {
+          fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(mb(os.kv_free));
+        }
 #pragma unroll
         for (int e = 0; e < 32; ++e)
           S[32 * q + e] = fmaf(fh, S[32 * q + e], fmaf(fl, S[32 * q + e], x[e]));
       }
-      fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(mb(os.kv_free));
     }
     if (s_out && ok && v < DV) {
       const float f = (float)decay_pow(l2, 1 - e0);
@@ -414,157 +504,181 @@ lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin
                                                         f * S[4 * e + 2], f * S[4 * e + 3]);
     }
   } else if (warp < 8) {
-    fewer_registers<112>();
-    // ---- K~ ----------------------------------------------------------------------------------
+    fewer_registers<80>();
+    // ---- V~ ----------------------------------------------------------------------------------
+    const uint32_t tl = (uint32_t)((warp & 3) * 32) << 16;
     for (int c = 0; c < nstate; ++c) {
-      const int s = c % 3;
-      if (!wait(mb(os.full[s]), (uint32_t)(c / 3) & 1u)) break;
+      const int s = c % NS;
+      if (!wait(mb(os.full[s]), (uint32_t)(c / NS) & 1u)) break;
       if (c > 0 && !wait(mb(os.kv_done), (uint32_t)(c - 1) & 1u)) break;
-      const int last = min(kC, sg.n - chunk_at(c)) - 1;
-      split_keys<DK, 128>(sm + s * L::STAGE + L::KT, sm + L::SPLIT, tid - 128,
-                          [&](int r) { return pw[rev ? r : max(last - r, 0)]; });
-      fence_smem_to_async();
+      fence_after_sync();
+      weigh_values<DV>(sm + s * L::STAGE + 2 * L::KT, tb + tl + L::VW, (warp & 3) * 32 + lane,
+                       tab.rows.wt[sg.n - chunk_at(c) < kC], 1.f);
+      tmem_wait_st();
+      fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(mb(os.kt_full));
+      if (lane == 0) mbar_arrive(mb(os.vw_full));
     }
   } else if (warp < 12) {
-    fewer_registers<112>();
-    // ---- P of chunk c, then the outputs of chunk c - 1 ----------------------------------------
-    const int q4 = warp & 3;
-    const uint32_t tl = (uint32_t)(q4 * 32) << 16;
-    const int v = q4 * 32 + lane;
-    __nv_bfloat16* ob =
-        (__nv_bfloat16*)sc.job[job].o + (((size_t)b * sc.T + sg.a) * sc.H + h) * DV;
-    for (int c = 0; c <= nch; ++c) {
-      if (c < nch) {
-        if (!wait(mb(os.g_full), (uint32_t)c & 1u)) break;
-        fence_after_sync();
-        // an M = 64 accumulator: row t in lane 32 (t / 16) + t % 16.  P's buffer was last read
-        // by the product of chunk c - 2, which came before this Gram
-        const int t = 16 * q4 + (lane & 15);
-        unsigned char* pt = sm + L::P + (c & 1) * 8192 + t * 128;
+    fewer_registers<72>();
+    // ---- P -------------------------------------------------------------------------------------
+    // an M = 64 accumulator: row t in lane 32 (t / 16) + t % 16
+    const int t0 = 16 * (warp & 3) + (lane >> 2), j0 = 2 * (lane & 3);
+    const uint32_t tl = (uint32_t)((warp & 3) * 32) << 16;
+    for (int c = 0; c < nch; ++c) {
+      if (!wait(mb(os.g_full), (uint32_t)c & 1u)) break;
+      fence_after_sync();
+      float x[32];
+      tmem_ld_16x64(tb + tl + L::G, x);
+      tmem_wait_ld();
+      // P's buffer was last read by O2 of chunk c - 2, which came before this G
+      unsigned char* pt = sm + L::P + (c & 1) * 8192;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          float x[32];
-          tmem_ld32(tb + tl + L::G + 32 * half, x);
-          tmem_wait_ld();
-          if (lane < 16) {
+      for (int n = 0; n < 8; ++n)
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const int gap = rev ? 32 * half + e - t : t - (32 * half + e);
-              x[e] = gap >= 0 ? x[e] * pw[gap] : 0.f;
-            }
+        for (int hf = 0; hf < 2; ++hf) {
+          const int t = t0 + 8 * hf;
+          float y[2];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              *reinterpret_cast<float4*>(pt + (((4 * half + e) ^ (t & 7)) << 4)) =
-                  make_float4(pack2(x[8 * e], x[8 * e + 1]), pack2(x[8 * e + 2], x[8 * e + 3]),
-                              pack2(x[8 * e + 4], x[8 * e + 5]),
-                              pack2(x[8 * e + 6], x[8 * e + 7]));
+          for (int e = 0; e < 2; ++e) {
+            const int j = 8 * n + j0 + e, gap = rev ? j - t : t - j;
+            y[e] = gap >= 0 ? x[4 * n + 2 * hf + e] * tab.pw[max(gap, 0)] : 0.f;
           }
+          *reinterpret_cast<float*>(pt + t * 128 + ((n ^ (t & 7)) << 4) + 2 * j0) =
+              pack2(y[0], y[1]);
         }
-        fence_smem_to_async();
-        fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(mb(os.p_full[c & 1]));
+      fence_smem_to_async();
+      fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(mb(os.p_full[c & 1]));
+    }
+  } else if (warp < 16) {
+    fewer_registers<80>();
+    // ---- the outputs: thread = value channel ------------------------------------------------
+    const int v = (warp & 3) * 32 + lane;
+    const uint32_t tl = (uint32_t)((warp & 3) * 32) << 16;
+    const bool odd = lane & 1;
+    unsigned char* so = sm + L::O + (v >> 6) * kC * 128 + (v & 6) * 2;
+    const int c3 = (v & 63) >> 3;
+    bool ok = true;
+    for (int c = 0; c < nch; ++c) {
+      ok = wait(mb(os.o_full), (uint32_t)c & 1u);
+      // the last store has read its tile
+      if (tid == 12 * 32) bulk_wait_read_all();
+      if (named_bar_or(1, 128, !ok)) break;
+      fence_after_sync();
+      const int at = chunk_at(c);
+      const float* fo = tab.fo[(p == 0 && c == 0 ? e0 : 1) + (sg.n - at < kC ? 2 : 0)];
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        float x[32], y[32];
+        tmem_ld32(tb + tl + L::O1 + 32 * half, x);
+        tmem_ld32(tb + tl + L::O2 + 32 * half, y);
+        tmem_wait_ld();
+        if (half == 1) {
+          fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(mb(os.o_free));
+        }
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(fo + 32 * half + e);
+          x[e] = fmaf(x[e], f.x, y[e]);
+          x[e + 1] = fmaf(x[e + 1], f.y, y[e + 1]);
+          x[e + 2] = fmaf(x[e + 2], f.z, y[e + 2]);
+          x[e + 3] = fmaf(x[e + 3], f.w, y[e + 3]);
+        }
+        // two lanes swap, so that each writes two neighbouring channels of one token
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          const float got = __shfl_xor_sync(0xffffffffu, odd ? x[e] : x[e + 1], 1);
+          const float two = odd ? pack2(got, x[e + 1]) : pack2(x[e], got);
+          const int r = 32 * half + e + odd;
+          if (v < DV)
+            *reinterpret_cast<float*>(so + r * 128 + ((c3 ^ ((e + odd) & 7)) << 4)) = two;
+        }
       }
-      if (c > 0) {
-        const int d = c - 1, w = d & 1;
-        if (!wait(mb(os.o_full[w]), (uint32_t)(d >> 1) & 1u)) break;
-        fence_after_sync();
-        const int x0 = chunk_at(d), Lc = min(kC, sg.n - x0);
-        const int E = p == 0 && d == 0 ? e0 : 1;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          float x[32], y[32];
-          tmem_ld32(tb + tl + L::O1 + 64 * w + 32 * half, x);
-          tmem_ld32(tb + tl + L::O2 + 64 * w + 32 * half, y);
-          tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int r = 32 * half + e;
-            x[e] = fmaf(x[e], pw[rev ? max(Lc - 1 - r, 0) + E : r + E], y[e]);
-          }
-          // two lanes swap halves, so that each stores two neighbouring channels of one token
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const bool odd = lane & 1;
-            const float got = __shfl_xor_sync(0xffffffffu, odd ? x[e] : x[e + 1], 1);
-            const float two = odd ? pack2(got, x[e + 1]) : pack2(x[e], got);
-            const int r = 32 * half + e + odd;
-            if (r < Lc && v < DV)
-              *reinterpret_cast<float*>(ob + (size_t)(x0 + r) * sc.H * DV + (v & ~1)) = two;
-          }
-        }
-        fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(mb(os.o_free[w]));
+      fence_smem_to_async();
+      named_bar(1, 128);
+      if (tid == 12 * 32) {
+        // rows past the tensor's end are not written
+        for (int pn = 0; pn < DV / 64; ++pn)
+          tma_store_4d(&maps.o[job], sb + L::O + pn * kC * 128, 64 * pn, h, sg.a + at, b);
+        bulk_commit();
       }
     }
+    if (tid == 12 * 32) bulk_wait_all();
   } else {
-    fewer_registers<72>();
-    if (warp == 12) {
-      // ---- issuing warp --------------------------------------------------------------------------
+    fewer_registers<56>();
+    if (warp == 16) {
+      // ---- issuing warp: G, O1, O2 ---------------------------------------------------------------
       constexpr uint32_t id_g = idesc_bf16(64, 64), id_o1 = idesc_bf16(128, 64),
-                         id_o2 = idesc_a_mn(idesc_bf16(128, 64)),
-                         id_kv = idesc_a_mn(idesc_bf16_mn(128, DK));
+                         id_o2 = idesc_a_mn(idesc_bf16(128, 64));
       for (int c = 0; c <= nch; ++c) {
-        const int s = c % 3, w = c & 1;
-        const uint32_t at = sb + s * L::STAGE;
+        const int s = c % NS, w = c & 1;
         if (c < nch) {
-          if (!wait(mb(os.full[s]), (uint32_t)(c / 3) & 1u)) break;
+          if (!wait(mb(os.full[s]), (uint32_t)(c / NS) & 1u)) break;
           // G is free once P of the chunk before has been formed
           if (c > 0 && !wait(mb(os.p_full[w ^ 1]), (uint32_t)((c - 1) >> 1) & 1u)) break;
           fence_after_sync();
+          const uint64_t qd = k_base(sb + s * L::STAGE), kd = k_base(sb + s * L::STAGE + L::KT);
 #pragma unroll
           for (int ks = 0; ks < DK / 16; ++ks)
-            mma_bf16_w(tb + L::G, kmajor(at, kC, ks), kmajor(at + L::KT, kC, ks), id_g, ks > 0);
+            mma_bf16_w(tb + L::G, qd + k_step(ks), kd + k_step(ks), id_g, ks > 0);
           mma_commit_w(mb(os.g_full));
         }
         if (c > 0) {
-          // O2 of chunk c - 1
-          const int d = c - 1, sd = d % 3, wd = d & 1;
+          // O2 of chunk c - 1 (O1, before it in the pipe, waited for the outputs' buffer)
+          const int d = c - 1, sd = d % NS, wd = d & 1;
           if (c == nch && !wait(mb(os.p_full[wd]), (uint32_t)(d >> 1) & 1u)) break;
           fence_after_sync();
+          const uint64_t vd = mn_base(sb + sd * L::STAGE + 2 * L::KT, DV == 128);
+          const uint64_t pd = k_base(sb + L::P + wd * 8192);
 #pragma unroll
           for (int ks = 0; ks < kC / 16; ++ks)
-            mma_bf16_w(tb + L::O2 + 64 * wd, v_as_a<DV>(sb + sd * L::STAGE + 2 * L::KT, ks),
-                       kmajor(sb + L::P + wd * 8192, kC, ks), id_o2, ks > 0);
-          mma_commit_w(mb(os.o_full[wd]));
+            mma_bf16_w(tb + L::O2, vd + mn_step(ks), pd + k_step(ks), id_o2, ks > 0);
+          mma_commit_w(mb(os.o_full));
           mma_commit_w(mb(os.empty[sd]));
-        }
-        if (c < nstate) {
-          // the accumulator is free once the state has taken the chunk before
-          if (!wait(mb(os.kt_full), (uint32_t)c & 1u)) break;
-          if (c > 0 && !wait(mb(os.kv_free), (uint32_t)(c - 1) & 1u)) break;
-          fence_after_sync();
-#pragma unroll
-          for (int t = 2; t >= 0; --t)
-#pragma unroll
-            for (int ks = 0; ks < kC / 16; ++ks)
-              mma_bf16_w(tb + L::KV, v_as_a<DV>(at + 2 * L::KT, ks),
-                         mnmajor(sb + L::SPLIT + t * L::KT, kC, ks), id_kv, t < 2 || ks > 0);
-          mma_commit_w(mb(os.kv_done));
         }
         if (c < nch) {
           if (!wait(mb(os.s_ready), (uint32_t)c & 1u)) break;
-          if (c >= 2 && !wait(mb(os.o_free[w]), (uint32_t)((c - 2) >> 1) & 1u)) break;
+          if (c > 0 && !wait(mb(os.o_free), (uint32_t)(c - 1) & 1u)) break;
           fence_after_sync();
+          const uint64_t qd = k_base(sb + s * L::STAGE);
 #pragma unroll
           for (int ks = 0; ks < DK / 16; ++ks)
-            mma_bf16_ta_w(tb + L::O1 + 64 * w, tb + L::SB + 8 * ks, kmajor(at, kC, ks), id_o1,
-                          ks > 0);
+            mma_bf16_ta_w(tb + L::O1, tb + L::SB + 8 * ks, qd + k_step(ks), id_o1, ks > 0);
           mma_commit_w(mb(os.o1_done));
         }
       }
       // the products issued here complete before tensor memory is freed
-      mma_commit_w(mb(os.drained));
-      mbar_wait(mb(os.drained), 0, kDrain);
-    } else if (warp == 13) {
+      mma_commit_w(mb(os.drained[0]));
+      mbar_wait(mb(os.drained[0]), 0, kDrain);
+    } else if (warp == 17) {
+      // ---- issuing warp: KV ------------------------------------------------------------------------
+      for (int c = 0; c < nch; ++c) {
+        const int s = c % NS;
+        if (c < nstate) {
+          if (!wait(mb(os.full[s]), (uint32_t)(c / NS) & 1u)) break;
+          if (!wait(mb(os.vw_full), (uint32_t)c & 1u)) break;
+          // the accumulator is free once the state has taken the chunk before
+          if (c > 0 && !wait(mb(os.kv_free), (uint32_t)(c - 1) & 1u)) break;
+          fence_after_sync();
+          issue_kv<DK>(tb + L::KV, tb + L::VW, sb + s * L::STAGE + L::KT);
+          mma_commit_w(mb(os.kv_done));
+          mma_commit_w(mb(os.empty[s]));
+        } else if (lane == 0) {
+          mbar_arrive(mb(os.empty[s]));
+        }
+      }
+      mma_commit_w(mb(os.drained[1]));
+      mbar_wait(mb(os.drained[1]), 0, kDrain);
+    } else if (warp == 18) {
       // ---- loader -----------------------------------------------------------------------------------
       int done = 0;
       for (int c = 0; c < nch; ++c) {
-        const int s = c % 3;
-        if (!wait(mb(os.empty[s]), ((uint32_t)(c / 3) & 1u) ^ 1u)) break;
+        const int s = c % NS;
+        if (!wait(mb(os.empty[s]), ((uint32_t)(c / NS) & 1u) ^ 1u)) break;
         if (lane == 0) {
           const uint32_t at = sb + s * L::STAGE;
           const int t0 = sg.a + chunk_at(c);
@@ -581,8 +695,8 @@ lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin
       }
       // copies in flight land before the CTA leaves, also when some warp gave up
       if (lane == 0)
-        for (int c = max(0, done - 3); c < done; ++c)
-          mbar_wait(mb(os.full[c % 3]), (uint32_t)(c / 3) & 1u, kDrain);
+        for (int c = max(0, done - NS); c < done; ++c)
+          mbar_wait(mb(os.full[c % NS]), (uint32_t)(c / NS) & 1u, kDrain);
     }
   }
   fence_before_sync();
@@ -596,7 +710,8 @@ cudaError_t launch_t(const LinScan& sc, cudaStream_t st) {
   for (int j = 0; j < sc.njobs; ++j)
     if (!encode_bthd_bf16(&maps.q[j], sc.job[j].q, sc.B, sc.T, sc.H, DK, 64, kC, true) ||
         !encode_bthd_bf16(&maps.k[j], sc.job[j].k, sc.B, sc.T, sc.H, DK, 64, kC, true) ||
-        !encode_bthd_bf16(&maps.v[j], sc.job[j].v, sc.B, sc.T, sc.H, DV, 64, kC, true))
+        !encode_bthd_bf16(&maps.v[j], sc.job[j].v, sc.B, sc.T, sc.H, DV, 64, kC, true) ||
+        !encode_bthd_bf16(&maps.o[j], sc.job[j].o, sc.B, sc.T, sc.H, DV, 64, kC, true))
       return cudaErrorInvalidValue;
   const uint32_t spin = attn_spin_limit();
   cudaError_t e;
@@ -605,7 +720,7 @@ cudaError_t launch_t(const LinScan& sc, cudaStream_t st) {
     constexpr int smem = SegLayout<DK, DV>::SMEM;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kern<<<dim3((unsigned)(sc.B * sc.H * (sc.nseg - 1)), sc.njobs), kLinWarps * 32, smem, st>>>(
+    kern<<<dim3((unsigned)(sc.B * sc.H * (sc.nseg - 1)), sc.njobs), kSegWarps * 32, smem, st>>>(
         maps, sc, spin);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
@@ -613,7 +728,7 @@ cudaError_t launch_t(const LinScan& sc, cudaStream_t st) {
   constexpr int smem = OutLayout<DK, DV>::SMEM;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kern<<<dim3((unsigned)(sc.B * sc.H * sc.nseg), sc.njobs), kLinWarps * 32, smem, st>>>(maps, sc,
+  kern<<<dim3((unsigned)(sc.B * sc.H * sc.nseg), sc.njobs), kOutWarps * 32, smem, st>>>(maps, sc,
                                                                                        spin);
   return cudaGetLastError();
 }
