@@ -56,29 +56,21 @@ __device__ __forceinline__ uint64_t mn_base(uint32_t tile, bool two_panels) {
 }
 __host__ __device__ constexpr uint64_t mn_step(int ks) { return (uint64_t)(ks * 2048) >> 4; }
 
-// tcgen05.ld of 16 lanes x 64 columns spread over all 32 threads: x[4 n + 2 h + e] is row
+// tcgen05.ld of 16 lanes x 16 columns spread over all 32 threads: x[4 n + 2 h + e] is row
 // lane / 4 + 8 h, column 8 n + 2 (lane % 4) + e.
-__device__ __forceinline__ void tmem_ld_16x64(uint32_t taddr, float (&v)[32]) {
+__device__ __forceinline__ void tmem_ld_16x16(uint32_t taddr, float (&v)[8]) {
   uint32_t* r = reinterpret_cast<uint32_t*>(v);
   asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-        "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
-        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
-        "=r"(r[31])
+        "=r"(r[7])
       : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
       :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
-         "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]),
-         "r"(r[13]), "r"(r[14]), "r"(r[15])
+         "r"(r[6]), "r"(r[7])
       : "memory");
 }
 
@@ -90,20 +82,22 @@ __device__ __forceinline__ void weigh_values(const unsigned char* v, uint32_t ta
   const int ch = lane_id % DV;
   const unsigned char* col = v + (ch >> 6) * kC * 128 + (ch & 7) * 2;
   const int c3 = (ch & 63) >> 3;
+  // (rolled: the roles' loop bodies run side by side, and unrolled they outgrew the instruction
+  // cache, which made every pass several times slower)
+#pragma unroll 1
+  for (int part = 0; part < 4; ++part) {
+    uint32_t out[3][8];
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    uint32_t out[3][16];
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const float4 w4 = *reinterpret_cast<const float4*>(wt + 32 * half + 4 * q);
+    for (int q = 0; q < 4; ++q) {
+      const float4 w4 = *reinterpret_cast<const float4*>(wt + 16 * part + 4 * q);
       const float w[4] = {w4.x * far, w4.y * far, w4.z * far, w4.w * far};
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int r = 32 * half + 4 * q + 2 * e;
+        const int r = 4 * q + 2 * e;
         const uint32_t x = *reinterpret_cast<const unsigned short*>(
-            col + r * 128 + ((c3 ^ (r & 7)) << 4));
+            col + part * 2048 + r * 128 + ((c3 ^ (r & 7)) << 4));
         const uint32_t y = *reinterpret_cast<const unsigned short*>(
-            col + (r + 1) * 128 + ((c3 ^ ((r + 1) & 7)) << 4));
+            col + part * 2048 + (r + 1) * 128 + ((c3 ^ ((r + 1) & 7)) << 4));
         float a = __uint_as_float(x << 16) * w[2 * e], b = __uint_as_float(y << 16) * w[2 * e + 1];
 #pragma unroll
         for (int s = 0; s < 3; ++s) {
@@ -116,7 +110,7 @@ __device__ __forceinline__ void weigh_values(const unsigned char* v, uint32_t ta
       }
     }
 #pragma unroll
-    for (int s = 0; s < 3; ++s) tmem_st16(taddr + 32 * s + 16 * half, out[s]);
+    for (int s = 0; s < 3; ++s) tmem_st8(taddr + 32 * s + 8 * part, out[s]);
   }
 }
 
@@ -313,7 +307,7 @@ lin_segment_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t 
 struct OutTables {
   RowTables rows;
   float fo[4][kC];                  // a^(i+E): [E + 2 ragged]
-  float pw[kC];                     // a^n
+  float gap[2 * kC];                // [63 + t - j]: a^|t-j| where row t sees row j, else 0
 };
 
 template <int DK, int DV>
@@ -324,7 +318,7 @@ struct OutLayout {
   static constexpr int O = P + 2 * 8192;                 // outputs on their way out
   static constexpr int TAB = O + VT;
   static constexpr int SMALL = TAB + (int)sizeof(OutTables);
-  static constexpr int SMEM = SMALL + 256 + 1024;
+  static constexpr int SMEM = SMALL + 256;      // no room to pad to 1024 bytes by hand
   static_assert(SMEM <= 232448, "shared memory");
   // tensor memory
   static constexpr uint32_t KV = 0;                      // DK columns
@@ -348,8 +342,11 @@ __global__ void __launch_bounds__(kOutWarps * 32, 1)
 lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin) {
   using L = OutLayout<DK, DV>;
   constexpr int NS = L::STAGES;
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  extern __shared__ __align__(1024) unsigned char sm[];
+  if ((smem_u32(sm) & 1023u) != 0) {       // the tiles' swizzle needs it
+    if (threadIdx.x == 0) atomicOr(sc.status, 1u);
+    return;
+  }
   OutSmall& os = *reinterpret_cast<OutSmall*>(sm + L::SMALL);
   OutTables& tab = *reinterpret_cast<OutTables*>(sm + L::TAB);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -390,8 +387,9 @@ lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin
     } else if (x < 6) {
       const int Lc = x >= 4 ? ragged : kC;
       tab.fo[x - 2][r] = (float)decay_pow(l2, (rev ? max(Lc - 1 - r, 0) : r) + (x & 1));
-    } else if (x == 6) {
-      tab.pw[r] = (float)decay_pow(l2, r);
+    } else if (x < 8) {
+      const int g = (tid - 6 * kC) - (kC - 1);     // t - j
+      tab.gap[tid - 6 * kC] = (rev ? g <= 0 : g >= 0) ? (float)decay_pow(l2, rev ? -g : g) : 0.f;
     }
   }
   if (warp == 0) tmem_alloc(&os.tmem, 512);
@@ -478,6 +476,7 @@ lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin
         fl = (float)(f - (double)fh);
         steps = now;
       }
+      const float2 fh2 = make_float2(fh, fh), fl2 = make_float2(fl, fl);
       if (!(ok = wait(mb(os.kv_done), (uint32_t)c & 1u))) break;
       fence_after_sync();
 #pragma unroll
@@ -491,8 +490,12 @@ lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin
           if (lane == 0) mbar_arrive(mb(os.kv_free));
         }
 #pragma unroll
-        for (int e = 0; e < 32; ++e)
-          S[32 * q + e] = fmaf(fh, S[32 * q + e], fmaf(fl, S[32 * q + e], x[e]));
+        for (int e = 0; e < 32; e += 2) {
+          const float2 u = make_float2(S[32 * q + e], S[32 * q + e + 1]);
+          const float2 y = fma2(fh2, u, fma2(fl2, u, make_float2(x[e], x[e + 1])));
+          S[32 * q + e] = y.x;
+          S[32 * q + e + 1] = y.y;
+        }
       }
     }
     if (s_out && ok && v < DV) {
@@ -528,25 +531,23 @@ lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin
     for (int c = 0; c < nch; ++c) {
       if (!wait(mb(os.g_full), (uint32_t)c & 1u)) break;
       fence_after_sync();
-      float x[32];
-      tmem_ld_16x64(tb + tl + L::G, x);
-      tmem_wait_ld();
       // P's buffer was last read by O2 of chunk c - 2, which came before this G
-      unsigned char* pt = sm + L::P + (c & 1) * 8192;
+      unsigned char* pt = sm + L::P + (c & 1) * 8192 + t0 * 128;
+#pragma unroll 1
+      for (int part = 0; part < 4; ++part) {
+        float x[8];
+        tmem_ld_16x16(tb + tl + L::G + 16 * part, x);
+        tmem_wait_ld();
+        const float* g = tab.gap + kC - 1 + t0 - 16 * part - j0;
 #pragma unroll
-      for (int n = 0; n < 8; ++n)
+        for (int n = 0; n < 2; ++n)
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          const int t = t0 + 8 * hf;
-          float y[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int j = 8 * n + j0 + e, gap = rev ? j - t : t - j;
-            y[e] = gap >= 0 ? x[4 * n + 2 * hf + e] * tab.pw[max(gap, 0)] : 0.f;
-          }
-          *reinterpret_cast<float*>(pt + t * 128 + ((n ^ (t & 7)) << 4) + 2 * j0) =
-              pack2(y[0], y[1]);
-        }
+          for (int hf = 0; hf < 2; ++hf)
+            *reinterpret_cast<float*>(pt + 8 * hf * 128 +
+                                      (((2 * part + n) ^ (t0 & 7)) << 4) + 2 * j0) =
+                pack2(x[4 * n + 2 * hf] * g[8 * hf - 8 * n],
+                      x[4 * n + 2 * hf + 1] * g[8 * hf - 8 * n - 1]);
+      }
       fence_smem_to_async();
       fence_before_sync();
       __syncwarp();
@@ -569,35 +570,34 @@ lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin
       fence_after_sync();
       const int at = chunk_at(c);
       const float* fo = tab.fo[(p == 0 && c == 0 ? e0 : 1) + (sg.n - at < kC ? 2 : 0)];
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        float x[32], y[32];
-        tmem_ld32(tb + tl + L::O1 + 32 * half, x);
-        tmem_ld32(tb + tl + L::O2 + 32 * half, y);
+#pragma unroll 1
+      for (int part = 0; part < 4; ++part) {
+        float x[16], y[16];
+        tmem_ld16(tb + tl + L::O1 + 16 * part, x);
+        tmem_ld16(tb + tl + L::O2 + 16 * part, y);
         tmem_wait_ld();
-        if (half == 1) {
-          fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(mb(os.o_free));
-        }
 #pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(fo + 32 * half + e);
+        for (int e = 0; e < 16; e += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(fo + 16 * part + e);
           x[e] = fmaf(x[e], f.x, y[e]);
           x[e + 1] = fmaf(x[e + 1], f.y, y[e + 1]);
           x[e + 2] = fmaf(x[e + 2], f.z, y[e + 2]);
           x[e + 3] = fmaf(x[e + 3], f.w, y[e + 3]);
         }
         // two lanes swap, so that each writes two neighbouring channels of one token
+        if (v < DV) {
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          const float got = __shfl_xor_sync(0xffffffffu, odd ? x[e] : x[e + 1], 1);
-          const float two = odd ? pack2(got, x[e + 1]) : pack2(x[e], got);
-          const int r = 32 * half + e + odd;
-          if (v < DV)
-            *reinterpret_cast<float*>(so + r * 128 + ((c3 ^ ((e + odd) & 7)) << 4)) = two;
+          for (int e = 0; e < 16; e += 2) {
+            const float got = __shfl_xor_sync(0xffffffffu, odd ? x[e] : x[e + 1], 1);
+            const float two = odd ? pack2(got, x[e + 1]) : pack2(x[e], got);
+            *reinterpret_cast<float*>(so + part * 2048 + (e + odd) * 128 +
+                                      ((c3 ^ ((e + odd) & 7)) << 4)) = two;
+          }
         }
       }
+      fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(mb(os.o_free));
       fence_smem_to_async();
       named_bar(1, 128);
       if (tid == 12 * 32) {
