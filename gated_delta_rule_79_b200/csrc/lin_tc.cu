@@ -24,8 +24,8 @@
 // operands at the full 128 bytes a cycle.  So V~^T and S are A operands from tensor memory, K is
 // read as TMA left it, and nothing but P and the outputs is written (with decayed keys as three
 // tiles in shared memory a chunk took 7600 cycles).  Passes run beside each other: warps 0-3
-// the state, 4-7 V~, 8-11 P, 12-15 the outputs, 16 and 17 issue (16 G, O1, O2; 17 KV, which waits
-// for none of them), 18 loads up to four chunks ahead.
+// the state, 4-11 V~, 12-15 P, 16-19 the outputs, 20 and 21 issue (20 G, O1, O2; 21 KV, which
+// waits for none of them), 22 loads up to four chunks ahead.
 //
 // Waits are bounded: a give-up sets the status word, drains what is in flight and ends the CTA.
 
@@ -74,18 +74,20 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
       : "memory");
 }
 
-// V~^T of one chunk into tensor memory by four warps: thread = value channel (TMEM lane), two
-// tokens to a column, the three bf16 terms 32 columns apart.  wt: the rows' weights, times far.
+// V~^T of tokens 16 p0 .. 16 p1 - 1 of a chunk into tensor memory by four warps: thread = value
+// channel (TMEM lane), two tokens to a column, the three bf16 terms 32 columns apart.  The terms
+// are cut off rather than rounded, which leaves 16, 8 and 0 of a float's 24 bits: their sum is
+// the float.  wt: the rows' weights, times far.
 template <int DV>
 __device__ __forceinline__ void weigh_values(const unsigned char* v, uint32_t taddr, int lane_id,
-                                             const float* wt, float far) {
+                                             const float* wt, float far, int p0, int p1) {
   const int ch = lane_id % DV;
   const unsigned char* col = v + (ch >> 6) * kC * 128 + (ch & 7) * 2;
   const int c3 = (ch & 63) >> 3;
   // (rolled: the roles' loop bodies run side by side, and unrolled they outgrew the instruction
   // cache, which made every pass several times slower)
 #pragma unroll 1
-  for (int part = 0; part < 4; ++part) {
+  for (int part = p0; part < p1; ++part) {
     uint32_t out[3][8];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -101,11 +103,10 @@ __device__ __forceinline__ void weigh_values(const unsigned char* v, uint32_t ta
         float a = __uint_as_float(x << 16) * w[2 * e], b = __uint_as_float(y << 16) * w[2 * e + 1];
 #pragma unroll
         for (int s = 0; s < 3; ++s) {
-          const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
-          const uint32_t u = *reinterpret_cast<const uint32_t*>(&p);
-          out[s][2 * q + e] = u;
-          a -= __uint_as_float(u << 16);
-          b -= __uint_as_float(u & 0xffff0000u);
+          const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
+          out[s][2 * q + e] = __byte_perm(ua, ub, 0x7632);
+          a -= __uint_as_float(ua & 0xffff0000u);
+          b -= __uint_as_float(ub & 0xffff0000u);
         }
       }
     }
@@ -249,7 +250,7 @@ lin_segment_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t 
       if (c >= 2 && !wait(mb(ss.kv_done[w]), (uint32_t)((c - 2) >> 1) & 1u)) break;
       fence_after_sync();
       weigh_values<DV>(sm + s * L::STAGE + L::KT, tb + tl + L::VW + 96 * w,
-                       (warp & 3) * 32 + lane, tab.wt[sg.n - c * kC < kC], ss.far[s]);
+                       (warp & 3) * 32 + lane, tab.wt[sg.n - c * kC < kC], ss.far[s], 0, 4);
       tmem_wait_st();
       fence_before_sync();
       __syncwarp();
@@ -334,8 +335,8 @@ struct OutSmall {
   uint32_t tmem;
   int abort;
 };
-// five warpgroups: 640 threads of 96 registers at launch, then 192 + 80 + 72 + 80 + 56
-constexpr int kOutWarps = 20;
+// six warpgroups: 768 threads of 80 registers at launch, then 192 + 2 x 56 + 56 + 72 + 48
+constexpr int kOutWarps = 24;
 
 template <int DK, int DV>
 __global__ void __launch_bounds__(kOutWarps * 32, 1)
@@ -369,7 +370,7 @@ lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin
       mbar_init(mb(os.drained[s]), 1);
     }
     mbar_init(mb(os.g_full), 1);
-    mbar_init(mb(os.vw_full), 4);
+    mbar_init(mb(os.vw_full), 8);
     mbar_init(mb(os.kv_done), 1);
     mbar_init(mb(os.kv_free), 4);
     mbar_init(mb(os.s_ready), 4);
@@ -381,7 +382,7 @@ lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin
   }
   {
     const int ragged = sg.n - (nch - 1) * kC;
-    const int r = tid % kC, x = tid / kC;          // ten rows of 64 threads
+    const int r = tid % kC, x = tid / kC;          // twelve rows of 64 threads
     if (x < 2) {
       tab.rows.wt[x][r] = row_weight(l2, rev, x ? ragged : kC, r);
     } else if (x < 6) {
@@ -506,8 +507,8 @@ lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin
         reinterpret_cast<float4*>(dst)[e] = make_float4(f * S[4 * e], f * S[4 * e + 1],
                                                         f * S[4 * e + 2], f * S[4 * e + 3]);
     }
-  } else if (warp < 8) {
-    fewer_registers<80>();
+  } else if (warp < 12) {
+    fewer_registers<56>();
     // ---- V~ ----------------------------------------------------------------------------------
     const uint32_t tl = (uint32_t)((warp & 3) * 32) << 16;
     for (int c = 0; c < nstate; ++c) {
@@ -516,14 +517,15 @@ lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin
       if (c > 0 && !wait(mb(os.kv_done), (uint32_t)(c - 1) & 1u)) break;
       fence_after_sync();
       weigh_values<DV>(sm + s * L::STAGE + 2 * L::KT, tb + tl + L::VW, (warp & 3) * 32 + lane,
-                       tab.rows.wt[sg.n - chunk_at(c) < kC], 1.f);
+                       tab.rows.wt[sg.n - chunk_at(c) < kC], 1.f, warp < 8 ? 0 : 2,
+                       warp < 8 ? 2 : 4);
       tmem_wait_st();
       fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(mb(os.vw_full));
     }
-  } else if (warp < 12) {
-    fewer_registers<72>();
+  } else if (warp < 16) {
+    fewer_registers<56>();
     // ---- P -------------------------------------------------------------------------------------
     // an M = 64 accumulator: row t in lane 32 (t / 16) + t % 16
     const int t0 = 16 * (warp & 3) + (lane >> 2), j0 = 2 * (lane & 3);
@@ -531,7 +533,7 @@ lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin
     for (int c = 0; c < nch; ++c) {
       if (!wait(mb(os.g_full), (uint32_t)c & 1u)) break;
       fence_after_sync();
-      // P's buffer was last read by O2 of chunk c - 2, which came before this G
+      // P's buffer was last read by O2 of chunk c - 2, which came before this G in the pipe
       unsigned char* pt = sm + L::P + (c & 1) * 8192 + t0 * 128;
 #pragma unroll 1
       for (int part = 0; part < 4; ++part) {
@@ -553,8 +555,8 @@ lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin
       __syncwarp();
       if (lane == 0) mbar_arrive(mb(os.p_full[c & 1]));
     }
-  } else if (warp < 16) {
-    fewer_registers<80>();
+  } else if (warp < 20) {
+    fewer_registers<72>();
     // ---- the outputs: thread = value channel ------------------------------------------------
     const int v = (warp & 3) * 32 + lane;
     const uint32_t tl = (uint32_t)((warp & 3) * 32) << 16;
@@ -565,7 +567,7 @@ lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin
     for (int c = 0; c < nch; ++c) {
       ok = wait(mb(os.o_full), (uint32_t)c & 1u);
       // the last store has read its tile
-      if (tid == 12 * 32) bulk_wait_read_all();
+      if (tid == 16 * 32) bulk_wait_read_all();
       if (named_bar_or(1, 128, !ok)) break;
       fence_after_sync();
       const int at = chunk_at(c);
@@ -600,61 +602,58 @@ lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin
       if (lane == 0) mbar_arrive(mb(os.o_free));
       fence_smem_to_async();
       named_bar(1, 128);
-      if (tid == 12 * 32) {
+      if (tid == 16 * 32) {
         // rows past the tensor's end are not written
         for (int pn = 0; pn < DV / 64; ++pn)
           tma_store_4d(&maps.o[job], sb + L::O + pn * kC * 128, 64 * pn, h, sg.a + at, b);
         bulk_commit();
       }
     }
-    if (tid == 12 * 32) bulk_wait_all();
+    if (tid == 16 * 32) bulk_wait_all();
   } else {
-    fewer_registers<56>();
-    if (warp == 16) {
+    fewer_registers<48>();
+    if (warp == 20) {
       // ---- issuing warp: G, O1, O2 ---------------------------------------------------------------
       constexpr uint32_t id_g = idesc_bf16(64, 64), id_o1 = idesc_bf16(128, 64),
                          id_o2 = idesc_a_mn(idesc_bf16(128, 64));
-      for (int c = 0; c <= nch; ++c) {
-        const int s = c % NS, w = c & 1;
-        if (c < nch) {
-          if (!wait(mb(os.full[s]), (uint32_t)(c / NS) & 1u)) break;
-          // G is free once P of the chunk before has been formed
-          if (c > 0 && !wait(mb(os.p_full[w ^ 1]), (uint32_t)((c - 1) >> 1) & 1u)) break;
-          fence_after_sync();
-          const uint64_t qd = k_base(sb + s * L::STAGE), kd = k_base(sb + s * L::STAGE + L::KT);
+      auto issue_g = [&](int c) -> bool {
+        const uint32_t at = sb + (c % NS) * L::STAGE;
+        if (!wait(mb(os.full[c % NS]), (uint32_t)(c / NS) & 1u)) return false;
+        fence_after_sync();
+        const uint64_t qd = k_base(at), kd = k_base(at + L::KT);
 #pragma unroll
-          for (int ks = 0; ks < DK / 16; ++ks)
-            mma_bf16_w(tb + L::G, qd + k_step(ks), kd + k_step(ks), id_g, ks > 0);
-          mma_commit_w(mb(os.g_full));
-        }
-        if (c > 0) {
-          // O2 of chunk c - 1 (O1, before it in the pipe, waited for the outputs' buffer)
-          const int d = c - 1, sd = d % NS, wd = d & 1;
-          if (c == nch && !wait(mb(os.p_full[wd]), (uint32_t)(d >> 1) & 1u)) break;
-          fence_after_sync();
-          const uint64_t vd = mn_base(sb + sd * L::STAGE + 2 * L::KT, DV == 128);
-          const uint64_t pd = k_base(sb + L::P + wd * 8192);
+        for (int ks = 0; ks < DK / 16; ++ks)
+          mma_bf16_w(tb + L::G, qd + k_step(ks), kd + k_step(ks), id_g, ks > 0);
+        mma_commit_w(mb(os.g_full));
+        return true;
+      };
+      bool ok = issue_g(0);
+      for (int c = 0; c < nch && ok; ++c) {
+        const uint32_t at = sb + (c % NS) * L::STAGE;
+        const int w = c & 1;
+        // P of this chunk has been formed, so G is free for the next one
+        if (!wait(mb(os.p_full[w]), (uint32_t)(c >> 1) & 1u)) break;
+        if (c + 1 < nch && !issue_g(c + 1)) break;
+        if (c > 0 && !wait(mb(os.o_free), (uint32_t)(c - 1) & 1u)) break;
+        fence_after_sync();
+        const uint64_t vd = mn_base(at + 2 * L::KT, DV == 128), pd = k_base(sb + L::P + w * 8192);
 #pragma unroll
-          for (int ks = 0; ks < kC / 16; ++ks)
-            mma_bf16_w(tb + L::O2, vd + mn_step(ks), pd + k_step(ks), id_o2, ks > 0);
-          mma_commit_w(mb(os.o_full));
-          mma_commit_w(mb(os.empty[sd]));
-        }
-        if (c < nch) {
-          if (!wait(mb(os.s_ready), (uint32_t)c & 1u)) break;
-          if (c > 0 && !wait(mb(os.o_free), (uint32_t)(c - 1) & 1u)) break;
-          fence_after_sync();
-          const uint64_t qd = k_base(sb + s * L::STAGE);
+        for (int ks = 0; ks < kC / 16; ++ks)
+          mma_bf16_w(tb + L::O2, vd + mn_step(ks), pd + k_step(ks), id_o2, ks > 0);
+        if (!wait(mb(os.s_ready), (uint32_t)c & 1u)) break;
+        fence_after_sync();
+        const uint64_t qd = k_base(at);
 #pragma unroll
-          for (int ks = 0; ks < DK / 16; ++ks)
-            mma_bf16_ta_w(tb + L::O1, tb + L::SB + 8 * ks, qd + k_step(ks), id_o1, ks > 0);
-          mma_commit_w(mb(os.o1_done));
-        }
+        for (int ks = 0; ks < DK / 16; ++ks)
+          mma_bf16_ta_w(tb + L::O1, tb + L::SB + 8 * ks, qd + k_step(ks), id_o1, ks > 0);
+        mma_commit_w(mb(os.o1_done));
+        mma_commit_w(mb(os.o_full));
+        mma_commit_w(mb(os.empty[c % NS]));
       }
       // the products issued here complete before tensor memory is freed
       mma_commit_w(mb(os.drained[0]));
       mbar_wait(mb(os.drained[0]), 0, kDrain);
-    } else if (warp == 17) {
+    } else if (warp == 21) {
       // ---- issuing warp: KV ------------------------------------------------------------------------
       for (int c = 0; c < nch; ++c) {
         const int s = c % NS;
@@ -673,7 +672,7 @@ lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin
       }
       mma_commit_w(mb(os.drained[1]));
       mbar_wait(mb(os.drained[1]), 0, kDrain);
-    } else if (warp == 18) {
+    } else if (warp == 22) {
       // ---- loader -----------------------------------------------------------------------------------
       int done = 0;
       for (int c = 0; c < nch; ++c) {
