@@ -56,8 +56,12 @@ __device__ __forceinline__ uint64_t mn_base(uint32_t tile, bool two_panels) {
 }
 __host__ __device__ constexpr uint64_t mn_step(int ks) { return (uint64_t)(ks * 2048) >> 4; }
 
-// tcgen05.ld of 16 lanes x 16 columns spread over all 32 threads: x[4 n + 2 h + e] is row
-// lane / 4 + 8 h, column 8 n + 2 (lane % 4) + e.
+// The passes move data between shared and tensor memory in 8 x 8 matrices, a thread holding two
+// neighbouring columns of row lane / 4 (ldmatrix, stmatrix, and the 16-lane shapes of tcgen05.ld
+// and .st all agree on it), which transposes without shuffles.
+//
+// tcgen05.ld of 16 lanes x 16 columns of fp32: x[4 n + 2 h + e] is row lane / 4 + 8 h, column
+// 8 n + 2 (lane % 4) + e.
 __device__ __forceinline__ void tmem_ld_16x16(uint32_t taddr, float (&v)[8]) {
   uint32_t* r = reinterpret_cast<uint32_t*>(v);
   asm volatile(
@@ -66,53 +70,81 @@ __device__ __forceinline__ void tmem_ld_16x16(uint32_t taddr, float (&v)[8]) {
         "=r"(r[7])
       : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
-      :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
-         "r"(r[6]), "r"(r[7])
-      : "memory");
+// tcgen05.st of 16 lanes x 8 columns: r[2 n + h] to row lane / 4 + 8 h, column 4 n + lane % 4.
+__device__ __forceinline__ void tmem_st_16x8(uint32_t taddr, const uint32_t (&r)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};"
+               :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void stsm4(uint32_t addr, const float (&r)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};"
+               :: "r"(addr), "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]) : "memory");
+}
+__device__ __forceinline__ void stsm4_t(uint32_t addr, const float (&r)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};"
+               :: "r"(addr), "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]) : "memory");
 }
 
-// V~^T of tokens 16 p0 .. 16 p1 - 1 of a chunk into tensor memory by four warps: thread = value
-// channel (TMEM lane), two tokens to a column, the three bf16 terms 32 columns apart.  The terms
-// are cut off rather than rounded, which leaves 16, 8 and 0 of a float's 24 bits: their sum is
-// the float.  wt: the rows' weights, times far.
+// Where this thread's matrix row of a [64 tokens][DV channels] tile lies, for ldmatrix and
+// stmatrix over 16 tokens x 16 channels (matrix i = lane / 8: tokens 8 (i / 2) .., channels
+// 8 (i % 2) ..): the first 16 of the warp's 32 channels, and the second 16.
 template <int DV>
-__device__ __forceinline__ void weigh_values(const unsigned char* v, uint32_t taddr, int lane_id,
-                                             const float* wt, float far, int p0, int p1) {
-  const int ch = lane_id % DV;
-  const unsigned char* col = v + (ch >> 6) * kC * 128 + (ch & 7) * 2;
-  const int c3 = (ch & 63) >> 3;
-  // (rolled: the roles' loop bodies run side by side, and unrolled they outgrew the instruction
-  // cache, which made every pass several times slower)
-#pragma unroll 1
-  for (int part = p0; part < p1; ++part) {
-    uint32_t out[3][8];
+struct TileRow {
+  uint32_t at[2];
+  __device__ __forceinline__ TileRow(uint32_t tile, int warp, int lane) {
+    const int ch = (warp & 3) * 32 % DV, i = lane >> 3, tok = (i >> 1) * 8 + (lane & 7);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const float4 w4 = *reinterpret_cast<const float4*>(wt + 16 * part + 4 * q);
-      const float w[4] = {w4.x * far, w4.y * far, w4.z * far, w4.w * far};
+    for (int hh = 0; hh < 2; ++hh)
+      at[hh] = tile + (uint32_t)((ch >> 6) * kC * 128 + tok * 128 +
+                                 (((((ch & 63) >> 3) + 2 * hh + (i & 1)) ^ (lane & 7)) << 4));
+  }
+};
+
+// The weights of this thread's tokens 16 part + 8 n + 2 (lane % 4) + {0, 1}, for four parts.
+struct TokenWeights {
+  float2 w[8];
+  __device__ __forceinline__ void load(const float* wt, int lane) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = 4 * q + 2 * e;
-        const uint32_t x = *reinterpret_cast<const unsigned short*>(
-            col + part * 2048 + r * 128 + ((c3 ^ (r & 7)) << 4));
-        const uint32_t y = *reinterpret_cast<const unsigned short*>(
-            col + part * 2048 + (r + 1) * 128 + ((c3 ^ ((r + 1) & 7)) << 4));
-        float a = __uint_as_float(x << 16) * w[2 * e], b = __uint_as_float(y << 16) * w[2 * e + 1];
+    for (int m = 0; m < 8; ++m)
+      w[m] = *reinterpret_cast<const float2*>(wt + 8 * m + 2 * (lane & 3));
+  }
+};
+
+// V~^T of parts p0 .. p0 + NP - 1 (16 tokens each) of a chunk into tensor memory by four warps:
+// value channels in the lanes, two tokens to a column, the three bf16 terms 32 columns apart.
+// The terms are cut off rather than rounded, which leaves 16, 8 and 0 of a float's 24 bits:
+// their sum is the float.
+template <int NP>
+__device__ __forceinline__ void weigh_values(const uint32_t (&row)[2], uint32_t taddr,
+                                             const TokenWeights& tw, int p0, float far) {
+  const float2 far2 = make_float2(far, far), minus = make_float2(-1.f, -1.f);
+#pragma unroll
+  for (int p = 0; p < NP; ++p)
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh) {
+      uint32_t x[4], out[3][4];
+      ldsm4_t(row[hh] + (uint32_t)(p0 + p) * 2048, x);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 w = mul2(tw.w[2 * p + (i >> 1)], far2);
+        float2 a = mul2(make_float2(__uint_as_float(x[i] << 16),
+                                    __uint_as_float(x[i] & 0xffff0000u)), w);
 #pragma unroll
         for (int s = 0; s < 3; ++s) {
-          const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
-          out[s][2 * q + e] = __byte_perm(ua, ub, 0x7632);
-          a -= __uint_as_float(ua & 0xffff0000u);
-          b -= __uint_as_float(ub & 0xffff0000u);
+          const uint32_t ua = __float_as_uint(a.x), ub = __float_as_uint(a.y);
+          out[s][i] = __byte_perm(ua, ub, 0x7632);
+          if (s < 2)
+            a = fma2(make_float2(__uint_as_float(ua & 0xffff0000u),
+                                 __uint_as_float(ub & 0xffff0000u)), minus, a);
         }
       }
-    }
 #pragma unroll
-    for (int s = 0; s < 3; ++s) tmem_st8(taddr + 32 * s + 8 * part, out[s]);
-  }
+      for (int s = 0; s < 3; ++s)
+        tmem_st_16x8(taddr + ((uint32_t)(16 * hh) << 16) + 32 * s + 8 * (p0 + p), out[s]);
+    }
 }
 
 // KV = V~^T K: twelve products, the smallest terms first (A in tensor memory, B the K tile).
@@ -243,14 +275,17 @@ lin_segment_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t 
     // ---- V~ ----------------------------------------------------------------------------------
     const int w = warp < 8 ? 0 : 1;
     const uint32_t tl = (uint32_t)((warp & 3) * 32) << 16;
+    TokenWeights tw;
+    tw.load(tab.wt[0], lane);
     for (int c = w; c < nch; c += 2) {
       const int s = c % NS;
+      if (sg.n - c * kC < kC) tw.load(tab.wt[1], lane);      // the last chunk
       if (!wait(mb(ss.full[s]), (uint32_t)(c / NS) & 1u)) break;
       // the product of chunk c - 2 has read this buffer
       if (c >= 2 && !wait(mb(ss.kv_done[w]), (uint32_t)((c - 2) >> 1) & 1u)) break;
       fence_after_sync();
-      weigh_values<DV>(sm + s * L::STAGE + L::KT, tb + tl + L::VW + 96 * w,
-                       (warp & 3) * 32 + lane, tab.wt[sg.n - c * kC < kC], ss.far[s], 0, 4);
+      const TileRow<DV> row(sb + s * L::STAGE + L::KT, warp, lane);
+      weigh_values<4>(row.at, tb + tl + L::VW + 96 * w, tw, 0, ss.far[s]);
       tmem_wait_st();
       fence_before_sync();
       __syncwarp();
@@ -510,15 +545,20 @@ lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin
   } else if (warp < 12) {
     fewer_registers<56>();
     // ---- V~ ----------------------------------------------------------------------------------
+    // (two warps to 32 channels, 32 tokens each)
     const uint32_t tl = (uint32_t)((warp & 3) * 32) << 16;
+    const int p0 = warp < 8 ? 0 : 2;
+    TokenWeights tw;
     for (int c = 0; c < nstate; ++c) {
       const int s = c % NS;
+      // in the scan's order the ragged chunk comes last, or first and the others after it
+      const int ragged = sg.n - chunk_at(c) < kC;
+      if (c == 0 || ragged || (rev && c == 1)) tw.load(tab.rows.wt[ragged] + 16 * p0, lane);
       if (!wait(mb(os.full[s]), (uint32_t)(c / NS) & 1u)) break;
       if (c > 0 && !wait(mb(os.kv_done), (uint32_t)(c - 1) & 1u)) break;
       fence_after_sync();
-      weigh_values<DV>(sm + s * L::STAGE + 2 * L::KT, tb + tl + L::VW, (warp & 3) * 32 + lane,
-                       tab.rows.wt[sg.n - chunk_at(c) < kC], 1.f, warp < 8 ? 0 : 2,
-                       warp < 8 ? 2 : 4);
+      const TileRow<DV> row(sb + s * L::STAGE + 2 * L::KT, warp, lane);
+      weigh_values<2>(row.at, tb + tl + L::VW, tw, p0, 1.f);
       tmem_wait_st();
       fence_before_sync();
       __syncwarp();
@@ -527,28 +567,36 @@ lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin
   } else if (warp < 16) {
     fewer_registers<56>();
     // ---- P -------------------------------------------------------------------------------------
-    // an M = 64 accumulator: row t in lane 32 (t / 16) + t % 16
+    // an M = 64 accumulator: row t in lane 32 (t / 16) + t % 16.  This thread's elements and
+    // their decays are the same in every chunk
     const int t0 = 16 * (warp & 3) + (lane >> 2), j0 = 2 * (lane & 3);
     const uint32_t tl = (uint32_t)((warp & 3) * 32) << 16;
+    float2 g[16];
+#pragma unroll
+    for (int n = 0; n < 8; ++n)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const float* at = tab.gap + kC - 1 + t0 + 8 * hf - 8 * n - j0;
+        g[2 * n + hf] = make_float2(at[0], at[-1]);
+      }
+    // matrix i = lane / 8: columns 8 (i / 2) .., rows 8 (i % 2) ..
+    const int tr = 16 * (warp & 3) + (lane & 8) + (lane & 7), n0 = lane >> 4;
     for (int c = 0; c < nch; ++c) {
       if (!wait(mb(os.g_full), (uint32_t)c & 1u)) break;
       fence_after_sync();
       // P's buffer was last read by O2 of chunk c - 2, which came before this G in the pipe
-      unsigned char* pt = sm + L::P + (c & 1) * 8192 + t0 * 128;
-#pragma unroll 1
+      const uint32_t pt = sb + L::P + (c & 1) * 8192 + tr * 128;
+#pragma unroll
       for (int part = 0; part < 4; ++part) {
-        float x[8];
+        float x[8], y[4];
         tmem_ld_16x16(tb + tl + L::G + 16 * part, x);
         tmem_wait_ld();
-        const float* g = tab.gap + kC - 1 + t0 - 16 * part - j0;
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf)
-            *reinterpret_cast<float*>(pt + 8 * hf * 128 +
-                                      (((2 * part + n) ^ (t0 & 7)) << 4) + 2 * j0) =
-                pack2(x[4 * n + 2 * hf] * g[8 * hf - 8 * n],
-                      x[4 * n + 2 * hf + 1] * g[8 * hf - 8 * n - 1]);
+        for (int i = 0; i < 4; ++i) {
+          const float2 z = mul2(make_float2(x[2 * i], x[2 * i + 1]), g[4 * part + i]);
+          y[i] = pack2(z.x, z.y);
+        }
+        stsm4(pt + (((2 * part + n0) ^ (tr & 7)) << 4), y);
       }
       fence_smem_to_async();
       fence_before_sync();
@@ -557,12 +605,10 @@ lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin
     }
   } else if (warp < 20) {
     fewer_registers<72>();
-    // ---- the outputs: thread = value channel ------------------------------------------------
-    const int v = (warp & 3) * 32 + lane;
+    // ---- the outputs -----------------------------------------------------------------------
     const uint32_t tl = (uint32_t)((warp & 3) * 32) << 16;
-    const bool odd = lane & 1;
-    unsigned char* so = sm + L::O + (v >> 6) * kC * 128 + (v & 6) * 2;
-    const int c3 = (v & 63) >> 3;
+    const TileRow<DV> row(sb + L::O, warp, lane);
+    const bool mine = (warp & 3) * 32 < DV;
     bool ok = true;
     for (int c = 0; c < nch; ++c) {
       ok = wait(mb(os.o_full), (uint32_t)c & 1u);
@@ -572,29 +618,24 @@ lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin
       fence_after_sync();
       const int at = chunk_at(c);
       const float* fo = tab.fo[(p == 0 && c == 0 ? e0 : 1) + (sg.n - at < kC ? 2 : 0)];
-#pragma unroll 1
+#pragma unroll
       for (int part = 0; part < 4; ++part) {
-        float x[16], y[16];
-        tmem_ld16(tb + tl + L::O1 + 16 * part, x);
-        tmem_ld16(tb + tl + L::O2 + 16 * part, y);
-        tmem_wait_ld();
+        const float2 f0 = *reinterpret_cast<const float2*>(fo + 16 * part + 2 * (lane & 3));
+        const float2 f1 = *reinterpret_cast<const float2*>(fo + 16 * part + 8 + 2 * (lane & 3));
 #pragma unroll
-        for (int e = 0; e < 16; e += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(fo + 16 * part + e);
-          x[e] = fmaf(x[e], f.x, y[e]);
-          x[e + 1] = fmaf(x[e + 1], f.y, y[e + 1]);
-          x[e + 2] = fmaf(x[e + 2], f.z, y[e + 2]);
-          x[e + 3] = fmaf(x[e + 3], f.w, y[e + 3]);
-        }
-        // two lanes swap, so that each writes two neighbouring channels of one token
-        if (v < DV) {
+        for (int hh = 0; hh < 2; ++hh) {
+          float x[8], y[8], z[4];
+          const uint32_t at = tb + tl + ((uint32_t)(16 * hh) << 16) + 16 * part;
+          tmem_ld_16x16(at + L::O1, x);
+          tmem_ld_16x16(at + L::O2, y);
+          tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            const float got = __shfl_xor_sync(0xffffffffu, odd ? x[e] : x[e + 1], 1);
-            const float two = odd ? pack2(got, x[e + 1]) : pack2(x[e], got);
-            *reinterpret_cast<float*>(so + part * 2048 + (e + odd) * 128 +
-                                      ((c3 ^ ((e + odd) & 7)) << 4)) = two;
+          for (int i = 0; i < 4; ++i) {
+            const float2 u = fma2(make_float2(x[2 * i], x[2 * i + 1]), i < 2 ? f0 : f1,
+                                  make_float2(y[2 * i], y[2 * i + 1]));
+            z[i] = pack2(u.x, u.y);
           }
+          if (mine) stsm4_t(row.at[hh] + part * 2048, z);
         }
       }
       fence_before_sync();
