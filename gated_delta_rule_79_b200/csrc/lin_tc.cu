@@ -3,8 +3,8 @@
 // segments are in lin_common.cuh.
 //
 // Chunks of 64 tokens.  Everything that meets the state runs transposed, value rows in the 128
-// TMEM lanes (d_v = 64 uses its one panel twice and ignores the upper lanes); a thread of warps
-// 0-3 holds a row of the fp32 state in registers:
+// TMEM lanes (d_v = 64 uses its one panel twice and ignores the upper lanes); two threads hold a
+// row of the fp32 state in registers:
 //
 //     G  = Q K^T                        (64 x 64, bf16 operands as they are: exact products)
 //     P  = G (.) a^(i_t - i_j), lower   (bf16)
@@ -13,7 +13,8 @@
 //     S  = a^(L-1+E) S + KV
 //
 // A bf16 product with decayed values would carry a rounding of 2^-9 into the fp32 state, so V~
-// enters as a sum of three bf16 terms (24 bits) whose products are exact, the smallest first.
+// enters as a sum of three bf16 terms (24 bits) whose products are exact, the smallest first
+// (of each half chunk).
 // KV is a new accumulator for every chunk, added to S by an fp32 fma: the tensor cores truncate
 // what they accumulate, and a state kept there lost 2e-7 of itself with each chunk of its memory
 // (measured: 7e-6 after 4096 tokens at a decay of 1 - 2^-11).  S is rounded to bf16 for O1, P
@@ -23,9 +24,10 @@
 // of an SM's share of 6.5 TB/s.  Next to it is shared memory: at N = 128 a product reads its two
 // operands at the full 128 bytes a cycle.  So V~^T and S are A operands from tensor memory, K is
 // read as TMA left it, and nothing but P and the outputs is written (with decayed keys as three
-// tiles in shared memory a chunk took 7600 cycles).  Passes run beside each other: warps 0-3
-// the state, 4-11 V~, 12-15 P, 16-19 the outputs, 20 and 21 issue (20 G, O1, O2; 21 KV, which
-// waits for none of them), 22 loads up to four chunks ahead.
+// tiles in shared memory a chunk took 7600 cycles).  Passes run beside each other: warps 0-7
+// the state, 8-15 V~ (four the first 32 tokens of a chunk, four the others, each as soon as KV has
+// read its half), 16-19 P, 20-23 the outputs, 24 and 25 issue (24 G, O1, O2; 25 KV, which waits
+// for none of them), 26 loads up to four chunks ahead.
 //
 // Waits are bounded: a give-up sets the status word, drains what is in flight and ends the CTA.
 
@@ -75,6 +77,15 @@ __device__ __forceinline__ void tmem_st_16x8(uint32_t taddr, const uint32_t (&r)
   asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};"
                :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
 }
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+      :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
+         "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]),
+         "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
@@ -114,7 +125,8 @@ struct TokenWeights {
 };
 
 // V~^T of parts p0 .. p0 + NP - 1 (16 tokens each) of a chunk into tensor memory by four warps:
-// value channels in the lanes, two tokens to a column, the three bf16 terms 32 columns apart.
+// value channels in the lanes, two tokens to a column; each half chunk has its three bf16 terms
+// of 16 columns one after the other.
 // The terms are cut off rather than rounded, which leaves 16, 8 and 0 of a float's 24 bits:
 // their sum is the float.
 template <int NP>
@@ -143,20 +155,22 @@ __device__ __forceinline__ void weigh_values(const uint32_t (&row)[2], uint32_t 
       }
 #pragma unroll
       for (int s = 0; s < 3; ++s)
-        tmem_st_16x8(taddr + ((uint32_t)(16 * hh) << 16) + 32 * s + 8 * (p0 + p), out[s]);
+        tmem_st_16x8(taddr + ((uint32_t)(16 * hh) << 16) + 48 * ((p0 + p) >> 1) + 16 * s +
+                         8 * ((p0 + p) & 1), out[s]);
     }
 }
 
-// KV = V~^T K: twelve products, the smallest terms first (A in tensor memory, B the K tile).
+// One half chunk's share of KV = V~^T K: six products (A in tensor memory, B the K tile).
 template <int DK>
-__device__ __forceinline__ void issue_kv(uint32_t d, uint32_t vw, uint32_t k_tile) {
+__device__ __forceinline__ void issue_kv(uint32_t d, uint32_t vw, uint32_t k_tile, int half) {
   constexpr uint32_t id = idesc_bf16_mn(128, DK);
-  const uint64_t kb = mn_base(k_tile, DK == 128);
+  const uint64_t kb = mn_base(k_tile, DK == 128) + mn_step(2) * half;
 #pragma unroll
   for (int t = 2; t >= 0; --t)
 #pragma unroll
-    for (int ks = 0; ks < kC / 16; ++ks)
-      mma_bf16_ta_w(d, vw + 32 * t + 8 * ks, kb + mn_step(ks), id, t < 2 || ks > 0);
+    for (int ks = 0; ks < 2; ++ks)
+      mma_bf16_ta_w(d, vw + 48 * half + 16 * t + 8 * ks, kb + mn_step(ks), id,
+                    half > 0 || t < 2 || ks > 0);
 }
 
 struct LinMaps {
@@ -300,7 +314,8 @@ lin_segment_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t 
         if (!wait(mb(ss.vw_full[w]), (uint32_t)(c >> 1) & 1u)) break;
         if (c >= 2 && !wait(mb(ss.kv_free[w]), (uint32_t)((c - 2) >> 1) & 1u)) break;
         fence_after_sync();
-        issue_kv<DK>(tb + L::KV + 128 * w, tb + L::VW + 96 * w, sb + s * L::STAGE);
+        issue_kv<DK>(tb + L::KV + 128 * w, tb + L::VW + 96 * w, sb + s * L::STAGE, 0);
+        issue_kv<DK>(tb + L::KV + 128 * w, tb + L::VW + 96 * w, sb + s * L::STAGE, 1);
         mma_commit_w(mb(ss.kv_done[w]));
         mma_commit_w(mb(ss.empty[s]));
       }
@@ -365,13 +380,13 @@ struct OutLayout {
 };
 struct OutSmall {
   unsigned long long full[4], empty[4];
-  unsigned long long g_full, p_full[2], vw_full, kv_done, kv_free, s_ready, o1_done, o_full,
-      o_free, drained[2];
+  unsigned long long g_full, p_full[2], vw_full[2], vw_free, kv_done, kv_free, s_ready, o1_done,
+      o_full, o_free, drained[2];
   uint32_t tmem;
   int abort;
 };
-// six warpgroups: 768 threads of 80 registers at launch, then 192 + 2 x 56 + 56 + 72 + 48
-constexpr int kOutWarps = 24;
+// seven warpgroups: 896 threads of 72 registers at launch, then 2 x 112 + 2 x 56 + 56 + 64 + 48
+constexpr int kOutWarps = 28;
 
 template <int DK, int DV>
 __global__ void __launch_bounds__(kOutWarps * 32, 1)
@@ -403,12 +418,13 @@ lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin
     for (int s = 0; s < 2; ++s) {
       mbar_init(mb(os.p_full[s]), 4);
       mbar_init(mb(os.drained[s]), 1);
+      mbar_init(mb(os.vw_full[s]), 4);
     }
     mbar_init(mb(os.g_full), 1);
-    mbar_init(mb(os.vw_full), 8);
+    mbar_init(mb(os.vw_free), 1);
     mbar_init(mb(os.kv_done), 1);
-    mbar_init(mb(os.kv_free), 4);
-    mbar_init(mb(os.s_ready), 4);
+    mbar_init(mb(os.kv_free), 8);
+    mbar_init(mb(os.s_ready), 8);
     mbar_init(mb(os.o1_done), 1);
     mbar_init(mb(os.o_full), 1);
     mbar_init(mb(os.o_free), 4);
@@ -417,7 +433,7 @@ lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin
   }
   {
     const int ragged = sg.n - (nch - 1) * kC;
-    const int r = tid % kC, x = tid / kC;          // twelve rows of 64 threads
+    const int r = tid % kC, x = tid / kC;          // fourteen rows of 64 threads
     if (x < 2) {
       tab.rows.wt[x][r] = row_weight(l2, rev, x ? ragged : kC, r);
     } else if (x < 6) {
@@ -438,28 +454,30 @@ lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin
   // chunk c in processing order: its first token in the segment
   auto chunk_at = [&](int c) { return (rev ? nch - 1 - c : c) * kC; };
 
-  if (warp < 4) {
-    more_registers<192>();
-    // ---- the state: thread = value row ----------------------------------------------------
-    const int v = warp * 32 + lane;
-    const uint32_t tl = (uint32_t)(warp * 32) << 16;
+  if (warp < 8) {
+    more_registers<112>();
+    // ---- the state: a thread has a row's first or second half ------------------------------
+    constexpr int DH = DK / 2;
+    const int v = (warp & 3) * 32 + lane, col = warp < 4 ? 0 : DH;
+    const uint32_t tl = (uint32_t)((warp & 3) * 32) << 16;
     // entering: the call's own state decayed over the tokens before, and what the earlier
     // segments left
-    float S[DK];
+    float S[DH];
 #pragma unroll
-    for (int e = 0; e < DK; ++e) S[e] = 0.f;
+    for (int e = 0; e < DH; ++e) S[e] = 0.f;
     if (v < DV) {
       const LinJob& jb = sc.job[job];
+      const size_t at = (size_t)bh * DV * DK;
       if (jb.s_in) {
         const float f = p == 0 ? 1.f : (float)decay_pow(l2, (long)sg.before + e0 - 1);
-        const float* s = jb.s_in + (size_t)bh * DV * DK;
         if (jb.s_trans) {
 #pragma unroll
-          for (int e = 0; e < DK; ++e) S[e] = f * s[(size_t)e * DV + v];
+          for (int e = 0; e < DH; ++e) S[e] = f * jb.s_in[at + (size_t)(col + e) * DV + v];
         } else {
 #pragma unroll
-          for (int e = 0; e < DK / 4; ++e) {
-            const float4 y = *reinterpret_cast<const float4*>(s + (size_t)v * DK + 4 * e);
+          for (int e = 0; e < DH / 4; ++e) {
+            const float4 y =
+                *reinterpret_cast<const float4*>(jb.s_in + at + (size_t)v * DK + col + 4 * e);
             S[4 * e] = f * y.x;
             S[4 * e + 1] = f * y.y;
             S[4 * e + 2] = f * y.z;
@@ -469,13 +487,13 @@ lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin
       }
       const float* part = sc.part +
                           ((size_t)job * sc.B * sc.H + bh) * (sc.nseg - 1) * DV * DK +
-                          (size_t)v * DK;
+                          (size_t)v * DK + col;
       for (int m = 0; m < p; ++m) {
         const Segment pm = segment(m, rev, sc.T, sc.seg_len, sc.nseg);
         const float f = (float)decay_pow(l2, (long)sg.before - pm.before - pm.n);
         const float* s = part + (size_t)m * DV * DK;
 #pragma unroll
-        for (int e = 0; e < DK / 4; ++e) {
+        for (int e = 0; e < DH / 4; ++e) {
           const float4 y = *reinterpret_cast<const float4*>(s + 4 * e);
           S[4 * e] = fmaf(f, y.x, S[4 * e]);
           S[4 * e + 1] = fmaf(f, y.y, S[4 * e + 1]);
@@ -494,11 +512,12 @@ lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin
       if (c > 0 && !(ok = wait(mb(os.o1_done), (uint32_t)(c - 1) & 1u))) break;
       fence_after_sync();
 #pragma unroll
-      for (int q = 0; q < DK / 64; ++q) {
-        float y[32];
+      for (int q = 0; q < DH / 32; ++q) {
+        uint32_t y[16];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) y[e] = pack2(S[64 * q + 2 * e], S[64 * q + 2 * e + 1]);
-        tmem_st32(tb + tl + L::SB + 32 * q, y);
+        for (int e = 0; e < 16; ++e)
+          y[e] = __float_as_uint(pack2(S[32 * q + 2 * e], S[32 * q + 2 * e + 1]));
+        tmem_st16(tb + tl + L::SB + col / 2 + 16 * q, y);
       }
       tmem_wait_st();
       fence_before_sync();
@@ -516,11 +535,11 @@ lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin
       if (!(ok = wait(mb(os.kv_done), (uint32_t)c & 1u))) break;
       fence_after_sync();
 #pragma unroll
-      for (int q = 0; q < DK / 32; ++q) {
+      for (int q = 0; q < DH / 32; ++q) {
         float x[32];
-        tmem_ld32(tb + tl + L::KV + 32 * q, x);
+        tmem_ld32(tb + tl + L::KV + col + 32 * q, x);
         tmem_wait_ld();
-        if (q == DK / 32 - 1) {
+        if (q == DH / 32 - 1) {
           fence_before_sync();
           __syncwarp();
           if (lane == 0) mbar_arrive(mb(os.kv_free));
@@ -536,18 +555,17 @@ lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin
     }
     if (s_out && ok && v < DV) {
       const float f = (float)decay_pow(l2, 1 - e0);
-      float* dst = s_out + (size_t)bh * DV * DK + (size_t)v * DK;
+      float* dst = s_out + (size_t)bh * DV * DK + (size_t)v * DK + col;
 #pragma unroll
-      for (int e = 0; e < DK / 4; ++e)
+      for (int e = 0; e < DH / 4; ++e)
         reinterpret_cast<float4*>(dst)[e] = make_float4(f * S[4 * e], f * S[4 * e + 1],
                                                         f * S[4 * e + 2], f * S[4 * e + 3]);
     }
-  } else if (warp < 12) {
+  } else if (warp < 16) {
     fewer_registers<56>();
     // ---- V~ ----------------------------------------------------------------------------------
-    // (two warps to 32 channels, 32 tokens each)
     const uint32_t tl = (uint32_t)((warp & 3) * 32) << 16;
-    const int p0 = warp < 8 ? 0 : 2;
+    const int half = warp < 12 ? 0 : 1, p0 = 2 * half;
     TokenWeights tw;
     for (int c = 0; c < nstate; ++c) {
       const int s = c % NS;
@@ -555,16 +573,17 @@ lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin
       const int ragged = sg.n - chunk_at(c) < kC;
       if (c == 0 || ragged || (rev && c == 1)) tw.load(tab.rows.wt[ragged] + 16 * p0, lane);
       if (!wait(mb(os.full[s]), (uint32_t)(c / NS) & 1u)) break;
-      if (c > 0 && !wait(mb(os.kv_done), (uint32_t)(c - 1) & 1u)) break;
+      // the product of the chunk before has read this half
+      if (c > 0 && !wait(mb(half ? os.kv_done : os.vw_free), (uint32_t)(c - 1) & 1u)) break;
       fence_after_sync();
       const TileRow<DV> row(sb + s * L::STAGE + 2 * L::KT, warp, lane);
       weigh_values<2>(row.at, tb + tl + L::VW, tw, p0, 1.f);
       tmem_wait_st();
       fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(mb(os.vw_full));
+      if (lane == 0) mbar_arrive(mb(os.vw_full[half]));
     }
-  } else if (warp < 16) {
+  } else if (warp < 20) {
     fewer_registers<56>();
     // ---- P -------------------------------------------------------------------------------------
     // an M = 64 accumulator: row t in lane 32 (t / 16) + t % 16.  This thread's elements and
@@ -603,8 +622,8 @@ lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin
       __syncwarp();
       if (lane == 0) mbar_arrive(mb(os.p_full[c & 1]));
     }
-  } else if (warp < 20) {
-    fewer_registers<72>();
+  } else if (warp < 24) {
+    fewer_registers<64>();
     // ---- the outputs -----------------------------------------------------------------------
     const uint32_t tl = (uint32_t)((warp & 3) * 32) << 16;
     const TileRow<DV> row(sb + L::O, warp, lane);
@@ -613,7 +632,7 @@ lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin
     for (int c = 0; c < nch; ++c) {
       ok = wait(mb(os.o_full), (uint32_t)c & 1u);
       // the last store has read its tile
-      if (tid == 16 * 32) bulk_wait_read_all();
+      if (tid == 20 * 32) bulk_wait_read_all();
       if (named_bar_or(1, 128, !ok)) break;
       fence_after_sync();
       const int at = chunk_at(c);
@@ -643,17 +662,17 @@ lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin
       if (lane == 0) mbar_arrive(mb(os.o_free));
       fence_smem_to_async();
       named_bar(1, 128);
-      if (tid == 16 * 32) {
+      if (tid == 20 * 32) {
         // rows past the tensor's end are not written
         for (int pn = 0; pn < DV / 64; ++pn)
           tma_store_4d(&maps.o[job], sb + L::O + pn * kC * 128, 64 * pn, h, sg.a + at, b);
         bulk_commit();
       }
     }
-    if (tid == 16 * 32) bulk_wait_all();
+    if (tid == 20 * 32) bulk_wait_all();
   } else {
     fewer_registers<48>();
-    if (warp == 20) {
+    if (warp == 24) {
       // ---- issuing warp: G, O1, O2 ---------------------------------------------------------------
       constexpr uint32_t id_g = idesc_bf16(64, 64), id_o1 = idesc_bf16(128, 64),
                          id_o2 = idesc_a_mn(idesc_bf16(128, 64));
@@ -694,17 +713,21 @@ lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin
       // the products issued here complete before tensor memory is freed
       mma_commit_w(mb(os.drained[0]));
       mbar_wait(mb(os.drained[0]), 0, kDrain);
-    } else if (warp == 21) {
+    } else if (warp == 25) {
       // ---- issuing warp: KV ------------------------------------------------------------------------
       for (int c = 0; c < nch; ++c) {
         const int s = c % NS;
         if (c < nstate) {
           if (!wait(mb(os.full[s]), (uint32_t)(c / NS) & 1u)) break;
-          if (!wait(mb(os.vw_full), (uint32_t)c & 1u)) break;
           // the accumulator is free once the state has taken the chunk before
+          if (!wait(mb(os.vw_full[0]), (uint32_t)c & 1u)) break;
           if (c > 0 && !wait(mb(os.kv_free), (uint32_t)(c - 1) & 1u)) break;
           fence_after_sync();
-          issue_kv<DK>(tb + L::KV, tb + L::VW, sb + s * L::STAGE + L::KT);
+          issue_kv<DK>(tb + L::KV, tb + L::VW, sb + s * L::STAGE + L::KT, 0);
+          mma_commit_w(mb(os.vw_free));
+          if (!wait(mb(os.vw_full[1]), (uint32_t)c & 1u)) break;
+          fence_after_sync();
+          issue_kv<DK>(tb + L::KV, tb + L::VW, sb + s * L::STAGE + L::KT, 1);
           mma_commit_w(mb(os.kv_done));
           mma_commit_w(mb(os.empty[s]));
         } else if (lane == 0) {
@@ -713,7 +736,7 @@ lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin
       }
       mma_commit_w(mb(os.drained[1]));
       mbar_wait(mb(os.drained[1]), 0, kDrain);
-    } else if (warp == 22) {
+    } else if (warp == 26) {
       // ---- loader -----------------------------------------------------------------------------------
       int done = 0;
       for (int c = 0; c < nch; ++c) {
