@@ -459,6 +459,9 @@ def backward_workspace_bytes(B, T, H, dk, dv, kda):
 
 # ---- linear attention with one decay per head; sliding-window softmax attention -----------
 
+# A decode step runs for a few microseconds, so these calls keep their own cost low: one test a
+# tensor (the reason for a refusal is worked out by _need afterwards), plain integers for pointers.
+
 def _on(device, stream):
     """Context in which a call on `stream` (None: the device's current one) allocates and
     launches: outputs and workspaces belong to that stream, the launch goes to that device."""
@@ -466,7 +469,29 @@ def _on(device, stream):
         return torch.cuda.stream(stream)
     if device.index != torch.cuda.current_device():
         return torch.cuda.device(device)
-    return contextlib.nullcontext()
+    return _HERE_ALREADY
+
+
+_HERE_ALREADY = contextlib.nullcontext()
+
+
+def _raw(device, stream):
+    if stream is not None:
+        return stream.cuda_stream
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _same(t, name, shape, dtype, device):
+    """data_ptr of t after _need's checks."""
+    if isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype \
+            and t.device == device and t.is_contiguous():
+        return t.data_ptr()
+    _need(t, name, shape, dtype, device)
+    return t.data_ptr()
+
+
+def _maybe(t, name, shape, dtype, device):
+    return None if t is None else _same(t, name, shape, dtype, device)
 
 
 def _scratch(workspace, need, device, what):
@@ -486,7 +511,7 @@ def _cuda(t, name, dim, form):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dim() != dim:
         raise ValueError(f"{name} must be {form}")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError("inputs must be CUDA tensors (there is no CPU path)")
     return t.device
 
@@ -494,7 +519,7 @@ def _cuda(t, name, dim, form):
 def _out(t, name, shape, dtype, device):
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    _need(t, name, shape, dtype, device)
+    _same(t, name, shape, dtype, device)
     return t
 
 
@@ -517,20 +542,17 @@ def lin_prefill(q, k, v, decay, s0=None, *, o=None, s_final=None, stream=None, w
     dv = v.shape[-1]
     dt = q.dtype
     code = _code(dt)
-    _need(k, "k", (B, T, H, dk), dt, dev)
-    _need(q, "q", (B, T, H, dk), dt, dev)
-    _need(v, "v", (B, T, H, dv), dt, dev)
-    _need(decay, "decay", (H,), torch.float32, dev)
-    if s0 is not None:
-        _need(s0, "s0", (B, H, dv, dk), torch.float32, dev)
+    state = (B, H, dv, dk)
+    ptrs = (_same(q, "q", (B, T, H, dk), dt, dev), _same(k, "k", (B, T, H, dk), dt, dev),
+            _same(v, "v", (B, T, H, dv), dt, dev), _same(decay, "decay", (H,), torch.float32, dev),
+            _maybe(s0, "s0", state, torch.float32, dev))
     with _on(dev, stream):
         o = _out(o, "o", (B, T, H, dv), dt, dev)
-        sf = None if s_final is False else _out(s_final, "s_final", (B, H, dv, dk), torch.float32,
-                                                dev)
+        sf = None if s_final is False else _out(s_final, "s_final", state, torch.float32, dev)
         ws, nws = _scratch(workspace, lib.gdr_lin_workspace_bytes(B, T, H, dk, dv, code, 0), dev,
                            "lin_prefill")
-        _check(lib.lin_prefill(_ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(s0), _ptr(o), _ptr(sf),
-                               B, T, H, dk, dv, code, _ptr(ws), nws, _stream(dev, stream)))
+        _check(lib.lin_prefill(*ptrs, o.data_ptr(), None if sf is None else sf.data_ptr(), B, T, H,
+                               dk, dv, code, ws.data_ptr(), nws, _raw(dev, stream)))
     return o, sf
 
 
@@ -542,15 +564,12 @@ def lin_decode(q, k, v, decay, state, *, o=None, stream=None):
     dv = v.shape[-1]
     dt = q.dtype
     code = _code(dt)
-    _need(q, "q", (N, H, dk), dt, dev)
-    _need(k, "k", (N, H, dk), dt, dev)
-    _need(v, "v", (N, H, dv), dt, dev)
-    _need(decay, "decay", (H,), torch.float32, dev)
-    _need(state, "state", (N, H, dv, dk), torch.float32, dev)
+    ptrs = (_same(q, "q", (N, H, dk), dt, dev), _same(k, "k", (N, H, dk), dt, dev),
+            _same(v, "v", (N, H, dv), dt, dev), _same(decay, "decay", (H,), torch.float32, dev),
+            _same(state, "state", (N, H, dv, dk), torch.float32, dev))
     with _on(dev, stream):
         o = _out(o, "o", (N, H, dv), dt, dev)
-        _check(lib.lin_decode(_ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(state), _ptr(o), N, H,
-                              dk, dv, code, _stream(dev, stream)))
+        _check(lib.lin_decode(*ptrs, o.data_ptr(), N, H, dk, dv, code, _raw(dev, stream)))
     return o
 
 
@@ -563,23 +582,19 @@ def lin_backward(q, k, v, decay, s0, do, ds_final=None, *, workspace=None, strea
     dv = v.shape[-1]
     dt = q.dtype
     code = _code(dt)
-    _need(q, "q", (B, T, H, dk), dt, dev)
-    _need(k, "k", (B, T, H, dk), dt, dev)
-    _need(v, "v", (B, T, H, dv), dt, dev)
-    _need(decay, "decay", (H,), torch.float32, dev)
-    if s0 is not None:
-        _need(s0, "s0", (B, H, dv, dk), torch.float32, dev)
-    _need(do, "do", (B, T, H, dv), dt, dev)
-    if ds_final is not None:
-        _need(ds_final, "ds_final", (B, H, dv, dk), torch.float32, dev)
+    state = (B, H, dv, dk)
+    ptrs = (_same(q, "q", (B, T, H, dk), dt, dev), _same(k, "k", (B, T, H, dk), dt, dev),
+            _same(v, "v", (B, T, H, dv), dt, dev), _same(decay, "decay", (H,), torch.float32, dev),
+            _maybe(s0, "s0", state, torch.float32, dev), _same(do, "do", (B, T, H, dv), dt, dev),
+            _maybe(ds_final, "ds_final", state, torch.float32, dev))
     with _on(dev, stream):
         dq, dk_, dv_ = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-        ds0 = torch.empty((B, H, dv, dk), dtype=torch.float32, device=dev)
+        ds0 = torch.empty(state, dtype=torch.float32, device=dev)
         ws, nws = _scratch(workspace, lib.gdr_lin_workspace_bytes(B, T, H, dk, dv, code, 1), dev,
                            "lin_backward")
-        _check(lib.lin_backward(_ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(s0), _ptr(do),
-                                _ptr(ds_final), _ptr(dq), _ptr(dk_), _ptr(dv_), _ptr(ds0), B, T, H,
-                                dk, dv, code, _ptr(ws), nws, _stream(dev, stream)))
+        _check(lib.lin_backward(*ptrs, dq.data_ptr(), dk_.data_ptr(), dv_.data_ptr(),
+                                ds0.data_ptr(), B, T, H, dk, dv, code, ws.data_ptr(), nws,
+                                _raw(dev, stream)))
     return dq, dk_, dv_, ds0
 
 
@@ -589,20 +604,13 @@ def attn_workspace_bytes(B, Tq, Tk, Hq, Hkv, d, dtype, backward=False, window=0,
                                         _int32(sinks, "sinks"), _code(dtype), int(backward))
 
 
-def _lengths(t, name, n, device):
-    if t is not None:
-        _need(t, name, (n,), torch.int32, device)
-    return t
-
-
 def _int32(x, name):
     """A window or a number of sinks as the C int it becomes (None: 0)."""
-    x = 0 if x is None else int(x)
-    if x > 0x7fffffff:
-        x = 0x7fffffff
+    if x is None:
+        return 0
     if x < 0 and name == "sinks":
         raise ValueError("sinks must not be negative")
-    return max(x, 0)
+    return min(max(int(x), 0), 0x7fffffff)
 
 
 def _attn_shapes(q, k, v):
@@ -610,10 +618,10 @@ def _attn_shapes(q, k, v):
     _cuda(k, "k", 4, "[B, Tk, Hkv, d]")
     B, Tq, Hq, d = q.shape
     Tk, Hkv = k.shape[1], k.shape[2]
-    _need(q, "q", (B, Tq, Hq, d), None, dev)
-    _need(k, "k", (B, Tk, Hkv, d), q.dtype, dev)
-    _need(v, "v", (B, Tk, Hkv, d), q.dtype, dev)
-    return dev, B, Tq, Tk, Hq, Hkv, d
+    ptrs = (_same(q, "q", (B, Tq, Hq, d), q.dtype, dev),
+            _same(k, "k", (B, Tk, Hkv, d), q.dtype, dev),
+            _same(v, "v", (B, Tk, Hkv, d), q.dtype, dev))
+    return dev, ptrs, B, Tq, Tk, Hq, Hkv, d
 
 
 def attn_prefill(q, k, v, *, window=0, sinks=0, scale=None, lengths=None, o=None, lse=None,
@@ -627,17 +635,17 @@ def attn_prefill(q, k, v, *, window=0, sinks=0, scale=None, lengths=None, o=None
     Returns (o in q's type, lse [B, Hq, Tq] float32); a query that sees nothing has o = 0 and
     lse = -inf.  Pass lse=False to skip it.
     """
-    dev, B, Tq, Tk, Hq, Hkv, d = _attn_shapes(q, k, v)
+    dev, ptrs, B, Tq, Tk, Hq, Hkv, d = _attn_shapes(q, k, v)
     code = _code(q.dtype)
-    _lengths(lengths, "lengths", B, dev)
+    lens = _maybe(lengths, "lengths", (B,), torch.int32, dev)
     w, n = _int32(window, "window"), _int32(sinks, "sinks")
     with _on(dev, stream):
         o = _out(o, "o", (B, Tq, Hq, d), q.dtype, dev)
         lse = None if lse is False else _out(lse, "lse", (B, Hq, Tq), torch.float32, dev)
         ws, nws = _scratch(workspace, 256, dev, "attn_prefill")
-        _check(lib.attn_prefill(_ptr(q), _ptr(k), _ptr(v), _ptr(lengths), _ptr(o), _ptr(lse), B,
-                                Tq, Tk, Hq, Hkv, d, w, n, d ** -0.5 if scale is None else scale,
-                                code, _ptr(ws), nws, _stream(dev, stream)))
+        _check(lib.attn_prefill(*ptrs, lens, o.data_ptr(), None if lse is None else lse.data_ptr(),
+                                B, Tq, Tk, Hq, Hkv, d, w, n, d ** -0.5 if scale is None else scale,
+                                code, ws.data_ptr(), nws, _raw(dev, stream)))
     return o, lse
 
 
@@ -645,32 +653,33 @@ def attn_backward(q, k, v, o, lse, do, *, window=0, sinks=0, scale=None, lengths
                   stream=None, workspace=None):
     """Gradients (dq, dk, dv, in the inputs' type) of L = sum <do, o> for
     attn_prefill(q, k, v, ...), from its o and lse."""
-    dev, B, Tq, Tk, Hq, Hkv, d = _attn_shapes(q, k, v)
+    dev, ptrs, B, Tq, Tk, Hq, Hkv, d = _attn_shapes(q, k, v)
     code = _code(q.dtype)
-    _need(o, "o", (B, Tq, Hq, d), q.dtype, dev)
-    _need(lse, "lse", (B, Hq, Tq), torch.float32, dev)
-    _need(do, "do", (B, Tq, Hq, d), q.dtype, dev)
-    _lengths(lengths, "lengths", B, dev)
+    lens = _maybe(lengths, "lengths", (B,), torch.int32, dev)
+    given = (_same(o, "o", (B, Tq, Hq, d), q.dtype, dev),
+             _same(lse, "lse", (B, Hq, Tq), torch.float32, dev),
+             _same(do, "do", (B, Tq, Hq, d), q.dtype, dev))
     w, n = _int32(window, "window"), _int32(sinks, "sinks")
     with _on(dev, stream):
         dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
         ws, nws = _scratch(workspace, lib.gdr_attn_workspace_bytes(B, Tq, Tk, Hq, Hkv, d, w, n,
                                                                    code, 1), dev, "attn_backward")
-        _check(lib.attn_backward(_ptr(q), _ptr(k), _ptr(v), _ptr(lengths), _ptr(o), _ptr(lse),
-                                 _ptr(do), _ptr(dq), _ptr(dk), _ptr(dv), B, Tq, Tk, Hq, Hkv, d, w,
-                                 n, d ** -0.5 if scale is None else scale, code, _ptr(ws), nws,
-                                 _stream(dev, stream)))
+        _check(lib.attn_backward(*ptrs, lens, *given, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                                 B, Tq, Tk, Hq, Hkv, d, w, n,
+                                 d ** -0.5 if scale is None else scale, code, ws.data_ptr(), nws,
+                                 _raw(dev, stream)))
     return dq, dk, dv
 
 
 def _paged(k_cache, v_cache, page_table, N, dt, dev):
     _cuda(k_cache, "k_cache", 4, "[npages, page, Hkv, d]")
     npages, page, Hkv, d = k_cache.shape
-    _need(k_cache, "k_cache", (npages, page, Hkv, d), dt, dev)
-    _need(v_cache, "v_cache", (npages, page, Hkv, d), dt, dev)
     _cuda(page_table, "page_table", 2, "[N, max_pages]")
-    _need(page_table, "page_table", (N, page_table.shape[1]), torch.int32, dev)
-    return npages, page, Hkv, d, page_table.shape[1]
+    max_pages = page_table.shape[1]
+    ptrs = (_same(k_cache, "k_cache", k_cache.shape, dt, dev),
+            _same(v_cache, "v_cache", k_cache.shape, dt, dev),
+            _same(page_table, "page_table", (N, max_pages), torch.int32, dev))
+    return ptrs, npages, page, Hkv, d, max_pages
 
 
 def attn_decode_workspace_bytes(N, Hq, Hkv, d, page, max_pages, dtype, window=0, sinks=0):
@@ -696,25 +705,22 @@ def attn_decode(q, k_cache, v_cache, page_table, lengths, *, k=None, v=None, win
     N, Hq, d = q.shape
     dt = q.dtype
     code = _code(dt)
-    _need(q, "q", (N, Hq, d), dt, dev)
-    npages, page, Hkv, dc, max_pages = _paged(k_cache, v_cache, page_table, N, dt, dev)
+    qp = _same(q, "q", (N, Hq, d), dt, dev)
+    ptrs, npages, page, Hkv, dc, max_pages = _paged(k_cache, v_cache, page_table, N, dt, dev)
     if dc != d:
         raise ValueError(f"the caches' head size {dc} is not q's {d}")
-    _need(lengths, "lengths", (N,), torch.int32, dev)
+    lens = _same(lengths, "lengths", (N,), torch.int32, dev)
     if (k is None) != (v is None):
         raise ValueError("k and v are given together or not at all")
-    if k is not None:
-        _need(k, "k", (N, Hkv, d), dt, dev)
-        _need(v, "v", (N, Hkv, d), dt, dev)
+    kp, vp = _maybe(k, "k", (N, Hkv, d), dt, dev), _maybe(v, "v", (N, Hkv, d), dt, dev)
     w, s = _int32(window, "window"), _int32(sinks, "sinks")
     with _on(dev, stream):
         o = _out(o, "o", (N, Hq, d), dt, dev)
         ws, nws = _scratch(workspace, lib.gdr_attn_decode_workspace_bytes(
             N, Hq, Hkv, d, page, max_pages, w, s, code), dev, "attn_decode")
-        _check(lib.attn_decode(_ptr(q), _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache),
-                               _ptr(page_table), _ptr(lengths), _ptr(o), N, Hq, Hkv, d, npages,
-                               page, max_pages, w, s, d ** -0.5 if scale is None else scale, code,
-                               _ptr(ws), nws, _stream(dev, stream)))
+        _check(lib.attn_decode(qp, kp, vp, *ptrs, lens, o.data_ptr(), N, Hq, Hkv, d, npages, page,
+                               max_pages, w, s, d ** -0.5 if scale is None else scale, code,
+                               ws.data_ptr(), nws, _raw(dev, stream)))
     return o
 
 
@@ -727,20 +733,16 @@ def kv_append(k, v, k_cache, v_cache, page_table, start, counts=None, *, stream=
     N, K, Hkv, d = k.shape
     dt = k.dtype
     code = _code(dt)
-    _need(k, "k", (N, K, Hkv, d), dt, dev)
-    _need(v, "v", (N, K, Hkv, d), dt, dev)
-    npages, page, hc, dc, max_pages = _paged(k_cache, v_cache, page_table, N, dt, dev)
+    kp, vp = _same(k, "k", (N, K, Hkv, d), dt, dev), _same(v, "v", (N, K, Hkv, d), dt, dev)
+    ptrs, npages, page, hc, dc, max_pages = _paged(k_cache, v_cache, page_table, N, dt, dev)
     if (hc, dc) != (Hkv, d):
         raise ValueError(f"the caches hold heads {hc} x {dc}, k and v {Hkv} x {d}")
-    _lengths(start, "start", N, dev)
-    _lengths(counts, "counts", N, dev)
-    if start is None:
-        raise TypeError("start must be a torch.Tensor")
+    sp = _same(start, "start", (N,), torch.int32, dev)
+    cp = _maybe(counts, "counts", (N,), torch.int32, dev)
     ws, nws = (None, 0) if workspace is None else _scratch(workspace, 256, dev, "kv_append")
     with _on(dev, stream):
-        _check(lib.kv_append(_ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(page_table),
-                             _ptr(start), _ptr(counts), N, K, Hkv, d, npages, page, max_pages,
-                             code, _ptr(ws), nws, _stream(dev, stream)))
+        _check(lib.kv_append(kp, vp, *ptrs, sp, cp, N, K, Hkv, d, npages, page, max_pages, code,
+                             None if ws is None else ws.data_ptr(), nws, _raw(dev, stream)))
 
 
 def prefill_path(dk, dv, dtype, kda):

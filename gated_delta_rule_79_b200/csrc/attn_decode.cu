@@ -493,39 +493,64 @@ attn_decode_simt(const PagedArgs a) {
   }
 }
 
-// Joins the parts of each (sequence, query head): a warp each.
+// Joins the parts of each (sequence, query head): four warps take the parts in turn, their
+// weights formed by all lanes beforehand, so that the loads of the outputs do not wait for one
+// another (a warp alone, a part at a time, took 23 us over 32 parts).
+constexpr int kMaxSplit = 256;
+
 template <typename T, int D>
 __global__ void __launch_bounds__(128)
 attn_decode_join(const PagedArgs a) {
-  const size_t nh = (size_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
+  __shared__ float wt[kMaxSplit], acc[4][D], red[2][4];
+  const int nh = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   wait_for_prior_grid();
-  if (nh >= (size_t)a.N * a.Hq) return;
-  const Visible vis = visible(a, (int)(nh / a.Hq), false);
+  const Visible vis = visible(a, nh / a.Hq, false);
   const int per = part_tokens(vis.count, a.nsplit);
   const int parts = (vis.count + per - 1) / per;
   if (parts <= 1) return;
-  const float* p = a.part + nh * a.nsplit * (D + 2);
-  const float* ml = p + (size_t)a.nsplit * D;
+  const float* p = a.part + (size_t)nh * a.nsplit * (D + 2);
+  const float2* ml = reinterpret_cast<const float2*>(p + (size_t)a.nsplit * D);
+  constexpr int PT = kMaxSplit / 128;
+  float2 x[PT];
   float m = -INFINITY;
-  for (int s = lane; s < parts; s += 32) m = fmaxf(m, ml[2 * s]);
+#pragma unroll
+  for (int e = 0; e < PT; ++e) {
+    x[e] = tid + 128 * e < parts ? ml[tid + 128 * e] : make_float2(-INFINITY, 0.f);
+    m = fmaxf(m, x[e].x);
+  }
 #pragma unroll
   for (int f = 16; f; f >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, f));
+  if (lane == 0) red[0][warp] = m;
+  __syncthreads();
+  m = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
   const float base = m == -INFINITY ? 0.f : m;
+  float l = 0.f;
+#pragma unroll
+  for (int e = 0; e < PT; ++e) {
+    const float f = exp2f(x[e].x - base);
+    wt[tid + 128 * e] = f;
+    l = fmaf(f, x[e].y, l);
+  }
+#pragma unroll
+  for (int f = 16; f; f >>= 1) l += __shfl_xor_sync(0xffffffffu, l, f);
+  if (lane == 0) red[1][warp] = l;
+  __syncthreads();
   constexpr int CPL = D / 32;
-  float l = 0.f, o[CPL] = {};
-#pragma unroll 4
-  for (int s = 0; s < parts; ++s) {
-    const float2 x = *reinterpret_cast<const float2*>(ml + 2 * s);
-    const float f = exp2f(x.x - base);
-    l = fmaf(f, x.y, l);
+  float o[CPL] = {};
+#pragma unroll 8
+  for (int s = warp; s < parts; s += 4) {
+    const float f = wt[s];
 #pragma unroll
     for (int e = 0; e < CPL; ++e) o[e] = fmaf(f, p[(size_t)s * D + lane + 32 * e], o[e]);
   }
-  const float inv = l != 0.f ? 1.f / l : 0.f;
 #pragma unroll
-  for (int e = 0; e < CPL; ++e)
-    Elem<T>::store((T*)a.o + nh * D + lane + 32 * e, o[e] * inv);
+  for (int e = 0; e < CPL; ++e) acc[warp][lane + 32 * e] = o[e];
+  __syncthreads();
+  l = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
+  const float inv = l != 0.f ? 1.f / l : 0.f;
+  if (tid < D)
+    Elem<T>::store((T*)a.o + (size_t)nh * D + tid,
+                   ((acc[0][tid] + acc[1][tid]) + (acc[2][tid] + acc[3][tid])) * inv);
 }
 
 // Token t of sequence n (t < counts[n]) goes to position start[n] + t of its pages: a thread
@@ -578,7 +603,7 @@ cudaError_t launch_t(const PagedArgs& a, cudaStream_t st) {
   }
   if (e != cudaSuccess || a.nsplit == 1) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(((size_t)a.N * a.Hq + 3) / 4), 1, 1);
+  cfg.gridDim = dim3((unsigned)(a.N * a.Hq), 1, 1);
   cfg.blockDim = dim3(128, 1, 1);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -616,7 +641,7 @@ int attn_decode_splits(int N, int Hq, int Hkv, int d, int dtype, long capacity, 
   const long by_ctas = (148L * 8 + base - 1) / base;
   long s = by_tokens < by_ctas ? by_tokens : by_ctas;
   if (s < 1) s = 1;
-  return (int)(s > 256 ? 256 : s);
+  return (int)(s > kMaxSplit ? kMaxSplit : s);
 }
 
 cudaError_t launch_attn_decode(const PagedArgs& a, cudaStream_t st) {

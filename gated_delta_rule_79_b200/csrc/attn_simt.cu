@@ -316,25 +316,42 @@ attn_dkv_simt(const AttnGradArgs a) {
   store_rows<T, D>((T*)a.dv + kat, ks, j0, a.f.Tk, ty, tx, dv);
 }
 
-// D_i = do_i . o_i: a warp for each row.
+// D_i = do_i . o_i: 16 bytes of both rows a thread, four rows in flight.
 template <typename T, int D>
 __global__ void __launch_bounds__(256)
 attn_delta_kernel(const T* __restrict__ o, const T* __restrict__ dO, float* __restrict__ delta,
                   int B, int Tq, int Hq) {
-  const size_t row = (size_t)blockIdx.x * 8 + (threadIdx.x >> 5);   // (b, i, h)
-  const int lane = threadIdx.x & 31;
-  if (row >= (size_t)B * Tq * Hq) return;
-  float s = 0.f;
+  constexpr int PER = 16 / sizeof(T), LPR = D / PER;      // elements a thread, lanes a row
+  constexpr int ROWS = 256 / LPR, R = 4;
+  const size_t rows = (size_t)B * Tq * Hq;                // (b, i, h)
+  const size_t first = (size_t)blockIdx.x * ROWS * R + threadIdx.x / LPR;
+  const int c = threadIdx.x % LPR * PER;
+  float s[R];
+  float4 x[R][PER / 4], y[R][PER / 4];
 #pragma unroll
-  for (int c = lane * 4; c < D; c += 128) {
-    const float4 x = Elem<T>::load4(o + row * D + c), y = Elem<T>::load4(dO + row * D + c);
-    s = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, s))));
+  for (int r = 0; r < R; ++r) {
+    const size_t row = min(first + (size_t)r * ROWS, rows - 1);
+#pragma unroll
+    for (int e = 0; e < PER / 4; ++e) {
+      x[r][e] = Elem<T>::load4(o + row * D + c + 4 * e);
+      y[r][e] = Elem<T>::load4(dO + row * D + c + 4 * e);
+    }
   }
 #pragma unroll
-  for (int f = 16; f; f >>= 1) s += __shfl_xor_sync(0xffffffffu, s, f);
-  if (lane == 0) {
-    const size_t h = row % Hq, bi = row / Hq;
-    delta[((bi / Tq) * Hq + h) * Tq + bi % Tq] = s;
+  for (int r = 0; r < R; ++r) {
+    s[r] = 0.f;
+#pragma unroll
+    for (int e = 0; e < PER / 4; ++e)
+      s[r] = fmaf(x[r][e].x, y[r][e].x,
+                  fmaf(x[r][e].y, y[r][e].y,
+                       fmaf(x[r][e].z, y[r][e].z, fmaf(x[r][e].w, y[r][e].w, s[r]))));
+#pragma unroll
+    for (int f = LPR / 2; f; f >>= 1) s[r] += __shfl_xor_sync(0xffffffffu, s[r], f);
+    const size_t row = first + (size_t)r * ROWS;
+    if (row < rows && c == 0) {
+      const size_t h = row % Hq, bi = row / Hq;
+      delta[((bi / Tq) * Hq + h) * Tq + bi % Tq] = s[r];
+    }
   }
 }
 
@@ -351,7 +368,8 @@ cudaError_t forward_t(const AttnArgs& a, cudaStream_t st) {
 template <typename T, int D>
 cudaError_t delta_t(const AttnGradArgs& a, cudaStream_t st) {
   const size_t rows = (size_t)a.f.B * a.f.Tq * a.f.Hq;
-  attn_delta_kernel<T, D><<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(
+  constexpr size_t per = 4 * (256 / (D * sizeof(T) / 16));
+  attn_delta_kernel<T, D><<<(unsigned)((rows + per - 1) / per), 256, 0, st>>>(
       (const T*)a.f.o, (const T*)a.dO, a.delta, a.f.B, a.f.Tq, a.f.Hq);
   return cudaGetLastError();
 }

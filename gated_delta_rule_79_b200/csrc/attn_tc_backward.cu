@@ -521,7 +521,9 @@ template <int D>
 __global__ void __launch_bounds__(256)
 attn_dkv_join(const AttnGradArgs a, const Parts parts) {
   const AttnArgs& f = a.f;
-  const int bh = blockIdx.x % (f.B * f.Hkv), tile = blockIdx.x / (f.B * f.Hkv);
+  constexpr int BLOCKS = kA * (D / 8) * 2 / 256;         // a piece a thread
+  const int at = blockIdx.x / BLOCKS;
+  const int bh = at % (f.B * f.Hkv), tile = at / (f.B * f.Hkv);
   const int b = bh / f.Hkv, hk = bh % f.Hkv;
   const int j0 = tile * kA;
   const Mask m = make_mask(f.lengths, b, f.Tq, f.Tk, f.window, f.sinks);
@@ -534,21 +536,21 @@ attn_dkv_join(const AttnGradArgs a, const Parts parts) {
   const int item = head ? tile * parts.pfirst
                         : parts.nfirst * parts.pfirst + (tile - parts.nfirst) * parts.prest;
   const size_t step = (size_t)f.B * f.Hkv * 2 * kA * D;      // from a part to the next
-  for (int e = threadIdx.x; e < 2 * kA * (D / 8); e += 256) {
-    const int w = e / (kA * (D / 8)), row = e / (D / 8) % kA, c = e % (D / 8) * 8;
-    if (j0 + row >= f.Tk) continue;
-    const float* src = a.part + ((((size_t)item * f.B * f.Hkv + bh) * 2 + w) * kA + row) * D + c;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-    for (int p = 0; p < used; ++p) {
-      const float4 u = *reinterpret_cast<const float4*>(src + p * step);
-      const float4 v = *reinterpret_cast<const float4*>(src + p * step + 4);
-      x.x += u.x, x.y += u.y, x.z += u.z, x.w += u.w;
-      y.x += v.x, y.y += v.y, y.z += v.z, y.w += v.w;
-    }
-    *reinterpret_cast<float4*>((__nv_bfloat16*)(w ? a.dk : a.dv) +
-                               (((size_t)b * f.Tk + j0 + row) * f.Hkv + hk) * D + c) =
-        make_float4(pack2(x.x, x.y), pack2(x.z, x.w), pack2(y.x, y.y), pack2(y.z, y.w));
+  const int e = blockIdx.x % BLOCKS * 256 + threadIdx.x;
+  const int w = e / (kA * (D / 8)), row = e / (D / 8) % kA, c = e % (D / 8) * 8;
+  if (j0 + row >= f.Tk) return;
+  const float* src = a.part + ((((size_t)item * f.B * f.Hkv + bh) * 2 + w) * kA + row) * D + c;
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+#pragma unroll 4
+  for (int p = 0; p < used; ++p) {
+    const float4 u = *reinterpret_cast<const float4*>(src + p * step);
+    const float4 v = *reinterpret_cast<const float4*>(src + p * step + 4);
+    x.x += u.x, x.y += u.y, x.z += u.z, x.w += u.w;
+    y.x += v.x, y.y += v.y, y.z += v.z, y.w += v.w;
   }
+  *reinterpret_cast<float4*>((__nv_bfloat16*)(w ? a.dk : a.dv) +
+                             (((size_t)b * f.Tk + j0 + row) * f.Hkv + hk) * D + c) =
+      make_float4(pack2(x.x, x.y), pack2(x.z, x.w), pack2(y.x, y.y), pack2(y.z, y.w));
 }
 
 // Steps of a key tile when every sequence is whole (the host's tile_steps).
@@ -614,7 +616,8 @@ cudaError_t launch_t(const AttnGradArgs& a, cudaStream_t st) {
   kk<<<(unsigned)p.items() * bh, kWarpsB * 32, L::SMEM, st>>>(kb, vb, qs, ds, a, p, spin);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (p.pfirst > 1 || p.prest > 1) {
-    attn_dkv_join<D><<<(unsigned)(p.prest > 1 ? p.ntiles : p.nfirst) * bh, 256, 0, st>>>(a, p);
+    const unsigned tiles = (unsigned)(p.prest > 1 ? p.ntiles : p.nfirst);
+    attn_dkv_join<D><<<tiles * bh * (kA * (D / 8) * 2 / 256), 256, 0, st>>>(a, p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   kq<<<(unsigned)((f.Tq + kA - 1) / kA * f.Hq * f.B), kWarpsB * 32, L::SMEM, st>>>(qb, db, ks, vs,
