@@ -9,6 +9,7 @@ module raises if libgdr.so has not been built.
 
 import contextlib
 import ctypes
+import functools
 import os
 import threading
 
@@ -474,11 +475,16 @@ def _on(device, stream):
 
 _HERE_ALREADY = contextlib.nullcontext()
 
+# workspace sizes by the sizes of a call
+_lin_bytes = functools.lru_cache(maxsize=256)(lib.gdr_lin_workspace_bytes)
+_attn_bytes = functools.lru_cache(maxsize=256)(lib.gdr_attn_workspace_bytes)
+_decode_bytes = functools.lru_cache(maxsize=256)(lib.gdr_attn_decode_workspace_bytes)
+
 
 def _raw(device, stream):
     if stream is not None:
         return stream.cuda_stream
-    return torch.cuda.current_stream(device).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _same(t, name, shape, dtype, device):
@@ -523,6 +529,14 @@ def _out(t, name, shape, dtype, device):
     return t
 
 
+def _out_like(t, name, like):
+    """An output of the shape and type of `like`, one of the checked inputs."""
+    if t is None:
+        return torch.empty_like(like)
+    _same(t, name, like.shape, like.dtype, like.device)
+    return t
+
+
 def lin_workspace_bytes(B, T, H, dk, dv, dtype, backward=False):
     """Bytes of device workspace for lin_prefill (or lin_backward) at these sizes."""
     return lib.gdr_lin_workspace_bytes(B, T, H, dk, dv, _code(dtype), int(backward))
@@ -547,10 +561,9 @@ def lin_prefill(q, k, v, decay, s0=None, *, o=None, s_final=None, stream=None, w
             _same(v, "v", (B, T, H, dv), dt, dev), _same(decay, "decay", (H,), torch.float32, dev),
             _maybe(s0, "s0", state, torch.float32, dev))
     with _on(dev, stream):
-        o = _out(o, "o", (B, T, H, dv), dt, dev)
+        o = _out_like(o, "o", v)
         sf = None if s_final is False else _out(s_final, "s_final", state, torch.float32, dev)
-        ws, nws = _scratch(workspace, lib.gdr_lin_workspace_bytes(B, T, H, dk, dv, code, 0), dev,
-                           "lin_prefill")
+        ws, nws = _scratch(workspace, _lin_bytes(B, T, H, dk, dv, code, 0), dev, "lin_prefill")
         _check(lib.lin_prefill(*ptrs, o.data_ptr(), None if sf is None else sf.data_ptr(), B, T, H,
                                dk, dv, code, ws.data_ptr(), nws, _raw(dev, stream)))
     return o, sf
@@ -568,7 +581,7 @@ def lin_decode(q, k, v, decay, state, *, o=None, stream=None):
             _same(v, "v", (N, H, dv), dt, dev), _same(decay, "decay", (H,), torch.float32, dev),
             _same(state, "state", (N, H, dv, dk), torch.float32, dev))
     with _on(dev, stream):
-        o = _out(o, "o", (N, H, dv), dt, dev)
+        o = _out_like(o, "o", v)
         _check(lib.lin_decode(*ptrs, o.data_ptr(), N, H, dk, dv, code, _raw(dev, stream)))
     return o
 
@@ -590,8 +603,7 @@ def lin_backward(q, k, v, decay, s0, do, ds_final=None, *, workspace=None, strea
     with _on(dev, stream):
         dq, dk_, dv_ = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
         ds0 = torch.empty(state, dtype=torch.float32, device=dev)
-        ws, nws = _scratch(workspace, lib.gdr_lin_workspace_bytes(B, T, H, dk, dv, code, 1), dev,
-                           "lin_backward")
+        ws, nws = _scratch(workspace, _lin_bytes(B, T, H, dk, dv, code, 1), dev, "lin_backward")
         _check(lib.lin_backward(*ptrs, dq.data_ptr(), dk_.data_ptr(), dv_.data_ptr(),
                                 ds0.data_ptr(), B, T, H, dk, dv, code, ws.data_ptr(), nws,
                                 _raw(dev, stream)))
@@ -640,7 +652,7 @@ def attn_prefill(q, k, v, *, window=0, sinks=0, scale=None, lengths=None, o=None
     lens = _maybe(lengths, "lengths", (B,), torch.int32, dev)
     w, n = _int32(window, "window"), _int32(sinks, "sinks")
     with _on(dev, stream):
-        o = _out(o, "o", (B, Tq, Hq, d), q.dtype, dev)
+        o = _out_like(o, "o", q)
         lse = None if lse is False else _out(lse, "lse", (B, Hq, Tq), torch.float32, dev)
         ws, nws = _scratch(workspace, 256, dev, "attn_prefill")
         _check(lib.attn_prefill(*ptrs, lens, o.data_ptr(), None if lse is None else lse.data_ptr(),
@@ -662,8 +674,8 @@ def attn_backward(q, k, v, o, lse, do, *, window=0, sinks=0, scale=None, lengths
     w, n = _int32(window, "window"), _int32(sinks, "sinks")
     with _on(dev, stream):
         dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-        ws, nws = _scratch(workspace, lib.gdr_attn_workspace_bytes(B, Tq, Tk, Hq, Hkv, d, w, n,
-                                                                   code, 1), dev, "attn_backward")
+        ws, nws = _scratch(workspace, _attn_bytes(B, Tq, Tk, Hq, Hkv, d, w, n, code, 1), dev,
+                           "attn_backward")
         _check(lib.attn_backward(*ptrs, lens, *given, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
                                  B, Tq, Tk, Hq, Hkv, d, w, n,
                                  d ** -0.5 if scale is None else scale, code, ws.data_ptr(), nws,
@@ -715,9 +727,9 @@ def attn_decode(q, k_cache, v_cache, page_table, lengths, *, k=None, v=None, win
     kp, vp = _maybe(k, "k", (N, Hkv, d), dt, dev), _maybe(v, "v", (N, Hkv, d), dt, dev)
     w, s = _int32(window, "window"), _int32(sinks, "sinks")
     with _on(dev, stream):
-        o = _out(o, "o", (N, Hq, d), dt, dev)
-        ws, nws = _scratch(workspace, lib.gdr_attn_decode_workspace_bytes(
-            N, Hq, Hkv, d, page, max_pages, w, s, code), dev, "attn_decode")
+        o = _out_like(o, "o", q)
+        ws, nws = _scratch(workspace, _decode_bytes(N, Hq, Hkv, d, page, max_pages, w, s, code),
+                           dev, "attn_decode")
         _check(lib.attn_decode(qp, kp, vp, *ptrs, lens, o.data_ptr(), N, Hq, Hkv, d, npages, page,
                                max_pages, w, s, d ** -0.5 if scale is None else scale, code,
                                ws.data_ptr(), nws, _raw(dev, stream)))

@@ -20,6 +20,7 @@
 // The join reads parts in order, so results do not depend on scheduling.
 
 #include "attn_common.cuh"
+#include "once.h"
 
 namespace gdr {
 namespace {
@@ -582,8 +583,9 @@ kv_append_kernel(const AppendArgs a) {
 }
 
 template <typename K>
-cudaError_t launch_main(K kern, int smem, const PagedArgs& a, unsigned grid, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+cudaError_t launch_main(K kern, int smem, const PagedArgs& a, unsigned grid, cudaStream_t st,
+                        std::atomic<unsigned long long>& done) {
+  cudaError_t e = allow_smem(kern, smem, done);
   if (e != cudaSuccess) return e;
   kern<<<grid, kWarps * 32, smem, st>>>(a);
   return cudaGetLastError();
@@ -592,14 +594,16 @@ cudaError_t launch_main(K kern, int smem, const PagedArgs& a, unsigned grid, cud
 template <typename T, int D>
 cudaError_t launch_t(const PagedArgs& a, cudaStream_t st) {
   const int G = a.Hq / a.Hkv;
+  static std::atomic<unsigned long long> done{0};
   cudaError_t e;
   if constexpr (sizeof(T) == 2 && D >= 64) {
     const unsigned grid = (unsigned)((size_t)a.N * a.Hkv * ((G + 15) / 16) * a.nsplit);
-    e = launch_main(attn_decode_tc<D>, TcSmem<D>::BYTES, a, grid, st);
+    e = launch_main(attn_decode_tc<D>, TcSmem<D>::BYTES, a, grid, st, done);
   } else {
     const unsigned grid =
         (unsigned)((size_t)a.N * a.Hkv * ((G + kSHeads - 1) / kSHeads) * a.nsplit);
-    e = launch_main(attn_decode_simt<T, D>, (int)sizeof(SimtSmem<T, D>), a, grid, st);
+    e = launch_main(attn_decode_simt<T, D>, (int)sizeof(SimtSmem<T, D>), a, grid, st,
+                    done);
   }
   if (e != cudaSuccess || a.nsplit == 1) return e;
   cudaLaunchConfig_t cfg = {};

@@ -10,6 +10,7 @@
 // Bound: fp32 multiply-adds, 4 d flops a pair forward, 14 d backward (two rebuilds).
 
 #include "attn_common.cuh"
+#include "once.h"
 
 namespace gdr {
 namespace {
@@ -359,7 +360,8 @@ template <typename T, int D>
 cudaError_t forward_t(const AttnArgs& a, cudaStream_t st) {
   auto kern = attn_forward_simt<T, D>;
   constexpr int smem = (int)sizeof(FwdSmem<D>);
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<unsigned long long> done{0};
+  cudaError_t e = allow_smem(kern, smem, done);
   if (e != cudaSuccess) return e;
   kern<<<(unsigned)((a.Tq + kB - 1) / kB * a.Hq * a.B), kThreads, smem, st>>>(a);
   return cudaGetLastError();
@@ -379,9 +381,10 @@ cudaError_t backward_t(const AttnGradArgs& a, cudaStream_t st) {
   constexpr int smem = (int)sizeof(BwdSmem<D>);
   auto kq = attn_dq_simt<T, D>;
   auto kk = attn_dkv_simt<T, D>;
-  cudaError_t e = cudaFuncSetAttribute(kq, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<unsigned long long> done{0}, done2{0};
+  cudaError_t e = allow_smem(kq, smem, done);
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(kk, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    e = allow_smem(kk, smem, done2);
   if (e != cudaSuccess) return e;
   if (a.f.Tq > 0) {
     kq<<<(unsigned)((a.f.Tq + kB - 1) / kB * a.f.Hq * a.f.B), kThreads, smem, st>>>(a);

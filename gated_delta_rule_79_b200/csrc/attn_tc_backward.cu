@@ -23,6 +23,7 @@
 // load of an SM, whose fp32 sums a small kernel adds in order.
 
 #include "attn_tc.cuh"
+#include "once.h"
 #include "tma_host.h"
 
 namespace gdr {
@@ -606,9 +607,10 @@ cudaError_t launch_t(const AttnGradArgs& a, cudaStream_t st) {
     return cudaErrorInvalidValue;
   auto kq = attn_dq_tc<D>;
   auto kk = attn_dkv_tc<D>;
-  cudaError_t e = cudaFuncSetAttribute(kq, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
+  static std::atomic<unsigned long long> done{0}, done2{0};
+  cudaError_t e = allow_smem(kq, L::SMEM, done);
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(kk, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
+    e = allow_smem(kk, L::SMEM, done2);
   if (e != cudaSuccess) return e;
   const uint32_t spin = attn_spin_limit();
   const Parts p = plan_parts(f);

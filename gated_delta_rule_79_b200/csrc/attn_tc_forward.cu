@@ -21,6 +21,7 @@
 // Waits are bounded: a give-up sets the status word, drains what is in flight and ends the CTA.
 
 #include "attn_tc.cuh"
+#include "once.h"
 #include "tma_host.h"
 
 namespace gdr {
@@ -341,7 +342,8 @@ cudaError_t launch_t(const AttnArgs& a, cudaStream_t st) {
     return cudaErrorInvalidValue;
   auto kern = attn_forward_tc<D>;
   constexpr int smem = FwdLayout<D>::SMEM;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<unsigned long long> done{0};
+  cudaError_t e = allow_smem(kern, smem, done);
   if (e != cudaSuccess) return e;
   const unsigned grid = (unsigned)((a.Tq + 2 * kT - 1) / (2 * kT) * a.Hq * a.B);
   kern<<<grid, kWarpsF * 32, smem, st>>>(mq, mk, mv, a, attn_spin_limit());

@@ -8,6 +8,7 @@
 // S q.  Bound: fp32 multiply-adds, 2 (2 d_k d_v + 16 (d_k + d_v)) flops a token.
 
 #include "lin_common.cuh"
+#include "once.h"
 
 namespace gdr {
 namespace {
@@ -253,7 +254,8 @@ cudaError_t launch_t(const LinScan& sc, cudaStream_t st) {
   }
   constexpr int smem = (int)sizeof(OutSmem<DK, DV>);
   auto kern = lin_out_simt<T, DK, DV>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<unsigned long long> done{0};
+  cudaError_t e = allow_smem(kern, smem, done);
   if (e != cudaSuccess) return e;
   kern<<<dim3((unsigned)(sc.B * sc.H * sc.nseg), sc.njobs), kThreads, smem, st>>>(sc);
   return cudaGetLastError();

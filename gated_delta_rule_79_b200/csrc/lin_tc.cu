@@ -33,6 +33,7 @@
 
 #include "attn_tc.cuh"
 #include "lin_common.cuh"
+#include "once.h"
 #include "tma_host.h"
 
 namespace gdr {
@@ -777,11 +778,12 @@ cudaError_t launch_t(const LinScan& sc, cudaStream_t st) {
         !encode_bthd_bf16(&maps.o[j], sc.job[j].o, sc.B, sc.T, sc.H, DV, 64, kC, true))
       return cudaErrorInvalidValue;
   const uint32_t spin = attn_spin_limit();
+  static std::atomic<unsigned long long> done{0}, done2{0};
   cudaError_t e;
   if (sc.nseg > 1) {
     auto kern = lin_segment_tc<DK, DV>;
     constexpr int smem = SegLayout<DK, DV>::SMEM;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    e = allow_smem(kern, smem, done);
     if (e != cudaSuccess) return e;
     kern<<<dim3((unsigned)(sc.B * sc.H * (sc.nseg - 1)), sc.njobs), kSegWarps * 32, smem, st>>>(
         maps, sc, spin);
@@ -789,7 +791,7 @@ cudaError_t launch_t(const LinScan& sc, cudaStream_t st) {
   }
   auto kern = lin_out_tc<DK, DV>;
   constexpr int smem = OutLayout<DK, DV>::SMEM;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  e = allow_smem(kern, smem, done2);
   if (e != cudaSuccess) return e;
   kern<<<dim3((unsigned)(sc.B * sc.H * sc.nseg), sc.njobs), kOutWarps * 32, smem, st>>>(maps, sc,
                                                                                        spin);
