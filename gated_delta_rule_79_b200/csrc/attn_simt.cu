@@ -2,12 +2,17 @@
 // and head size 32 (the tensor-core kernels are attn_tc_forward.cu, attn_tc_backward.cu).
 // The mathematics and the mask are in attn_common.cuh.
 //
-// Tiles of 64 queries x 64 keys, 256 threads as 16 x 16, each with a 4 x 4 piece of the
-// score tile and 4 rows x d/16 columns of the products over it.  One pass over the keys
-// with the running maximum and sum; the backward rebuilds the probabilities from lse, once
-// for dq (a CTA per query tile) and once for dk, dv (a CTA per key tile, which walks the
-// query heads of its group itself, so no sum crosses CTAs and results are deterministic).
-// Bound: fp32 multiply-adds, 4 d flops a pair forward, 14 d backward (two rebuilds).
+// A CTA keeps a tile of 32 rows (queries, or for dk and dv keys) and streams tiles of 64 rows of
+// the other side past it.  Two groups of 128 threads take the streamed tiles in turn, each with
+// its own statistics and sums, which join at the end: one group alone leaves a warp for each
+// scheduler, which issues a multiply-add every other cycle at best.  The threads of a group stand
+// as 8 x 16, each with a 4 x 4 piece of the score tile and 4 rows x d/16 columns of the products
+// over it.  One pass over the keys with the running maximum and sum; the backward rebuilds the
+// probabilities from lse, once for dq and once for dk, dv (a CTA walks the query heads of its
+// group itself, so no sum crosses CTAs and results are deterministic).
+// Bound: fp32 multiply-adds, 4 d flops a pair forward, 14 d backward (two rebuilds).  777 tokens
+// x 6 heads x 3 sequences (d = 64, forward + dk, dv + dq): tiles of 64 rows by 256 threads took
+// 129 + 204 + 162 us, of 32 rows by one group 92 + 155 + 119.
 
 #include "attn_common.cuh"
 #include "once.h"
@@ -17,15 +22,23 @@ namespace {
 
 using namespace attn;
 
-constexpr int kB = 64;          // queries and keys of a tile
-constexpr int kThreads = 256;
+constexpr int kA = 32;          // rows of the tile that stays
+constexpr int kB = 64;          // rows of the tiles that stream
+constexpr int kGroup = 128;     // threads that share a streamed tile
+constexpr int kThreads = 2 * kGroup;
 constexpr int kLd = kB + 4;
 
-// rows r0 .. r0 + 63 of x [rows][heads][D] into dst [64][D + 4], zeros at and past `end`
-template <typename T, int D>
+__device__ __forceinline__ void group_sync(int g) {
+  asm volatile("bar.sync %0, %1;" :: "r"(1 + g), "r"(kGroup) : "memory");
+}
+
+// rows r0 .. r0 + ROWS - 1 of x [rows][heads][D] into dst [ROWS][D + 4], zeros at and past `end`
+// by the threads t of n
+template <typename T, int D, int ROWS, int N>
 __device__ __forceinline__ void load_tile(float* dst, const T* x, size_t row_stride, int r0,
-                                          int end) {
-  for (int e = threadIdx.x; e < kB * (D / 4); e += kThreads) {
+                                          int end, int t) {
+#pragma unroll 4
+  for (int e = t; e < ROWS * (D / 4); e += N) {
     const int r = e / (D / 4), c = (e % (D / 4)) * 4;
     float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
     if (r0 + r < end) f = Elem<T>::load4(x + (size_t)(r0 + r) * row_stride + c);
@@ -58,50 +71,49 @@ __device__ __forceinline__ void tile_dot(const float* x, const float* y, int ty,
   }
 }
 
-// acc[a][..] += sum_j m[4 ty + a][j] y[j][columns of tx]  (columns tx*W + 16*W*g + e)
+// The columns of thread tx: tx W + 16 W g + e, e < W, g < G; W consecutive ones per read.
 template <int D>
 struct Cols {
   static constexpr int N = D / 16, W = N < 4 ? N : 4, G = N / W;
+  static __device__ __forceinline__ void load(const float* row, int tx, float (&v)[N]) {
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const float* p = row + tx * W + 16 * W * g;
+      if constexpr (W == 4) {
+        const float4 f = *reinterpret_cast<const float4*>(p);
+        v[4 * g] = f.x, v[4 * g + 1] = f.y, v[4 * g + 2] = f.z, v[4 * g + 3] = f.w;
+      } else {
+        const float2 f = *reinterpret_cast<const float2*>(p);
+        v[0] = f.x, v[1] = f.y;
+      }
+    }
+  }
 };
+
+// acc[a][..] += sum_j m[4 ty + a][j] y[j][columns of tx]
 template <int D>
 __device__ __forceinline__ void tile_acc(const float* m, const float* y, int ty, int tx,
                                          float (&acc)[4][Cols<D>::N]) {
   using C = Cols<D>;
-#pragma unroll 4
-  for (int j = 0; j < kB; ++j) {
-    float p[4];
+#pragma unroll 2
+  for (int j = 0; j < kB; j += 4) {
+    float p[4][4];
 #pragma unroll
-    for (int a = 0; a < 4; ++a) p[a] = m[(4 * ty + a) * kLd + j];
+    for (int a = 0; a < 4; ++a) {
+      const float4 f = *reinterpret_cast<const float4*>(m + (4 * ty + a) * kLd + j);
+      p[a][0] = f.x, p[a][1] = f.y, p[a][2] = f.z, p[a][3] = f.w;
+    }
 #pragma unroll
-    for (int g = 0; g < C::G; ++g)
+    for (int u = 0; u < 4; ++u) {
+      float v[C::N];
+      C::load(y + (j + u) * (D + 4), tx, v);
 #pragma unroll
-      for (int e = 0; e < C::W; ++e) {
-        const float s = y[j * (D + 4) + tx * C::W + 16 * C::W * g + e];
+      for (int e = 0; e < C::N; ++e)
 #pragma unroll
-        for (int a = 0; a < 4; ++a) acc[a][g * C::W + e] = fmaf(p[a], s, acc[a][g * C::W + e]);
-      }
+        for (int a = 0; a < 4; ++a) acc[a][e] = fmaf(p[a][u], v[e], acc[a][e]);
+    }
   }
 }
-// the same with m transposed: acc[a][..] += sum_i m[i][4 ty + a] y[i][..]
-template <int D>
-__device__ __forceinline__ void tile_acc_t(const float* m, const float* y, int ty, int tx,
-                                           float (&acc)[4][Cols<D>::N]) {
-  using C = Cols<D>;
-#pragma unroll 4
-  for (int i = 0; i < kB; ++i) {
-    const float4 p4 = *reinterpret_cast<const float4*>(m + i * kLd + 4 * ty);
-    const float p[4] = {p4.x, p4.y, p4.z, p4.w};
-#pragma unroll
-    for (int g = 0; g < C::G; ++g)
-#pragma unroll
-      for (int e = 0; e < C::W; ++e) {
-        const float s = y[i * (D + 4) + tx * C::W + 16 * C::W * g + e];
-#pragma unroll
-        for (int a = 0; a < 4; ++a) acc[a][g * C::W + e] = fmaf(p[a], s, acc[a][g * C::W + e]);
-      }
-  }
-}
-
 template <typename T, int D>
 __device__ __forceinline__ void store_rows(T* x, size_t row_stride, int r0, int end, int ty,
                                            int tx, const float (&acc)[4][Cols<D>::N]) {
@@ -133,7 +145,11 @@ __device__ __forceinline__ float row_sum(float x) {
 
 template <int D>
 struct FwdSmem {
-  float q[kB * (D + 4)], k[kB * (D + 4)], v[kB * (D + 4)], p[kB * kLd];
+  float q[kA * (D + 4)];
+  struct {
+    float k[kB * (D + 4)], v[kB * (D + 4)], p[kA * kLd];
+  } g[2];
+  float mx[kA], sum[kA];            // the second group's, for the join
 };
 
 template <typename T, int D>
@@ -141,33 +157,34 @@ __global__ void __launch_bounds__(kThreads)
 attn_forward_simt(const AttnArgs a) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   FwdSmem<D>& sm = *reinterpret_cast<FwdSmem<D>*>(smem_raw);
-  const int nq = (a.Tq + kB - 1) / kB;
-  // the last query tiles see the most keys without a window, so they start first
-  const int qt = nq - 1 - (int)(blockIdx.x % nq);
-  const int bh = blockIdx.x / nq, h = bh % a.Hq, b = bh / a.Hq;
+  const int nq = (a.Tq + kA - 1) / kA;
+  // the last queries see the most keys without a window, so they start first
+  const int bh = blockIdx.x % (a.B * a.Hq), h = bh % a.Hq, b = bh / a.Hq;
+  const int i0 = (nq - 1 - (int)(blockIdx.x / (unsigned)(a.B * a.Hq))) * kA;
   const int hk = h / (a.Hq / a.Hkv);
-  const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
-  const int i0 = qt * kB;
+  const int grp = threadIdx.x / kGroup, tid = threadIdx.x % kGroup, ty = tid >> 4, tx = tid & 15;
   const Mask m = make_mask(a.lengths, b, a.Tq, a.Tk, a.window, a.sinks);
-  const KeyTiles kt = key_tiles<kB>(m, i0, min(i0 + kB, a.Tq) - 1);
+  const KeyTiles kt = key_tiles<kB>(m, i0, min(i0 + kA, a.Tq) - 1);
   const size_t qs = (size_t)a.Hq * D, ks = (size_t)a.Hkv * D;
   const T* q = (const T*)a.q + (size_t)b * a.Tq * qs + (size_t)h * D;
   const T* k = (const T*)a.k + (size_t)b * a.Tk * ks + (size_t)hk * D;
   const T* v = (const T*)a.v + (size_t)b * a.Tk * ks + (size_t)hk * D;
-  load_tile<T, D>(sm.q, q, qs, i0, a.Tq);
+  load_tile<T, D, kA, kThreads>(sm.q, q, qs, i0, a.Tq, threadIdx.x);
+  __syncthreads();
+  auto& st = sm.g[grp];
   float acc[4][Cols<D>::N] = {};
   float mx[4], sum[4];
 #pragma unroll
   for (int r = 0; r < 4; ++r) mx[r] = -INFINITY, sum[r] = 0.f;
   const float c = a.scale * kLog2e;
-  for (int x = 0; x < kt.count(); ++x) {
+  for (int x = grp; x < kt.count(); x += 2) {
     const int j0 = kt.tile(x) * kB;
-    __syncthreads();
-    load_tile<T, D>(sm.k, k, ks, j0, m.len);
-    load_tile<T, D>(sm.v, v, ks, j0, m.len);
-    __syncthreads();
+    group_sync(grp);
+    load_tile<T, D, kB, kGroup>(st.k, k, ks, j0, m.len, tid);
+    load_tile<T, D, kB, kGroup>(st.v, v, ks, j0, m.len, tid);
+    group_sync(grp);
     float g[4][4];
-    tile_dot<D>(sm.q, sm.k, ty, tx, g);
+    tile_dot<D>(sm.q, st.k, ty, tx, g);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int pos = m.off + i0 + 4 * ty + r;
@@ -185,20 +202,44 @@ attn_forward_simt(const AttnArgs a) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float w = exp2f(g[r][e] - base);
-        sm.p[(4 * ty + r) * kLd + tx + 16 * e] = w;
+        st.p[(4 * ty + r) * kLd + tx + 16 * e] = w;
         part += w;
       }
-      sum[r] = fmaf(sum[r], f, row_sum(part));
+      sum[r] = fmaf(sum[r], f, part);       // this thread's columns only, until the end
 #pragma unroll
       for (int e = 0; e < Cols<D>::N; ++e) acc[r][e] *= f;
     }
     __syncwarp();       // a tile row's 16 lanes lie in one warp
-    tile_acc<D>(sm.p, sm.v, ty, tx, acc);
+    tile_acc<D>(st.p, st.v, ty, tx, acc);
   }
+#pragma unroll
+  for (int r = 0; r < 4; ++r) sum[r] = row_sum(sum[r]);
+  // the second group hands over its rows (in its key buffer), the first adds and writes them
+  float* other = sm.g[1].k;
+  if (grp == 1) {
+    group_sync(1);            // all of it is done with the buffer
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      if (tx == 0) sm.mx[4 * ty + r] = mx[r], sm.sum[4 * ty + r] = sum[r];
+#pragma unroll
+      for (int e = 0; e < Cols<D>::N; ++e)
+        other[((4 * ty + r) * Cols<D>::N + e) * 16 + tx] = acc[r][e];
+    }
+  }
+  __syncthreads();
+  if (grp == 1) return;
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     const int i = i0 + 4 * ty + r;
-    const float inv = sum[r] > 0.f || sum[r] != sum[r] ? 1.f / sum[r] : 0.f;
+    const float m2 = sm.mx[4 * ty + r], now = fmaxf(mx[r], m2);
+    const float base = now == -INFINITY ? 0.f : now;
+    const float f1 = exp2f(mx[r] - base), f2 = exp2f(m2 - base);
+    mx[r] = now;
+    sum[r] = fmaf(sum[r], f1, sm.sum[4 * ty + r] * f2);
+#pragma unroll
+    for (int e = 0; e < Cols<D>::N; ++e)
+      acc[r][e] = fmaf(acc[r][e], f1, other[((4 * ty + r) * Cols<D>::N + e) * 16 + tx] * f2);
+    const float inv = sum[r] == 0.f ? 0.f : 1.f / sum[r];
 #pragma unroll
     for (int e = 0; e < Cols<D>::N; ++e) acc[r][e] *= inv;
     if (tx == 0 && i < a.Tq && a.lse)
@@ -209,112 +250,158 @@ attn_forward_simt(const AttnArgs a) {
 }
 
 template <int D>
-struct BwdSmem {
-  float q[kB * (D + 4)], k[kB * (D + 4)], v[kB * (D + 4)], d[kB * (D + 4)];
-  float p[kB * kLd], s[kB * kLd];
-  float lse[kB], delta[kB];
+struct DqSmem {
+  float q[kA * (D + 4)], d[kA * (D + 4)];
+  struct {
+    float k[kB * (D + 4)], v[kB * (D + 4)], s[kA * kLd];
+  } g[2];
 };
 
-// The tile's probabilities (into sm.p when wanted) and score gradients (into sm.s), from
-// the loaded q, k, v, do, lse, delta tiles.
-template <int D, bool KEEP_P>
-__device__ __forceinline__ void tile_grads(BwdSmem<D>& sm, const Mask& m, int i0, int j0,
-                                           float scale, int ty, int tx) {
-  float g[4][4], dp[4][4];
-  tile_dot<D>(sm.q, sm.k, ty, tx, g);
-  tile_dot<D>(sm.d, sm.v, ty, tx, dp);
+// The second group's sums to the first, through `buf`.  Returns whether this is the first.
+template <int N>
+__device__ __forceinline__ bool join_groups(float* buf, int grp, int ty, int tx,
+                                            float (&acc)[4][N]) {
+  __syncthreads();
+  if (grp == 1) {
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int i = 4 * ty + r, pos = m.off + i0 + i;
+    for (int r = 0; r < 4; ++r)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int j = tx + 16 * e;
-      const bool sees = m.sees(pos, j0 + j);
-      const float w = sees ? exp2f((g[r][e] * scale - sm.lse[i]) * kLog2e) : 0.f;
-      if (KEEP_P) sm.p[i * kLd + j] = w;
-      sm.s[i * kLd + j] = sees ? scale * w * (dp[r][e] - sm.delta[i]) : 0.f;
-    }
+      for (int e = 0; e < N; ++e) buf[((4 * ty + r) * N + e) * 16 + tx] = acc[r][e];
   }
-}
-
-template <typename T, int D>
-__device__ __forceinline__ void load_query_side(BwdSmem<D>& sm, const AttnGradArgs& a, int b,
-                                                int h, int i0, int end) {
-  const size_t qs = (size_t)a.f.Hq * D;
-  const size_t at = (size_t)b * a.f.Tq * qs + (size_t)h * D;
-  load_tile<T, D>(sm.q, (const T*)a.f.q + at, qs, i0, end);
-  load_tile<T, D>(sm.d, (const T*)a.dO + at, qs, i0, end);
-  if (threadIdx.x < kB) {
-    const int i = i0 + threadIdx.x;
-    const size_t r = ((size_t)b * a.f.Hq + h) * a.f.Tq + i;
-    sm.lse[threadIdx.x] = i < end ? a.f.lse[r] : 0.f;
-    sm.delta[threadIdx.x] = i < end ? a.delta[r] : 0.f;
+  __syncthreads();
+  if (grp == 0) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int e = 0; e < N; ++e) acc[r][e] += buf[((4 * ty + r) * N + e) * 16 + tx];
   }
+  return grp == 0;
 }
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads)
 attn_dq_simt(const AttnGradArgs a) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
-  BwdSmem<D>& sm = *reinterpret_cast<BwdSmem<D>*>(smem_raw);
-  const int nq = (a.f.Tq + kB - 1) / kB;
-  const int qt = nq - 1 - (int)(blockIdx.x % nq);
-  const int bh = blockIdx.x / nq, h = bh % a.f.Hq, b = bh / a.f.Hq;
-  const int hk = h / (a.f.Hq / a.f.Hkv);
-  const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
-  const int i0 = qt * kB;
-  const Mask m = make_mask(a.f.lengths, b, a.f.Tq, a.f.Tk, a.f.window, a.f.sinks);
-  const KeyTiles kt = key_tiles<kB>(m, i0, min(i0 + kB, a.f.Tq) - 1);
-  const size_t qs = (size_t)a.f.Hq * D, ks = (size_t)a.f.Hkv * D;
-  const size_t kat = (size_t)b * a.f.Tk * ks + (size_t)hk * D;
+  DqSmem<D>& sm = *reinterpret_cast<DqSmem<D>*>(smem_raw);
+  const AttnArgs& f = a.f;
+  const int nq = (f.Tq + kA - 1) / kA;
+  const int bh = blockIdx.x % (f.B * f.Hq), h = bh % f.Hq, b = bh / f.Hq;
+  const int i0 = (nq - 1 - (int)(blockIdx.x / (unsigned)(f.B * f.Hq))) * kA;
+  const int hk = h / (f.Hq / f.Hkv);
+  const int grp = threadIdx.x / kGroup, tid = threadIdx.x % kGroup, ty = tid >> 4, tx = tid & 15;
+  const Mask m = make_mask(f.lengths, b, f.Tq, f.Tk, f.window, f.sinks);
+  const KeyTiles kt = key_tiles<kB>(m, i0, min(i0 + kA, f.Tq) - 1);
+  const size_t qs = (size_t)f.Hq * D, ks = (size_t)f.Hkv * D;
+  const size_t qat = (size_t)b * f.Tq * qs + (size_t)h * D;
+  const size_t kat = (size_t)b * f.Tk * ks + (size_t)hk * D;
   // rows past the length see nothing; their q and do may hold anything
-  load_query_side<T, D>(sm, a, b, h, i0, min(a.f.Tq, m.len - m.off));
-  float acc[4][Cols<D>::N] = {};
-  for (int x = 0; x < kt.count(); ++x) {
-    const int j0 = kt.tile(x) * kB;
-    __syncthreads();
-    load_tile<T, D>(sm.k, (const T*)a.f.k + kat, ks, j0, m.len);
-    load_tile<T, D>(sm.v, (const T*)a.f.v + kat, ks, j0, m.len);
-    __syncthreads();
-    tile_grads<D, false>(sm, m, i0, j0, a.f.scale, ty, tx);
-    __syncwarp();
-    tile_acc<D>(sm.s, sm.k, ty, tx, acc);
+  const int end = min(f.Tq, m.len - m.off);
+  load_tile<T, D, kA, kThreads>(sm.q, (const T*)f.q + qat, qs, i0, end, threadIdx.x);
+  load_tile<T, D, kA, kThreads>(sm.d, (const T*)a.dO + qat, qs, i0, end, threadIdx.x);
+  __syncthreads();
+  auto& st = sm.g[grp];
+  float lse[4], delta[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int i = i0 + 4 * ty + r;
+    const size_t at = ((size_t)b * f.Hq + h) * f.Tq + i;
+    lse[r] = i < end ? f.lse[at] : 0.f;
+    delta[r] = i < end ? a.delta[at] : 0.f;
   }
-  store_rows<T, D>((T*)a.dq + (size_t)b * a.f.Tq * qs + (size_t)h * D, qs, i0, a.f.Tq, ty, tx,
-                   acc);
+  float acc[4][Cols<D>::N] = {};
+  for (int x = grp; x < kt.count(); x += 2) {
+    const int j0 = kt.tile(x) * kB;
+    group_sync(grp);
+    load_tile<T, D, kB, kGroup>(st.k, (const T*)f.k + kat, ks, j0, m.len, tid);
+    load_tile<T, D, kB, kGroup>(st.v, (const T*)f.v + kat, ks, j0, m.len, tid);
+    group_sync(grp);
+    float g[4][4], dp[4][4];
+    tile_dot<D>(sm.q, st.k, ty, tx, g);
+    tile_dot<D>(sm.d, st.v, ty, tx, dp);
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int j = tx + 16 * e;
+        const float w = exp2f((g[r][e] * f.scale - lse[r]) * kLog2e);
+        st.s[(4 * ty + r) * kLd + j] = m.sees(m.off + i0 + 4 * ty + r, j0 + j)
+                                           ? f.scale * w * (dp[r][e] - delta[r]) : 0.f;
+      }
+    __syncwarp();
+    tile_acc<D>(st.s, st.k, ty, tx, acc);
+  }
+  if (join_groups(sm.g[1].k, grp, ty, tx, acc))
+    store_rows<T, D>((T*)a.dq + qat, qs, i0, f.Tq, ty, tx, acc);
 }
+
+template <int D>
+struct DkvSmem {
+  float k[kA * (D + 4)], v[kA * (D + 4)];
+  struct {
+    float q[kB * (D + 4)], d[kB * (D + 4)];
+    float p[kA * kLd], s[kA * kLd];
+    float lse[kB], delta[kB];
+  } g[2];
+};
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads)
 attn_dkv_simt(const AttnGradArgs a) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
-  BwdSmem<D>& sm = *reinterpret_cast<BwdSmem<D>*>(smem_raw);
-  const int nk = (a.f.Tk + kB - 1) / kB;
-  const int kt = blockIdx.x % nk;
-  const int bh = blockIdx.x / nk, hk = bh % a.f.Hkv, b = bh / a.f.Hkv;
-  const int G = a.f.Hq / a.f.Hkv;
-  const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
-  const int j0 = kt * kB;
-  const Mask m = make_mask(a.f.lengths, b, a.f.Tq, a.f.Tk, a.f.window, a.f.sinks);
-  const size_t ks = (size_t)a.f.Hkv * D;
-  const size_t kat = (size_t)b * a.f.Tk * ks + (size_t)hk * D;
-  load_tile<T, D>(sm.k, (const T*)a.f.k + kat, ks, j0, m.len);
-  load_tile<T, D>(sm.v, (const T*)a.f.v + kat, ks, j0, m.len);
+  DkvSmem<D>& sm = *reinterpret_cast<DkvSmem<D>*>(smem_raw);
+  const AttnArgs& f = a.f;
+  // the first keys, which the most queries see without a window, start first
+  const int bh = blockIdx.x % (f.B * f.Hkv), hk = bh % f.Hkv, b = bh / f.Hkv;
+  const int j0 = (int)(blockIdx.x / (unsigned)(f.B * f.Hkv)) * kA;
+  const int G = f.Hq / f.Hkv;
+  const int grp = threadIdx.x / kGroup, tid = threadIdx.x % kGroup, ty = tid >> 4, tx = tid & 15;
+  const Mask m = make_mask(f.lengths, b, f.Tq, f.Tk, f.window, f.sinks);
+  const size_t qs = (size_t)f.Hq * D, ks = (size_t)f.Hkv * D;
+  const size_t kat = (size_t)b * f.Tk * ks + (size_t)hk * D;
+  load_tile<T, D, kA, kThreads>(sm.k, (const T*)f.k + kat, ks, j0, m.len, threadIdx.x);
+  load_tile<T, D, kA, kThreads>(sm.v, (const T*)f.v + kat, ks, j0, m.len, threadIdx.x);
+  __syncthreads();
+  auto& st = sm.g[grp];
   int lo, hi;
-  query_range(m, j0, min(j0 + kB, a.f.Tk) - 1, a.f.Tq, lo, hi);
+  query_range(m, j0, min(j0 + kA, f.Tk) - 1, f.Tq, lo, hi);
+  const int end = min(f.Tq, m.len - m.off);
   float dk[4][Cols<D>::N] = {}, dv[4][Cols<D>::N] = {};
-  for (int g = 0; g < G; ++g)
-    for (int i0 = lo / kB * kB; i0 < hi; i0 += kB) {
-      __syncthreads();
-      load_query_side<T, D>(sm, a, b, hk * G + g, i0, min(a.f.Tq, m.len - m.off));
-      __syncthreads();
-      tile_grads<D, true>(sm, m, i0, j0, a.f.scale, ty, tx);
-      __syncthreads();
-      tile_acc_t<D>(sm.p, sm.d, ty, tx, dv);
-      tile_acc_t<D>(sm.s, sm.q, ty, tx, dk);
+  const int first = lo / kB, nt = hi > lo ? (hi + kB - 1) / kB - first : 0;
+  for (int x = grp; x < G * nt; x += 2) {
+    const int h = hk * G + x / nt, i0 = (first + x % nt) * kB;
+    const size_t qat = (size_t)b * f.Tq * qs + (size_t)h * D;
+    group_sync(grp);
+    load_tile<T, D, kB, kGroup>(st.q, (const T*)f.q + qat, qs, i0, end, tid);
+    load_tile<T, D, kB, kGroup>(st.d, (const T*)a.dO + qat, qs, i0, end, tid);
+    if (tid < kB) {
+      const size_t at = ((size_t)b * f.Hq + h) * f.Tq + i0 + tid;
+      st.lse[tid] = i0 + tid < end ? f.lse[at] : 0.f;
+      st.delta[tid] = i0 + tid < end ? a.delta[at] : 0.f;
     }
-  store_rows<T, D>((T*)a.dk + kat, ks, j0, a.f.Tk, ty, tx, dk);
-  store_rows<T, D>((T*)a.dv + kat, ks, j0, a.f.Tk, ty, tx, dv);
+    group_sync(grp);
+    float g[4][4], dp[4][4];
+    tile_dot<D>(sm.k, st.q, ty, tx, g);
+    tile_dot<D>(sm.v, st.d, ty, tx, dp);
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = tx + 16 * e, at = (4 * ty + r) * kLd + i;
+        const bool sees = m.sees(m.off + i0 + i, j0 + 4 * ty + r);
+        const float w = sees ? exp2f((g[r][e] * f.scale - st.lse[i]) * kLog2e) : 0.f;
+        st.p[at] = w;
+        st.s[at] = sees ? f.scale * w * (dp[r][e] - st.delta[i]) : 0.f;
+      }
+    __syncwarp();
+    tile_acc<D>(st.p, st.d, ty, tx, dv);
+    tile_acc<D>(st.s, st.q, ty, tx, dk);
+  }
+  const bool mine = join_groups(sm.g[1].q, grp, ty, tx, dk);
+  join_groups(sm.g[1].d, grp, ty, tx, dv);
+  if (mine) {
+    store_rows<T, D>((T*)a.dk + kat, ks, j0, f.Tk, ty, tx, dk);
+    store_rows<T, D>((T*)a.dv + kat, ks, j0, f.Tk, ty, tx, dv);
+  }
 }
 
 // D_i = do_i . o_i: 16 bytes of both rows a thread, four rows in flight.
@@ -363,7 +450,7 @@ cudaError_t forward_t(const AttnArgs& a, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
   cudaError_t e = allow_smem(kern, smem, done);
   if (e != cudaSuccess) return e;
-  kern<<<(unsigned)((a.Tq + kB - 1) / kB * a.Hq * a.B), kThreads, smem, st>>>(a);
+  kern<<<(unsigned)((a.Tq + kA - 1) / kA) * (unsigned)(a.Hq * a.B), kThreads, smem, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -378,19 +465,17 @@ cudaError_t delta_t(const AttnGradArgs& a, cudaStream_t st) {
 
 template <typename T, int D>
 cudaError_t backward_t(const AttnGradArgs& a, cudaStream_t st) {
-  constexpr int smem = (int)sizeof(BwdSmem<D>);
   auto kq = attn_dq_simt<T, D>;
   auto kk = attn_dkv_simt<T, D>;
+  constexpr int sq = (int)sizeof(DqSmem<D>), sk = (int)sizeof(DkvSmem<D>);
   static std::atomic<unsigned long long> done{0}, done2{0};
-  cudaError_t e = allow_smem(kq, smem, done);
+  cudaError_t e = allow_smem(kq, sq, done);
   if (e == cudaSuccess)
-    e = allow_smem(kk, smem, done2);
+    e = allow_smem(kk, sk, done2);
   if (e != cudaSuccess) return e;
-  if (a.f.Tq > 0) {
-    kq<<<(unsigned)((a.f.Tq + kB - 1) / kB * a.f.Hq * a.f.B), kThreads, smem, st>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  }
-  kk<<<(unsigned)((a.f.Tk + kB - 1) / kB * a.f.Hkv * a.f.B), kThreads, smem, st>>>(a);
+  kk<<<(unsigned)((a.f.Tk + kA - 1) / kA) * (unsigned)(a.f.Hkv * a.f.B), kThreads, sk, st>>>(a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  kq<<<(unsigned)((a.f.Tq + kA - 1) / kA) * (unsigned)(a.f.Hq * a.f.B), kThreads, sq, st>>>(a);
   return cudaGetLastError();
 }
 

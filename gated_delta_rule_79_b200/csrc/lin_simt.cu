@@ -169,38 +169,53 @@ lin_out_simt(const LinScan sc) {
     }
     __syncthreads();
     {
-      float o[2][NG][W] = {};
+      float o[2][VPT] = {};
       const int t0 = 2 * ty;
-      for (int c = 0; c < DK; ++c) {
-        const float qa = sm.q[t0][c], qc = sm.q[t0 + 1][c];
+      auto row = [&](const float* r, float (&x)[VPT]) {      // this thread's columns of a row
 #pragma unroll
-        for (int g = 0; g < NG; ++g)
-#pragma unroll
-          for (int e = 0; e < W; ++e) {
-            const float s = sm.st[c][tx * W + 16 * W * g + e];
-            o[0][g][e] = fmaf(qa, s, o[0][g][e]);
-            o[1][g][e] = fmaf(qc, s, o[1][g][e]);
+        for (int g = 0; g < NG; ++g) {
+          if constexpr (W == 4) {
+            const float4 f = *reinterpret_cast<const float4*>(r + tx * 4 + 64 * g);
+            x[4 * g] = f.x, x[4 * g + 1] = f.y, x[4 * g + 2] = f.z, x[4 * g + 3] = f.w;
+          } else {
+            const float2 f = *reinterpret_cast<const float2*>(r + tx * 2);
+            x[0] = f.x, x[1] = f.y;
           }
+        }
+      };
+#pragma unroll 2
+      for (int c = 0; c < DK; c += 4) {
+        const float4 qa = *reinterpret_cast<const float4*>(&sm.q[t0][c]);
+        const float4 qc = *reinterpret_cast<const float4*>(&sm.q[t0 + 1][c]);
+        const float ua[4] = {qa.x, qa.y, qa.z, qa.w}, uc[4] = {qc.x, qc.y, qc.z, qc.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float x[VPT];
+          row(sm.st[c + i], x);
+#pragma unroll
+          for (int e = 0; e < VPT; ++e) {
+            o[0][e] = fmaf(ua[i], x[e], o[0][e]);
+            o[1][e] = fmaf(uc[i], x[e], o[1][e]);
+          }
+        }
       }
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int i = jb.rev ? L - 1 - (t0 + u) : t0 + u;
         const float f = t0 + u < L ? sm.pw[i + E] : 0.f;
 #pragma unroll
-        for (int g = 0; g < NG; ++g)
-#pragma unroll
-          for (int e = 0; e < W; ++e) o[u][g][e] *= f;
+        for (int e = 0; e < VPT; ++e) o[u][e] *= f;
       }
-      for (int j = 0; j < L; ++j) {
+#pragma unroll 4
+      for (int j = 0; j < kC; ++j) {          // rows past L are zero
         const float pa = sm.p[t0][j], pc = sm.p[t0 + 1][j];
+        float x[VPT];
+        row(sm.v[j], x);
 #pragma unroll
-        for (int g = 0; g < NG; ++g)
-#pragma unroll
-          for (int e = 0; e < W; ++e) {
-            const float s = sm.v[j][tx * W + 16 * W * g + e];
-            o[0][g][e] = fmaf(pa, s, o[0][g][e]);
-            o[1][g][e] = fmaf(pc, s, o[1][g][e]);
-          }
+        for (int e = 0; e < VPT; ++e) {
+          o[0][e] = fmaf(pa, x[e], o[0][e]);
+          o[1][e] = fmaf(pc, x[e], o[1][e]);
+        }
       }
 #pragma unroll
       for (int u = 0; u < 2; ++u)
@@ -210,7 +225,7 @@ lin_out_simt(const LinScan sc) {
           for (int g = 0; g < NG; ++g)
 #pragma unroll
             for (int e = 0; e < W; ++e)
-              Elem<T>::store(dst + tx * W + 16 * W * g + e, o[u][g][e]);
+              Elem<T>::store(dst + tx * W + 16 * W * g + e, o[u][W * g + e]);
         }
     }
     // the chunk's decay as a pair of floats: its rounding would otherwise be the same in
