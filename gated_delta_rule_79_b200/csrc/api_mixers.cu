@@ -66,12 +66,16 @@ bool lin_sizes_ok(int B, int T, int H) {
          (long long)B * T * H <= (1LL << 38);
 }
 
-// How the tokens are cut: into as many segments as bring (batch, head, scan) pairs up to
-// about one CTA for each SM, none below 256 tokens; one segment when the pairs fill the GPU
-// alone, since every segment but the last reads its keys and values once more.
-void lin_cut(long chains, int T, int& seg_len, int& nseg) {
-  long want = kSMs / (chains > 0 ? chains : 1);
-  const long most = ((long)T + 255) / 256;
+bool lin_tc(int dk, int dv, int dtype) { return dtype == GDR_BF16 && dk >= 64 && dv >= 64; }
+
+// How the tokens are cut.  The tensor-core kernels run one CTA on an SM and stream, so the
+// chains (batch, head, scan) are cut until about every SM has one, into no less than 256 tokens;
+// every segment but the last reads its keys and values once more.  The CUDA-core kernels are
+// bound by arithmetic and want several CTAs on an SM, so there four to an SM, from 64 tokens on.
+void lin_cut(long chains, int T, bool tc, int& seg_len, int& nseg) {
+  long want = (tc ? kSMs : 4 * kSMs) / (chains > 0 ? chains : 1);
+  const long least = tc ? 256 : 64;
+  const long most = ((long)T + least - 1) / least;
   if (want > most) want = most;
   if (want < 1) want = 1;
   const long per = (T + want - 1) / want;
@@ -80,17 +84,17 @@ void lin_cut(long chains, int T, int& seg_len, int& nseg) {
   if (nseg < 1) nseg = 1;
 }
 
-size_t lin_part_bytes(int B, int T, int H, int dk, int dv, int njobs) {
+size_t lin_part_bytes(int B, int T, int H, int dk, int dv, int dtype, int njobs) {
   int seg_len, nseg;
-  lin_cut((long)B * H * njobs, T, seg_len, nseg);
+  lin_cut((long)B * H * njobs, T, lin_tc(dk, dv, dtype), seg_len, nseg);
   return (size_t)njobs * B * H * (nseg - 1) * dk * dv * sizeof(float);
 }
 
 cudaError_t run_scans(LinScan& sc, void* workspace, cudaStream_t st) {
   sc.status = (unsigned int*)workspace;
   sc.part = (float*)((unsigned char*)workspace + kStatusBytes);
-  lin_cut((long)sc.B * sc.H * sc.njobs, sc.T, sc.seg_len, sc.nseg);
-  const bool tc = sc.dtype == GDR_BF16 && sc.dk >= 64 && sc.dv >= 64;
+  const bool tc = lin_tc(sc.dk, sc.dv, sc.dtype);
+  lin_cut((long)sc.B * sc.H * sc.njobs, sc.T, tc, sc.seg_len, sc.nseg);
   return tc ? launch_lin_tc(sc, st) : launch_lin_simt(sc, st);
 }
 
@@ -190,11 +194,11 @@ extern "C" {
 
 size_t gdr_lin_workspace_bytes(int B, int T, int H, int dk, int dv, int dtype, int backward) {
   if (!lin_sizes_ok(B, T, H) || !head_ok(dk) || !head_ok(dv) || !dtype_ok(dtype)) return 0;
-  size_t part = lin_part_bytes(B, T, H, dk, dv, 1);
+  size_t part = lin_part_bytes(B, T, H, dk, dv, dtype, 1);
   if (backward) {
     // the scans run together when their head sizes agree, else in two launches
-    const size_t all = dk == dv ? lin_part_bytes(B, T, H, dk, dv, 3)
-                                : lin_part_bytes(B, T, H, dk, dv, 2);
+    const size_t all = dk == dv ? lin_part_bytes(B, T, H, dk, dv, dtype, 3)
+                                : lin_part_bytes(B, T, H, dk, dv, dtype, 2);
     if (all > part) part = all;
   }
   return kStatusBytes + part;

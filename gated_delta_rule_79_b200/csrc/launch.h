@@ -119,11 +119,13 @@ constexpr int kLinMaxJobs = 3;
 struct LinScan {
   LinJob job[kLinMaxJobs];
   const float* decay;   // [H]
-  float* part;          // [njobs, B, H, nseg - 1, dv, dk]: what each segment left
+  float* part;          // [njobs, B, H, nseg - 1, dv, dk]: what each segment left, then the
+                        // state the next one is entered with
   unsigned int* status;
   int njobs, B, T, H, dk, dv, dtype;
   int seg_len, nseg;
 };
+cudaError_t launch_lin_carry(const LinScan& sc, cudaStream_t stream);
 cudaError_t launch_lin_tc(const LinScan& sc, cudaStream_t stream);    // bf16, dk and dv >= 64
 cudaError_t launch_lin_simt(const LinScan& sc, cudaStream_t stream);
 

@@ -23,9 +23,9 @@
 // E = 0 in their first chunk (e0 below), 1 after it.
 //
 // A call is cut along the tokens into nseg segments of seg_len tokens, so that few (batch,
-// head) pairs still fill the GPU: a first kernel forms what each segment but the last
-// leaves in the state, a second one starts every segment from the sum of what entered
-// before it and writes the outputs.
+// head) pairs still fill the GPU: a first kernel forms what each segment but the last leaves in
+// the state, a second one (lin_carry.cu) runs through the segments and turns that into the
+// state each of them is entered with, a third one writes the outputs.
 #pragma once
 
 #include "common.cuh"

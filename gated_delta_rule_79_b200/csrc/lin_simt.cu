@@ -3,9 +3,9 @@
 // passes over the segments are in lin_common.cuh.
 //
 // Chunks of 32 tokens.  A thread of the 16 x 16 grid keeps (d_v / 16) x (d_k / 16) elements
-// of the state in registers, so the rank-32 update of a chunk costs one shared-memory read
-// per 4 to 8 multiply-adds; the outputs' kernel mirrors the state in shared memory for
-// S q.  Bound: fp32 multiply-adds, 2 (2 d_k d_v + 16 (d_k + d_v)) flops a token.
+// of the state in registers; the outputs' kernel mirrors the state in shared memory for S q.
+// Bound: fp32 multiply-adds, 2 (2 d_k d_v + 16 (d_k + d_v)) flops a token, with the reads of the
+// operands from shared memory close behind: four neighbours to a read.
 
 #include "lin_common.cuh"
 #include "once.h"
@@ -18,26 +18,69 @@ using namespace lin;
 constexpr int kC = 32;
 constexpr int kThreads = 256;
 
+// N = D / 16 elements a thread of D: column j of thread tx, four (or two) neighbours at a time,
+// and row i of thread ty, N neighbours.
+template <int D>
+struct Share {
+  static constexpr int N = D / 16, W = N < 4 ? N : 4;
+  static __device__ __forceinline__ int col(int tx, int j) {
+    return tx * W + 16 * W * (j / W) + j % W;
+  }
+  static __device__ __forceinline__ void cols(const float* r, int tx, float (&x)[N]) {
+#pragma unroll
+    for (int j = 0; j < N; j += W) read(r + col(tx, j), &x[j]);
+  }
+  static __device__ __forceinline__ void rows(const float* r, int ty, float (&x)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; i += W) read(r + ty * N + i, &x[i]);
+  }
+
+ private:
+  static __device__ __forceinline__ void read(const float* p, float* x) {
+    if constexpr (W == 4) {
+      const float4 f = *reinterpret_cast<const float4*>(p);
+      x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
+    } else {
+      const float2 f = *reinterpret_cast<const float2*>(p);
+      x[0] = f.x, x[1] = f.y;
+    }
+  }
+};
+
+// S[i][j] += w sum over one token's v_i k_j
+template <int DK, int DV>
+__device__ __forceinline__ void add_token(float (&S)[DV / 16][DK / 16], const float* k,
+                                          const float* v, float w, int ty, int tx) {
+  float kk[DK / 16], vv[DV / 16];
+  Share<DK>::cols(k, tx, kk);
+  Share<DV>::rows(v, ty, vv);
+#pragma unroll
+  for (int j = 0; j < DK / 16; ++j) kk[j] *= w;
+#pragma unroll
+  for (int i = 0; i < DV / 16; ++i)
+#pragma unroll
+    for (int j = 0; j < DK / 16; ++j) S[i][j] = fmaf(vv[i], kk[j], S[i][j]);
+}
+
 // The sum over the segment's tokens of a^(n-1-i) v_i k_i^T.
 template <typename T, int DK, int DV>
 __global__ void __launch_bounds__(kThreads)
 lin_segment_simt(const LinScan sc) {
   const LinJob& jb = sc.job[blockIdx.y];
-  __shared__ float ks[kC][DK + 4], vs[kC][DV + 4], w[kC];
+  __shared__ float ks[kC][DK + 4], vs[kC][DV + 4], near[kC];
   const int p = blockIdx.x % (sc.nseg - 1), bh = blockIdx.x / (sc.nseg - 1);
   const int b = bh / sc.H, h = bh % sc.H;
   const Segment sg = segment(p, jb.rev, sc.T, sc.seg_len, sc.nseg);
   const double l2 = log2_decay(sc.decay[h]);
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+  if (tid < kC) near[tid] = (float)decay_pow(l2, tid);
   float acc[DV / 16][DK / 16] = {};
   const T* kb = (const T*)jb.k + (((size_t)b * sc.T + sg.a) * sc.H + h) * DK;
   const T* vb = (const T*)jb.v + (((size_t)b * sc.T + sg.a) * sc.H + h) * DV;
   for (int x0 = 0; x0 < sg.n; x0 += kC) {
+    const int L = min(kC, sg.n - x0);
+    const float far = (float)decay_pow(l2, jb.rev ? x0 : sg.n - x0 - L);
     __syncthreads();
-    if (tid < kC) {
-      const int x = x0 + tid;
-      w[tid] = x < sg.n ? (float)decay_pow(l2, jb.rev ? x : sg.n - 1 - x) : 0.f;
-    }
     for (int e = tid; e < kC * (DK / 4); e += kThreads) {
       const int r = e / (DK / 4), c = (e % (DK / 4)) * 4;
       float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -51,23 +94,16 @@ lin_segment_simt(const LinScan sc) {
       *reinterpret_cast<float4*>(&vs[r][c]) = f;
     }
     __syncthreads();
-    for (int r = 0; r < kC; ++r) {
-      float kk[DK / 16], wr = w[r];
-#pragma unroll
-      for (int j = 0; j < DK / 16; ++j) kk[j] = ks[r][tx + 16 * j] * wr;
-#pragma unroll
-      for (int i = 0; i < DV / 16; ++i) {
-        const float vv = vs[r][ty + 16 * i];
-#pragma unroll
-        for (int j = 0; j < DK / 16; ++j) acc[i][j] = fmaf(vv, kk[j], acc[i][j]);
-      }
-    }
+#pragma unroll 4
+    for (int r = 0; r < kC; ++r)
+      add_token<DK, DV>(acc, ks[r], vs[r], near[jb.rev ? r : max(L - 1 - r, 0)] * far, ty, tx);
   }
   float* dst = sc.part + (((size_t)blockIdx.y * sc.B * sc.H + bh) * (sc.nseg - 1) + p) * DV * DK;
 #pragma unroll
   for (int i = 0; i < DV / 16; ++i)
 #pragma unroll
-    for (int j = 0; j < DK / 16; ++j) dst[(ty + 16 * i) * DK + tx + 16 * j] = acc[i][j];
+    for (int j = 0; j < DK / 16; ++j)
+      dst[(ty * (DV / 16) + i) * DK + Share<DK>::col(tx, j)] = acc[i][j];
 }
 
 template <int DK, int DV>
@@ -83,7 +119,7 @@ __global__ void __launch_bounds__(kThreads)
 lin_out_simt(const LinScan sc) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   OutSmem<DK, DV>& sm = *reinterpret_cast<OutSmem<DK, DV>*>(smem_raw);
-  constexpr int VPT = DV / 16, W = VPT < 4 ? VPT : 4, NG = VPT / W;
+  constexpr int VPT = DV / 16;
   const LinJob& jb = sc.job[blockIdx.y];
   const int p = blockIdx.x % sc.nseg, bh = blockIdx.x / sc.nseg;
   const int b = bh / sc.H, h = bh % sc.H;
@@ -92,30 +128,20 @@ lin_out_simt(const LinScan sc) {
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
   if (tid <= kC) sm.pw[tid] = (float)decay_pow(l2, tid);
 
-  // state entering the segment: the call's own, decayed over the tokens before, and what
-  // the earlier segments left.  For p = 0 it is used as it is, with e0 below.
+  // state entering the segment: the call's own, or what lin_carry.cu left for this one
   float S[DV / 16][DK / 16] = {};
-  if (jb.s_in) {
-    const float f = p == 0 ? 1.f : (float)decay_pow(l2, (long)sg.before + jb.e0 - 1);
-    const float* s = jb.s_in + (size_t)bh * DV * DK;
+  if (p > 0 || jb.s_in) {
+    const float* s =
+        p == 0 ? jb.s_in + (size_t)bh * DV * DK
+               : sc.part + (((size_t)blockIdx.y * sc.B * sc.H + bh) * (sc.nseg - 1) + p - 1) * DV * DK;
+    const bool turned = p == 0 && jb.s_trans;
 #pragma unroll
     for (int i = 0; i < DV / 16; ++i)
 #pragma unroll
       for (int j = 0; j < DK / 16; ++j) {
-        const int r = ty + 16 * i, c = tx + 16 * j;
-        S[i][j] = f * s[jb.s_trans ? c * DV + r : r * DK + c];
+        const int r = ty * (DV / 16) + i, c = Share<DK>::col(tx, j);
+        S[i][j] = s[turned ? c * DV + r : r * DK + c];
       }
-  }
-  for (int m = 0; m < p; ++m) {
-    const Segment pm = segment(m, jb.rev, sc.T, sc.seg_len, sc.nseg);
-    const float f = (float)decay_pow(l2, (long)sg.before - pm.before - pm.n);
-    const float* s =
-        sc.part + (((size_t)blockIdx.y * sc.B * sc.H + bh) * (sc.nseg - 1) + m) * DV * DK;
-#pragma unroll
-    for (int i = 0; i < DV / 16; ++i)
-#pragma unroll
-      for (int j = 0; j < DK / 16; ++j)
-        S[i][j] = fmaf(f, s[(ty + 16 * i) * DK + tx + 16 * j], S[i][j]);
   }
 
   const size_t row0 = ((size_t)b * sc.T + sg.a) * sc.H + h;
@@ -148,11 +174,13 @@ lin_out_simt(const LinScan sc) {
 #pragma unroll
     for (int i = 0; i < DV / 16; ++i)
 #pragma unroll
-      for (int j = 0; j < DK / 16; ++j) sm.st[tx + 16 * j][ty + 16 * i] = S[i][j];
+      for (int j = 0; j < DK / 16; ++j)
+        sm.st[Share<DK>::col(tx, j)][ty * (DV / 16) + i] = S[i][j];
     __syncthreads();
     {
       const int t = tid >> 3, j0 = tid & 7;
       float g[4] = {};
+#pragma unroll 4
       for (int c = 0; c < DK; c += 4) {
         const float4 a = *reinterpret_cast<const float4*>(&sm.q[t][c]);
 #pragma unroll
@@ -171,19 +199,7 @@ lin_out_simt(const LinScan sc) {
     {
       float o[2][VPT] = {};
       const int t0 = 2 * ty;
-      auto row = [&](const float* r, float (&x)[VPT]) {      // this thread's columns of a row
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          if constexpr (W == 4) {
-            const float4 f = *reinterpret_cast<const float4*>(r + tx * 4 + 64 * g);
-            x[4 * g] = f.x, x[4 * g + 1] = f.y, x[4 * g + 2] = f.z, x[4 * g + 3] = f.w;
-          } else {
-            const float2 f = *reinterpret_cast<const float2*>(r + tx * 2);
-            x[0] = f.x, x[1] = f.y;
-          }
-        }
-      };
-#pragma unroll 2
+#pragma unroll 4
       for (int c = 0; c < DK; c += 4) {
         const float4 qa = *reinterpret_cast<const float4*>(&sm.q[t0][c]);
         const float4 qc = *reinterpret_cast<const float4*>(&sm.q[t0 + 1][c]);
@@ -191,7 +207,7 @@ lin_out_simt(const LinScan sc) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           float x[VPT];
-          row(sm.st[c + i], x);
+          Share<DV>::cols(sm.st[c + i], tx, x);
 #pragma unroll
           for (int e = 0; e < VPT; ++e) {
             o[0][e] = fmaf(ua[i], x[e], o[0][e]);
@@ -210,7 +226,7 @@ lin_out_simt(const LinScan sc) {
       for (int j = 0; j < kC; ++j) {          // rows past L are zero
         const float pa = sm.p[t0][j], pc = sm.p[t0 + 1][j];
         float x[VPT];
-        row(sm.v[j], x);
+        Share<DV>::cols(sm.v[j], tx, x);
 #pragma unroll
         for (int e = 0; e < VPT; ++e) {
           o[0][e] = fmaf(pa, x[e], o[0][e]);
@@ -222,10 +238,8 @@ lin_out_simt(const LinScan sc) {
         if (t0 + u < L) {
           T* dst = ob + (size_t)(x0 + t0 + u) * sc.H * DV;
 #pragma unroll
-          for (int g = 0; g < NG; ++g)
-#pragma unroll
-            for (int e = 0; e < W; ++e)
-              Elem<T>::store(dst + tx * W + 16 * W * g + e, o[u][W * g + e]);
+          for (int e = 0; e < VPT; ++e)
+            Elem<T>::store(dst + Share<DV>::col(tx, e), o[u][e]);
         }
     }
     // the chunk's decay as a pair of floats: its rounding would otherwise be the same in
@@ -236,18 +250,9 @@ lin_out_simt(const LinScan sc) {
     for (int i = 0; i < DV / 16; ++i)
 #pragma unroll
       for (int j = 0; j < DK / 16; ++j) S[i][j] = fmaf(fh, S[i][j], fl * S[i][j]);
-    for (int r = 0; r < L; ++r) {
-      const float wr = sm.pw[jb.rev ? r : L - 1 - r];
-      float kk[DK / 16];
-#pragma unroll
-      for (int j = 0; j < DK / 16; ++j) kk[j] = sm.k[r][tx + 16 * j] * wr;
-#pragma unroll
-      for (int i = 0; i < DV / 16; ++i) {
-        const float vv = sm.v[r][ty + 16 * i];
-#pragma unroll
-        for (int j = 0; j < DK / 16; ++j) S[i][j] = fmaf(vv, kk[j], S[i][j]);
-      }
-    }
+#pragma unroll 4
+    for (int r = 0; r < kC; ++r)            // rows past L are zero
+      add_token<DK, DV>(S, sm.k[r], sm.v[r], sm.pw[jb.rev ? r : max(L - 1 - r, 0)], ty, tx);
   }
   if (jb.s_out && p == sc.nseg - 1) {
     const float f = (float)decay_pow(l2, 1 - jb.e0);
@@ -255,7 +260,8 @@ lin_out_simt(const LinScan sc) {
 #pragma unroll
     for (int i = 0; i < DV / 16; ++i)
 #pragma unroll
-      for (int j = 0; j < DK / 16; ++j) s[(ty + 16 * i) * DK + tx + 16 * j] = f * S[i][j];
+      for (int j = 0; j < DK / 16; ++j)
+        s[(ty * (DV / 16) + i) * DK + Share<DK>::col(tx, j)] = f * S[i][j];
   }
 }
 
@@ -265,6 +271,7 @@ cudaError_t launch_t(const LinScan& sc, cudaStream_t st) {
     lin_segment_simt<T, DK, DV>
         <<<dim3((unsigned)(sc.B * sc.H * (sc.nseg - 1)), sc.njobs), kThreads, 0, st>>>(sc);
     cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess) e = launch_lin_carry(sc, st);
     if (e != cudaSuccess) return e;
   }
   constexpr int smem = (int)sizeof(OutSmem<DK, DV>);

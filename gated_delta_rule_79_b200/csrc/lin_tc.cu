@@ -461,45 +461,26 @@ lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin
     constexpr int DH = DK / 2;
     const int v = (warp & 3) * 32 + lane, col = warp < 4 ? 0 : DH;
     const uint32_t tl = (uint32_t)((warp & 3) * 32) << 16;
-    // entering: the call's own state decayed over the tokens before, and what the earlier
-    // segments left
+    // entering: the call's own state, or what lin_carry.cu left for this segment
     float S[DH];
 #pragma unroll
     for (int e = 0; e < DH; ++e) S[e] = 0.f;
-    if (v < DV) {
-      const LinJob& jb = sc.job[job];
-      const size_t at = (size_t)bh * DV * DK;
-      if (jb.s_in) {
-        const float f = p == 0 ? 1.f : (float)decay_pow(l2, (long)sg.before + e0 - 1);
-        if (jb.s_trans) {
+    const LinJob& jb = sc.job[job];
+    if (v < DV && (p > 0 || jb.s_in)) {
+      const float* s =
+          p == 0 ? jb.s_in + (size_t)bh * DV * DK
+                 : sc.part + (((size_t)job * sc.B * sc.H + bh) * (sc.nseg - 1) + p - 1) * DV * DK;
+      if (p == 0 && jb.s_trans) {
 #pragma unroll
-          for (int e = 0; e < DH; ++e) S[e] = f * jb.s_in[at + (size_t)(col + e) * DV + v];
-        } else {
-#pragma unroll
-          for (int e = 0; e < DH / 4; ++e) {
-            const float4 y =
-                *reinterpret_cast<const float4*>(jb.s_in + at + (size_t)v * DK + col + 4 * e);
-            S[4 * e] = f * y.x;
-            S[4 * e + 1] = f * y.y;
-            S[4 * e + 2] = f * y.z;
-            S[4 * e + 3] = f * y.w;
-          }
-        }
-      }
-      const float* part = sc.part +
-                          ((size_t)job * sc.B * sc.H + bh) * (sc.nseg - 1) * DV * DK +
-                          (size_t)v * DK + col;
-      for (int m = 0; m < p; ++m) {
-        const Segment pm = segment(m, rev, sc.T, sc.seg_len, sc.nseg);
-        const float f = (float)decay_pow(l2, (long)sg.before - pm.before - pm.n);
-        const float* s = part + (size_t)m * DV * DK;
+        for (int e = 0; e < DH; ++e) S[e] = s[(size_t)(col + e) * DV + v];
+      } else {
 #pragma unroll
         for (int e = 0; e < DH / 4; ++e) {
-          const float4 y = *reinterpret_cast<const float4*>(s + 4 * e);
-          S[4 * e] = fmaf(f, y.x, S[4 * e]);
-          S[4 * e + 1] = fmaf(f, y.y, S[4 * e + 1]);
-          S[4 * e + 2] = fmaf(f, y.z, S[4 * e + 2]);
-          S[4 * e + 3] = fmaf(f, y.w, S[4 * e + 3]);
+          const float4 y = *reinterpret_cast<const float4*>(s + (size_t)v * DK + col + 4 * e);
+          S[4 * e] = y.x;
+          S[4 * e + 1] = y.y;
+          S[4 * e + 2] = y.z;
+          S[4 * e + 3] = y.w;
         }
       }
     }
@@ -787,7 +768,9 @@ cudaError_t launch_t(const LinScan& sc, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     kern<<<dim3((unsigned)(sc.B * sc.H * (sc.nseg - 1)), sc.njobs), kSegWarps * 32, smem, st>>>(
         maps, sc, spin);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    e = cudaGetLastError();
+    if (e == cudaSuccess) e = launch_lin_carry(sc, st);
+    if (e != cudaSuccess) return e;
   }
   auto kern = lin_out_tc<DK, DV>;
   constexpr int smem = OutLayout<DK, DV>::SMEM;
