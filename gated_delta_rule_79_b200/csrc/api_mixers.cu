@@ -87,7 +87,7 @@ void lin_cut(long chains, int T, bool tc, int& seg_len, int& nseg) {
 size_t lin_part_bytes(int B, int T, int H, int dk, int dv, int dtype, int njobs) {
   int seg_len, nseg;
   lin_cut((long)B * H * njobs, T, lin_tc(dk, dv, dtype), seg_len, nseg);
-  return (size_t)njobs * B * H * (nseg - 1) * dk * dv * sizeof(float);
+  return nseg > 1 ? (size_t)njobs * B * H * nseg * dk * dv * sizeof(float) : 0;
 }
 
 cudaError_t run_scans(LinScan& sc, void* workspace, cudaStream_t st) {
@@ -95,6 +95,7 @@ cudaError_t run_scans(LinScan& sc, void* workspace, cudaStream_t st) {
   sc.part = (float*)((unsigned char*)workspace + kStatusBytes);
   const bool tc = lin_tc(sc.dk, sc.dv, sc.dtype);
   lin_cut((long)sc.B * sc.H * sc.njobs, sc.T, tc, sc.seg_len, sc.nseg);
+  sc.part_rows = !tc;
   return tc ? launch_lin_tc(sc, st) : launch_lin_simt(sc, st);
 }
 

@@ -119,8 +119,9 @@ constexpr int kLinMaxJobs = 3;
 struct LinScan {
   LinJob job[kLinMaxJobs];
   const float* decay;   // [H]
-  float* part;          // [njobs, B, H, nseg - 1, dv, dk]: what each segment left, then the
-                        // state the next one is entered with
+  float* part;          // nseg > 1: [njobs, B, H, nseg] states: in slot p + 1 what segment p left,
+                        // then in slot p the state that segment p is entered with
+  int part_rows;        // 1: the states in part lie row by row; 0: as lin::part_at says
   unsigned int* status;
   int njobs, B, T, H, dk, dv, dtype;
   int seg_len, nseg;

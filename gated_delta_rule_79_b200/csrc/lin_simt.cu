@@ -73,6 +73,7 @@ lin_segment_simt(const LinScan sc) {
   const Segment sg = segment(p, jb.rev, sc.T, sc.seg_len, sc.nseg);
   const double l2 = log2_decay(sc.decay[h]);
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+  let_next_start();
   if (tid < kC) near[tid] = (float)decay_pow(l2, tid);
   float acc[DV / 16][DK / 16] = {};
   const T* kb = (const T*)jb.k + (((size_t)b * sc.T + sg.a) * sc.H + h) * DK;
@@ -98,7 +99,7 @@ lin_segment_simt(const LinScan sc) {
     for (int r = 0; r < kC; ++r)
       add_token<DK, DV>(acc, ks[r], vs[r], near[jb.rev ? r : max(L - 1 - r, 0)] * far, ty, tx);
   }
-  float* dst = sc.part + (((size_t)blockIdx.y * sc.B * sc.H + bh) * (sc.nseg - 1) + p) * DV * DK;
+  float* dst = sc.part + (((size_t)blockIdx.y * sc.B * sc.H + bh) * sc.nseg + p + 1) * DV * DK;
 #pragma unroll
   for (int i = 0; i < DV / 16; ++i)
 #pragma unroll
@@ -128,19 +129,21 @@ lin_out_simt(const LinScan sc) {
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
   if (tid <= kC) sm.pw[tid] = (float)decay_pow(l2, tid);
 
-  // state entering the segment: the call's own, or what lin_carry.cu left for this one
+  // state entering the segment: what lin_carry.cu left for it, or the call's own if it is the
+  // only one
+  wait_for_previous();
   float S[DV / 16][DK / 16] = {};
-  if (p > 0 || jb.s_in) {
+  const bool parts = sc.nseg > 1;
+  if (parts || jb.s_in) {
     const float* s =
-        p == 0 ? jb.s_in + (size_t)bh * DV * DK
-               : sc.part + (((size_t)blockIdx.y * sc.B * sc.H + bh) * (sc.nseg - 1) + p - 1) * DV * DK;
-    const bool turned = p == 0 && jb.s_trans;
+        parts ? sc.part + (((size_t)blockIdx.y * sc.B * sc.H + bh) * sc.nseg + p) * DV * DK
+              : jb.s_in + (size_t)bh * DV * DK;
 #pragma unroll
     for (int i = 0; i < DV / 16; ++i)
 #pragma unroll
       for (int j = 0; j < DK / 16; ++j) {
         const int r = ty * (DV / 16) + i, c = Share<DK>::col(tx, j);
-        S[i][j] = s[turned ? c * DV + r : r * DK + c];
+        S[i][j] = s[!parts && jb.s_trans ? c * DV + r : r * DK + c];
       }
   }
 
@@ -279,7 +282,9 @@ cudaError_t launch_t(const LinScan& sc, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
   cudaError_t e = allow_smem(kern, smem, done);
   if (e != cudaSuccess) return e;
-  kern<<<dim3((unsigned)(sc.B * sc.H * sc.nseg), sc.njobs), kThreads, smem, st>>>(sc);
+  const dim3 grid((unsigned)(sc.B * sc.H * sc.nseg), sc.njobs);
+  if (sc.nseg > 1) return launch_after(kern, grid, kThreads, smem, st, sc);
+  kern<<<grid, kThreads, smem, st>>>(sc);
   return cudaGetLastError();
 }
 

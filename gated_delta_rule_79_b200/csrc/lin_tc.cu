@@ -240,6 +240,7 @@ lin_segment_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t 
     ss.abort = 0;
     fence_mbar_init();
   }
+  let_next_start();
   if (tid < 2 * kC)
     tab.wt[tid / kC][tid % kC] =
         row_weight(l2, rev, tid < kC ? kC : sg.n - (nch - 1) * kC, tid % kC);
@@ -278,11 +279,10 @@ lin_segment_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t 
       if (lane == 0) mbar_arrive(mb(ss.kv_free[w]));
     }
     if (ok && v < DV) {
-      float* dst = sc.part + (((size_t)job * sc.B * sc.H + bh) * (sc.nseg - 1) + p) * DV * DK +
-                   (size_t)v * DK;
+      float* dst = sc.part + (((size_t)job * sc.B * sc.H + bh) * sc.nseg + p + 1) * DV * DK;
 #pragma unroll
       for (int e = 0; e < DK / 4; ++e)
-        reinterpret_cast<float4*>(dst)[e] =
+        *reinterpret_cast<float4*>(dst + part_at(DV, v, 4 * e)) =
             make_float4(S[4 * e], S[4 * e + 1], S[4 * e + 2], S[4 * e + 3]);
     }
   } else if (warp < 12) {
@@ -461,16 +461,28 @@ lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin
     constexpr int DH = DK / 2;
     const int v = (warp & 3) * 32 + lane, col = warp < 4 ? 0 : DH;
     const uint32_t tl = (uint32_t)((warp & 3) * 32) << 16;
-    // entering: the call's own state, or what lin_carry.cu left for this segment
+    // entering: what lin_carry.cu left for this segment, or the call's own state if it is the
+    // only one
     float S[DH];
 #pragma unroll
     for (int e = 0; e < DH; ++e) S[e] = 0.f;
     const LinJob& jb = sc.job[job];
-    if (v < DV && (p > 0 || jb.s_in)) {
-      const float* s =
-          p == 0 ? jb.s_in + (size_t)bh * DV * DK
-                 : sc.part + (((size_t)job * sc.B * sc.H + bh) * (sc.nseg - 1) + p - 1) * DV * DK;
-      if (p == 0 && jb.s_trans) {
+    if (sc.nseg > 1) {
+      wait_for_previous();
+      const float* s = sc.part + (((size_t)job * sc.B * sc.H + bh) * sc.nseg + p) * DV * DK;
+      if (v < DV) {
+#pragma unroll
+        for (int e = 0; e < DH / 4; ++e) {
+          const float4 y = *reinterpret_cast<const float4*>(s + part_at(DV, v, col + 4 * e));
+          S[4 * e] = y.x;
+          S[4 * e + 1] = y.y;
+          S[4 * e + 2] = y.z;
+          S[4 * e + 3] = y.w;
+        }
+      }
+    } else if (v < DV && jb.s_in) {
+      const float* s = jb.s_in + (size_t)bh * DV * DK;
+      if (jb.s_trans) {
 #pragma unroll
         for (int e = 0; e < DH; ++e) S[e] = s[(size_t)(col + e) * DV + v];
       } else {
@@ -776,8 +788,9 @@ cudaError_t launch_t(const LinScan& sc, cudaStream_t st) {
   constexpr int smem = OutLayout<DK, DV>::SMEM;
   e = allow_smem(kern, smem, done2);
   if (e != cudaSuccess) return e;
-  kern<<<dim3((unsigned)(sc.B * sc.H * sc.nseg), sc.njobs), kOutWarps * 32, smem, st>>>(maps, sc,
-                                                                                       spin);
+  const dim3 grid((unsigned)(sc.B * sc.H * sc.nseg), sc.njobs);
+  if (sc.nseg > 1) return launch_after(kern, grid, kOutWarps * 32, smem, st, maps, sc, spin);
+  kern<<<grid, kOutWarps * 32, smem, st>>>(maps, sc, spin);
   return cudaGetLastError();
 }
 

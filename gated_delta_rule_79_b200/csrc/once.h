@@ -21,4 +21,22 @@ inline cudaError_t allow_smem(K kern, int bytes, std::atomic<unsigned long long>
   return e;
 }
 
+// Launches `kern` so that its blocks may start before the kernel before it in the stream has
+// finished; the kernel itself waits (griddepcontrol.wait) before it reads what that one wrote.
+template <typename... P, typename... A>
+inline cudaError_t launch_after(void (*kern)(P...), dim3 grid, int threads, int smem,
+                                cudaStream_t st, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads, 1, 1);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 }  // namespace gdr

@@ -74,6 +74,19 @@ def test_prefill_carries_in_place_and_in_parts():
     assert torch.allclose(S, s, atol=1e-3)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_segments_with_the_state_carried_in_place(dtype):
+    """The last segment writes the final state over the entering one, which the first segment
+    reads."""
+    import gated_delta_rule_79_b200 as g
+    q, k, v, a, s0 = _cuda(*_inputs(1, 1500, 2, 128, 128, dtype))
+    o, s = g.lin_prefill(q, k, v, a, s0)
+    for _ in range(5):
+        S = s0.clone()
+        o2, _ = g.lin_prefill(q, k, v, a, S, s_final=S)
+        assert torch.equal(o, o2) and torch.equal(S, s)
+
+
 def test_no_tokens():
     import gated_delta_rule_79_b200 as g
     q, k, v, a, s0 = _cuda(*_inputs(2, 0, 3, 64, 32, "bf16"))
