@@ -161,17 +161,18 @@ __device__ __forceinline__ void weigh_values(const uint32_t (&row)[2], uint32_t 
     }
 }
 
-// One half chunk's share of KV = V~^T K: six products (A in tensor memory, B the K tile).
-template <int DK>
-__device__ __forceinline__ void issue_kv(uint32_t d, uint32_t vw, uint32_t k_tile, int half) {
-  constexpr uint32_t id = idesc_bf16_mn(128, DK);
-  const uint64_t kb = mn_base(k_tile, DK == 128) + mn_step(2) * half;
+// The share of token half t in KV = V~^T K (A in tensor memory, B the K tile), NH panels of 64
+// key channels from panel h on.
+template <int NH>
+__device__ __forceinline__ void issue_kv(uint32_t d, uint32_t vw, uint32_t k_tile, int t, int h) {
+  constexpr uint32_t id = idesc_bf16_mn(128, 64 * NH);
+  const uint64_t kb = mn_base(k_tile + h * kC * 128, NH == 2) + mn_step(2) * t;
 #pragma unroll
-  for (int t = 2; t >= 0; --t)
+  for (int s = 2; s >= 0; --s)
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks)
-      mma_bf16_ta_w(d, vw + 48 * half + 16 * t + 8 * ks, kb + mn_step(ks), id,
-                    half > 0 || t < 2 || ks > 0);
+      mma_bf16_ta_w(d + 64 * h, vw + 48 * t + 16 * s + 8 * ks, kb + mn_step(ks), id,
+                    t > 0 || s < 2 || ks > 0);
 }
 
 struct LinMaps {
@@ -315,8 +316,8 @@ lin_segment_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t 
         if (!wait(mb(ss.vw_full[w]), (uint32_t)(c >> 1) & 1u)) break;
         if (c >= 2 && !wait(mb(ss.kv_free[w]), (uint32_t)((c - 2) >> 1) & 1u)) break;
         fence_after_sync();
-        issue_kv<DK>(tb + L::KV + 128 * w, tb + L::VW + 96 * w, sb + s * L::STAGE, 0);
-        issue_kv<DK>(tb + L::KV + 128 * w, tb + L::VW + 96 * w, sb + s * L::STAGE, 1);
+        issue_kv<DK / 64>(tb + L::KV + 128 * w, tb + L::VW + 96 * w, sb + s * L::STAGE, 0, 0);
+        issue_kv<DK / 64>(tb + L::KV + 128 * w, tb + L::VW + 96 * w, sb + s * L::STAGE, 1, 0);
         mma_commit_w(mb(ss.kv_done[w]));
         mma_commit_w(mb(ss.empty[s]));
       }
@@ -381,8 +382,8 @@ struct OutLayout {
 };
 struct OutSmall {
   unsigned long long full[4], empty[4];
-  unsigned long long g_full, p_full[2], vw_full[2], vw_free, kv_done, kv_free, s_ready, o1_done,
-      o_full, o_free, drained[2];
+  unsigned long long g_full, p_full[2], vw_full[2], vw_free[2], kv_done[2], kv_free[2], s_ready,
+      o1_done, o_full, o_free, drained[2];
   uint32_t tmem;
   int abort;
 };
@@ -420,11 +421,11 @@ lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin
       mbar_init(mb(os.p_full[s]), 4);
       mbar_init(mb(os.drained[s]), 1);
       mbar_init(mb(os.vw_full[s]), 4);
+      mbar_init(mb(os.vw_free[s]), 1);
+      mbar_init(mb(os.kv_done[s]), 1);
+      mbar_init(mb(os.kv_free[s]), 4);
     }
     mbar_init(mb(os.g_full), 1);
-    mbar_init(mb(os.vw_free), 1);
-    mbar_init(mb(os.kv_done), 1);
-    mbar_init(mb(os.kv_free), 8);
     mbar_init(mb(os.s_ready), 8);
     mbar_init(mb(os.o1_done), 1);
     mbar_init(mb(os.o_full), 1);
@@ -458,8 +459,10 @@ lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin
   if (warp < 8) {
     more_registers<112>();
     // ---- the state: a thread has a row's first or second half ------------------------------
+    // (with d_k = 64 the two halves are in one panel of KV, which both wait for)
     constexpr int DH = DK / 2;
-    const int v = (warp & 3) * 32 + lane, col = warp < 4 ? 0 : DH;
+    const int v = (warp & 3) * 32 + lane, hf = warp < 4 ? 0 : 1, col = hf * DH;
+    const int pn = DK == 128 ? hf : 0;
     const uint32_t tl = (uint32_t)((warp & 3) * 32) << 16;
     // entering: what lin_carry.cu left for this segment, or the call's own state if it is the
     // only one
@@ -526,7 +529,7 @@ lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin
         steps = now;
       }
       const float2 fh2 = make_float2(fh, fh), fl2 = make_float2(fl, fl);
-      if (!(ok = wait(mb(os.kv_done), (uint32_t)c & 1u))) break;
+      if (!(ok = wait(mb(os.kv_done[pn]), (uint32_t)c & 1u))) break;
       fence_after_sync();
 #pragma unroll
       for (int q = 0; q < DH / 32; ++q) {
@@ -536,7 +539,7 @@ lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin
         if (q == DH / 32 - 1) {
           fence_before_sync();
           __syncwarp();
-          if (lane == 0) mbar_arrive(mb(os.kv_free));
+          if (lane == 0) mbar_arrive(mb(os.kv_free[hf]));
         }
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
@@ -567,8 +570,8 @@ lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin
       const int ragged = sg.n - chunk_at(c) < kC;
       if (c == 0 || ragged || (rev && c == 1)) tw.load(tab.rows.wt[ragged] + 16 * p0, lane);
       if (!wait(mb(os.full[s]), (uint32_t)(c / NS) & 1u)) break;
-      // the product of the chunk before has read this half
-      if (c > 0 && !wait(mb(half ? os.kv_done : os.vw_free), (uint32_t)(c - 1) & 1u)) break;
+      // the products of the chunk before have read this half
+      if (c > 0 && !wait(mb(os.vw_free[half]), (uint32_t)(c - 1) & 1u)) break;
       fence_after_sync();
       const TileRow<DV> row(sb + s * L::STAGE + 2 * L::KT, warp, lane);
       weigh_values<2>(row.at, tb + tl + L::VW, tw, p0, 1.f);
@@ -713,16 +716,27 @@ lin_out_tc(const __grid_constant__ LinMaps maps, const LinScan sc, uint32_t spin
         const int s = c % NS;
         if (c < nstate) {
           if (!wait(mb(os.full[s]), (uint32_t)(c / NS) & 1u)) break;
-          // the accumulator is free once the state has taken the chunk before
-          if (!wait(mb(os.vw_full[0]), (uint32_t)c & 1u)) break;
-          if (c > 0 && !wait(mb(os.kv_free), (uint32_t)(c - 1) & 1u)) break;
-          fence_after_sync();
-          issue_kv<DK>(tb + L::KV, tb + L::VW, sb + s * L::STAGE + L::KT, 0);
-          mma_commit_w(mb(os.vw_free));
-          if (!wait(mb(os.vw_full[1]), (uint32_t)c & 1u)) break;
-          fence_after_sync();
-          issue_kv<DK>(tb + L::KV, tb + L::VW, sb + s * L::STAGE + L::KT, 1);
-          mma_commit_w(mb(os.kv_done));
+          // In panels of 64 key channels, each free as soon as its half of the state has taken
+          // the chunk before; both panels take a half chunk's V~ before the next, which frees it
+          const uint32_t kt = sb + s * L::STAGE + L::KT;
+          bool ok = true;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (!(ok = ok && wait(mb(os.vw_full[t]), (uint32_t)c & 1u))) break;
+#pragma unroll
+            for (int h = 0; h < DK / 64; ++h) {
+              if (t == 0 && c > 0) {
+                if (!(ok = wait(mb(os.kv_free[h]), (uint32_t)(c - 1) & 1u))) break;
+                if (DK == 64 && !(ok = wait(mb(os.kv_free[1]), (uint32_t)(c - 1) & 1u))) break;
+              }
+              fence_after_sync();
+              issue_kv<1>(tb + L::KV, tb + L::VW, kt, t, h);
+              if (t == 1) mma_commit_w(mb(os.kv_done[h]));
+            }
+            if (!ok) break;
+            mma_commit_w(mb(os.vw_free[t]));
+          }
+          if (!ok) break;
           mma_commit_w(mb(os.empty[s]));
         } else if (lane == 0) {
           mbar_arrive(mb(os.empty[s]));
