@@ -48,6 +48,7 @@ struct BwdLayout {
   // tensor memory
   static constexpr uint32_t TS = 0;                      // S of buffer w at 128 w, dP 64 after
   static constexpr uint32_t TG = 256;                    // dq, or dv and D after it dk
+  static constexpr uint32_t TA = 384;                    // Q, and D / 2 after it dO (dq only)
 };
 
 struct BwdSmall {
@@ -61,9 +62,9 @@ __device__ __forceinline__ uint64_t* mb(unsigned long long& x) {
   return reinterpret_cast<uint64_t*>(&x);
 }
 
-__device__ __forceinline__ uint32_t bwd_setup(BwdSmall& s, int warp) {
+__device__ __forceinline__ uint32_t bwd_setup(BwdSmall& s, int warp, int big_arrivals) {
   if (threadIdx.x == 0) {
-    mbar_init(mb(s.big_full), 1);
+    mbar_init(mb(s.big_full), big_arrivals);
     mbar_init(mb(s.raw), 1);
     mbar_init(mb(s.all_done), 1);
     mbar_init(mb(s.drained), 1);
@@ -117,13 +118,14 @@ __device__ __forceinline__ bool load_stage(const CUtensorMap* mx, const CUtensor
 
 // Copies in flight land before the CTA leaves (`done` stages were loaded).
 __device__ __forceinline__ void drain_loads(BwdSmall& bs, int done) {
-  mbar_wait(mb(bs.big_full), 0, kDrain);
   for (int y = max(0, done - kStages); y < done; ++y)
     mbar_wait(mb(bs.full[y % kStages]), (uint32_t)(y / kStages) & 1u, kDrain);
 }
 
-// The issuing warp of both kernels over n steps.  NOUT products with the weights: dq (dS), or
-// dv (P) and dk (dS).
+// The issuing warp of both kernels over n steps.  The tile that stays is an A operand in shared
+// memory (K, V for dv and dk), or in tensor memory where that has room for it (Q, dO for dq): at
+// N = 64 a product with both operands in shared memory takes 49 cycles, bound by its reads, one
+// with A in tensor memory 33.
 template <int D, bool DKV>
 __device__ __forceinline__ void issue_steps(uint32_t sb, uint32_t tb, BwdSmall& bs, int n,
                                             const Waits& wait) {
@@ -137,14 +139,24 @@ __device__ __forceinline__ void issue_steps(uint32_t sb, uint32_t tb, BwdSmall& 
       fence_after_sync();
       const uint32_t at = sb + L::ST + s * L::STAGE;
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks)
-        mma_bf16_w(tb + L::TS + 128 * w, kmajor(sb + L::X, kA, ks), kmajor(at, kS, ks), id_s,
-                   ks > 0);
+      for (int ks = 0; ks < D / 16; ++ks) {
+        if (DKV)
+          mma_bf16_w(tb + L::TS + 128 * w, kmajor(sb + L::X, kA, ks), kmajor(at, kS, ks), id_s,
+                     ks > 0);
+        else
+          mma_bf16_ta_w(tb + L::TS + 128 * w, tb + L::TA + 8 * ks, kmajor(at, kS, ks), id_s,
+                        ks > 0);
+      }
       mma_commit_w(mb(bs.s_full[w]));
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks)
-        mma_bf16_w(tb + L::TS + 128 * w + 64, kmajor(sb + L::Y, kA, ks),
-                   kmajor(at + L::SMALL_T, kS, ks), id_s, ks > 0);
+      for (int ks = 0; ks < D / 16; ++ks) {
+        if (DKV)
+          mma_bf16_w(tb + L::TS + 128 * w + 64, kmajor(sb + L::Y, kA, ks),
+                     kmajor(at + L::SMALL_T, kS, ks), id_s, ks > 0);
+        else
+          mma_bf16_ta_w(tb + L::TS + 128 * w + 64, tb + L::TA + D / 2 + 8 * ks,
+                        kmajor(at + L::SMALL_T, kS, ks), id_s, ks > 0);
+      }
       mma_commit_w(mb(bs.dp_full[w]));
     }
     if (y > 0) {
@@ -199,8 +211,7 @@ __device__ __forceinline__ void store_row(uint32_t taddr, float f, bool have, bo
 
 template <int D>
 __global__ void __launch_bounds__(kWarpsB * 32, 1)
-attn_dq_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
-           const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+attn_dq_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
            const AttnGradArgs a, uint32_t spin) {
   using L = BwdLayout<D>;
   extern __shared__ unsigned char smem_raw[];
@@ -216,7 +227,7 @@ attn_dq_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
   const Mask m = make_mask(f.lengths, b, f.Tq, f.Tk, f.window, f.sinks);
   const KeyTiles kt = key_tiles<kS>(m, i0, min(i0 + kA, f.Tq) - 1);
   const int n = kt.count();
-  const uint32_t tb = bwd_setup(bs, warp);
+  const uint32_t tb = bwd_setup(bs, warp, 8);
   const uint32_t sb = smem_u32(sm);
   const Waits wait{f.status, &bs.abort, spin};
 
@@ -227,6 +238,23 @@ attn_dq_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
     const uint32_t tS = tb + tl + L::TS + 128 * w;
     const int i = i0 + row, p = m.off + i;
     const float c = f.scale * kLog2e;
+    {
+      // the query's row into its TMEM lane: q by the first group, do by the second
+      const uint4* src = reinterpret_cast<const uint4*>((const __nv_bfloat16*)(w ? a.dO : f.q) +
+                                                        (((size_t)b * f.Tq + i) * f.Hq + h) * D);
+#pragma unroll
+      for (int q = 0; q < D / 64; ++q) {
+        float x[32];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          reinterpret_cast<uint4*>(x)[e] = i < f.Tq ? src[8 * q + e] : make_uint4(0, 0, 0, 0);
+        tmem_st32(tb + tl + L::TA + D / 2 * w + 32 * q, x);
+      }
+      tmem_wait_st();
+      fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(mb(bs.big_full));
+    }
     const size_t at = ((size_t)b * f.Hq + h) * f.Tq + i;
     const float nl = i < f.Tq ? -f.lse[at] * kLog2e : 0.f;
     const float nd = i < f.Tq ? -a.delta[at] : 0.f;
@@ -284,14 +312,7 @@ attn_dq_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
     fewer_registers<80>();
     if (warp == 8) {
       issue_steps<D, false>(sb, tb, bs, n, wait);
-    } else if (warp == 9 && n > 0) {
-      if (lane == 0) {
-        mbar_expect_tx(mb(bs.big_full), 2 * L::BIG);
-        for (int pn = 0; pn < D / 64; ++pn) {
-          tma_load_4d(sb + L::X + pn * kA * 128, &tm_q, 64 * pn, h, i0, b, mb(bs.big_full));
-          tma_load_4d(sb + L::Y + pn * kA * 128, &tm_do, 64 * pn, h, i0, b, mb(bs.big_full));
-        }
-      }
+    } else if (warp == 9) {
       const int limit = m.len < f.Tk ? m.len : -1;
       uint32_t nraw = 0;
       int done = 0;
@@ -309,6 +330,9 @@ attn_dq_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
   fence_before_sync();
   __syncthreads();
   if (warp == 0) tmem_dealloc(tb, 512);
+  // its blocks start as those of the kernel before (dk, dv: nothing they need) leave their SMs;
+  // this one is not over before that one
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // How key tiles are cut: tiles [0, nfirst) into up to pfirst parts, the others into up to
@@ -360,10 +384,11 @@ attn_dkv_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
   int lo64, nt;
   tile_steps(m, j0, f.Tk, f.Tq, lo64, nt);
   const int used = parts.used(G * nt, most);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (part >= used) return;
   const int per = (G * nt + used - 1) / used;
   const int y0 = part * per, n = max(0, min(per, G * nt - y0));
-  const uint32_t tb = bwd_setup(bs, warp);
+  const uint32_t tb = bwd_setup(bs, warp, 1);
   const uint32_t sb = smem_u32(sm);
   const Waits wait{f.status, &bs.abort, spin};
 
@@ -509,7 +534,10 @@ attn_dkv_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         done = y + 1;
         if (!load_stage<D>(&tm_q, &tm_do, sm, bs, s, h, i0, b, limit, nraw, wait, lane)) break;
       }
-      if (lane == 0) drain_loads(bs, done);
+      if (lane == 0) {
+        mbar_wait(mb(bs.big_full), 0, kDrain);
+        drain_loads(bs, done);
+      }
     }
   }
   fence_before_sync();
@@ -595,10 +623,8 @@ template <int D>
 cudaError_t launch_t(const AttnGradArgs& a, cudaStream_t st) {
   using L = BwdLayout<D>;
   const AttnArgs& f = a.f;
-  CUtensorMap qb, db, kb, vb, qs, ds, ks, vs;      // tiles that stay, tiles that stream
-  if (!encode_bthd_bf16(&qb, f.q, f.B, f.Tq, f.Hq, D, 64, kA, true) ||
-      !encode_bthd_bf16(&db, a.dO, f.B, f.Tq, f.Hq, D, 64, kA, true) ||
-      !encode_bthd_bf16(&kb, f.k, f.B, f.Tk, f.Hkv, D, 64, kA, true) ||
+  CUtensorMap kb, vb, qs, ds, ks, vs;      // tiles that stay, tiles that stream
+  if (!encode_bthd_bf16(&kb, f.k, f.B, f.Tk, f.Hkv, D, 64, kA, true) ||
       !encode_bthd_bf16(&vb, f.v, f.B, f.Tk, f.Hkv, D, 64, kA, true) ||
       !encode_bthd_bf16(&qs, f.q, f.B, f.Tq, f.Hq, D, 64, kS, true) ||
       !encode_bthd_bf16(&ds, a.dO, f.B, f.Tq, f.Hq, D, 64, kS, true) ||
@@ -617,14 +643,15 @@ cudaError_t launch_t(const AttnGradArgs& a, cudaStream_t st) {
   const unsigned bh = (unsigned)(f.B * f.Hkv);
   kk<<<(unsigned)p.items() * bh, kWarpsB * 32, L::SMEM, st>>>(kb, vb, qs, ds, a, p, spin);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  e = launch_after(kq, dim3((unsigned)((f.Tq + kA - 1) / kA * f.Hq * f.B)), kWarpsB * 32, L::SMEM,
+                   st, ks, vs, a, spin);
+  if (e != cudaSuccess) return e;
   if (p.pfirst > 1 || p.prest > 1) {
     const unsigned tiles = (unsigned)(p.prest > 1 ? p.ntiles : p.nfirst);
     attn_dkv_join<D><<<tiles * bh * (kA * (D / 8) * 2 / 256), 256, 0, st>>>(a, p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    e = cudaGetLastError();
   }
-  kq<<<(unsigned)((f.Tq + kA - 1) / kA * f.Hq * f.B), kWarpsB * 32, L::SMEM, st>>>(qb, db, ks, vs,
-                                                                                  a, spin);
-  return cudaGetLastError();
+  return e;
 }
 
 }  // namespace
