@@ -38,12 +38,14 @@ __device__ __forceinline__ void report(unsigned int* status) {
 // A sequence's visible tokens, numbered 0 .. count-1: the sinks, then the window.
 struct Visible {
   int len, ns, gap, count;
+  bool fresh;           // the last one's key and value come with the call
   __device__ __forceinline__ int token(int x) const { return x < ns ? x : x + gap; }
 };
 __device__ __forceinline__ Visible visible(const PagedArgs& a, int n, bool note) {
   Visible v;
   const int cap = (int)min((long)a.max_pages << a.page_shift, (long)0x7fffffff);
   int len = a.lengths[n];
+  v.fresh = a.k_new && len > 0 && len <= cap;
   if (len < 0 || len > cap) {
     if (note) report(a.status);
     len = len < 0 ? 0 : cap;
@@ -110,7 +112,7 @@ struct Rows {
   __device__ __forceinline__ long find(int x, int end) const {
     if (x >= end) return -1;
     const int t = v.token(x);
-    if (a.k_new && t == v.len - 1) return -2;
+    if (v.fresh && t == v.len - 1) return -2;
     const int pg = a.table[(size_t)n * a.max_pages + (t >> a.page_shift)];
     if ((unsigned)pg >= (unsigned)a.npages) {
       report(a.status);
@@ -190,7 +192,7 @@ attn_decode_tc(const PagedArgs a) {
   if (part >= parts) return;
   const int h0 = hk * G + hb * 16, nh = min(16, G - hb * 16);
   const int x0 = part * per, x1 = min(vis.count, x0 + per);
-  if (a.k_new && hb == 0 && part == parts - 1 && vis.len > 0) store_new<bf16, D>(a, vis, n, hk);
+  if (vis.fresh && hb == 0 && part == parts - 1) store_new<bf16, D>(a, vis, n, hk);
 
   // query fragments, with the scale and log2 e applied to the scores later
   const int g = lane >> 2, t4 = lane & 3;
@@ -396,7 +398,7 @@ attn_decode_simt(const PagedArgs a) {
   if (part >= parts) return;
   const int h0 = hk * G + hb * kSHeads, nh = min(kSHeads, G - hb * kSHeads);
   const int x0 = part * per, x1 = min(vis.count, x0 + per);
-  if (a.k_new && hb == 0 && part == parts - 1 && vis.len > 0) store_new<T, D>(a, vis, n, hk);
+  if (vis.fresh && hb == 0 && part == parts - 1) store_new<T, D>(a, vis, n, hk);
   for (int e = tid; e < kSHeads * D; e += kWarps * 32)
     sm.q[e / D][e % D] =
         e / D < nh ? Elem<T>::load((const T*)a.q + ((size_t)n * a.Hq + h0 + e / D) * D + e % D)

@@ -375,7 +375,8 @@ GDR_API gdr_status kda_backward(const void* q, const void* k, const void* v,
  * token only).  States are [B, H, d_v, d_k] fp32 as above; q, k, v, o and the gradients of
  * q, k, v all have the type `dtype`; head sizes {32, 64, 128}; q is used as given.
  *
- * lin_prefill: any T >= 0; s0 NULL for zeros; s_final NULL to skip, or s0 itself.
+ * lin_prefill: any T >= 0; s0 NULL for zeros; s_final NULL to skip, or s0 itself; otherwise no
+ *   output may overlap an input.
  * lin_decode: one token for each of N sequences, the state updated in place.
  * lin_backward: gradients of L = sum <dO, o> + <ds_final, S_T> with respect to q, k, v and
  *   s0 (ds0 is written whether s0 was given or not; the decay has none); ds_final NULL for
@@ -383,7 +384,11 @@ GDR_API gdr_status kda_backward(const void* q, const void* k, const void* v,
  * Workspaces: gdr_lin_workspace_bytes(...) bytes (at least 256), 256-byte aligned.  The
  * first 256 bytes hold the status word that gdr_workspace_status reads: zero them once
  * before the first use to use that call; nothing else needs a fill.  Sizes for which it
- * returns 0 are refused. */
+ * returns 0 are refused.
+ * Precision: fp32 tensors are computed in fp32.  With bf16 tensors of head sizes 64 and 128 the
+ * products run on the tensor cores: the weights within a chunk of 64 tokens and the state that
+ * meets the queries are rounded to bf16 for the outputs; the states themselves are fp32
+ * throughout (values decayed by exact sums of bf16 terms). */
 GDR_API size_t gdr_lin_workspace_bytes(int B, int T, int H, int dk, int dv, int dtype,
                                        int backward);
 GDR_API gdr_status lin_prefill(const void* q, const void* k, const void* v, const float* decay,
@@ -447,9 +452,10 @@ GDR_API gdr_status attn_backward(const void* q, const void* k, const void* v, co
  *
  * The query sits at position lengths[n] - 1; window, sinks, scale as above.  Only pages that
  * hold visible tokens are read (those before a window may have been given away).  Lengths and
- * table entries are read on the device: lengths are clamped to 0 .. max_pages * page, tokens
- * whose table entry is outside the pool are left out, and either is recorded in the status
- * word (GDR_ERR_INVALID_ARG from gdr_workspace_status).  Sequences must not share the page of
+ * table entries are read on the device: lengths are clamped to 0 .. max_pages * page (a new
+ * token past that is neither stored nor seen), tokens whose table entry is outside the pool are
+ * left out, and either is recorded in the status word (GDR_ERR_INVALID_ARG from
+ * gdr_workspace_status).  Sequences must not share the page of
  * their new token.  The workspace must hold gdr_attn_decode_workspace_bytes(...) bytes.
  *
  * kv_append stores K tokens of each sequence: k, v [N, K, Hkv, d]; token t < counts[n] (NULL:

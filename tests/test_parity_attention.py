@@ -102,12 +102,24 @@ def _check_padded(q, k, v, dtype, lens, **kw):
     o, lse = _forward(q, k, v, dtype, lens, **kw)
     do = randn(q.shape, 5, dtype)
     for b, n in enumerate(lens):
-        do[b, n:] = float("inf")
+        do[b, max(0, n - (k.shape[1] - q.shape[1])):] = float("inf")
     got = g.attn_backward(q.cuda(), k.cuda(), v.cuda(), o, lse, do.cuda(), lengths=_lens(lens), **kw)
     u = unit(dtype)
     ref, rounding = attention_backward(to64(q), to64(k), to64(v), to64(do), lengths=lens, unit=u + F32, **kw)
     for name, x, r, b in zip(("dq", "dk", "dv"), got, ref, rounding):
         close(to64(x), r, u * np.abs(r) * (1 + 2 * u) + 1.02 * b + 1e-30, name)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("Tq,Tk,lens", [(130, 300, [300, 171, 170, 169, 5, 250]), (300, 130, [130, 1, 0, 77, 64, 128])])
+def test_part_of_a_padded_batch(dtype, Tq, Tk, lens):
+    """Fewer queries than keys (or more) and lengths that end among them, before and after."""
+    q, k, v = _inputs(6, Tq, Tk, 4, 2, 64, dtype, 9)
+    for x, off in ((q, Tk - Tq), (k, 0), (v, 0)):
+        for b, n in enumerate(lens):
+            x[b, max(0, n - off):] = float("nan")
+    _check_padded(q, k, v, dtype, lens, window=0)
+    _check_padded(q, k, v, dtype, lens, window=70, sinks=5)
 
 
 def test_lengths_outside_the_tensor_are_clamped():

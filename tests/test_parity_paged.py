@@ -140,6 +140,25 @@ def test_pages_and_lengths_outside_the_cache_are_left_out_and_reported():
     close(to64(o[1]), ref[0, 0], 2.0 ** -8 * 1.01 * (np.abs(ref) + mag)[0, 0] + F32, "without the pages")
 
 
+def test_new_token_past_a_full_cache_is_left_out():
+    import gated_delta_rule_79_b200 as g
+    c = Cache([32, 20], 2, 64, 16, "bf16", extra=0)
+    kc, vc, table, lens = c.cuda()
+    before = kc.clone(), vc.clone()
+    lens[0] = 33
+    q, new = randn((2, 4, 64), 1, "bf16"), randn((2, 2, 64), 2, "bf16")
+    ws = torch.zeros(g.attn_decode_workspace_bytes(2, 4, 2, 64, 16, c.per, torch.bfloat16),
+                     dtype=torch.uint8, device="cuda")
+    o = g.attn_decode(q.cuda(), kc, vc, table, lens, k=new.cuda(), v=new.cuda(), workspace=ws)
+    with pytest.raises(g.GdrError):
+        g.workspace_status(ws)
+    ref, mag = _expect(c, q, 0)
+    close(to64(o[0]), ref, 2.0 ** -8 * 1.01 * (np.abs(ref) + mag) + F32, "the 32 tokens it holds")
+    p0, p1 = (table[0].long(), table[1].long())
+    assert torch.equal(kc[p0], before[0][p0]) and torch.equal(vc[p0], before[1][p0])
+    assert torch.equal(kc[p1[1], 3].cpu(), new[1])
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("page", [1, 8, 128])
 def test_append(dtype, page):
