@@ -17,6 +17,10 @@
 // overwrite S and dP as bf16 operands.
 //
 // P and dS are rounded to bf16, as what they multiply is; the scale is applied to the fp32 sums.
+// Where a query sees few keys (up to kFew) the rounded o inside D weighs as much as these
+// roundings (all three together passed one and a half times the rounding of the results), so
+// there P and dS enter as two bf16 terms each, the second in the columns that the first leaves
+// free: four or eight more products a step, where there are few steps.
 //
 // A key tile that many queries see (one with sinks, or an early one without a window) would keep
 // its CTA busy after the others have finished: its queries are cut into parts of about the mean
@@ -35,6 +39,7 @@ constexpr int kA = 128;                     // rows of the tile that stays
 constexpr int kS = 64;                      // rows of the tiles that stream past
 constexpr int kWarpsB = 12;                 // 2 x 4 compute, then issue, load, 2 idle
 constexpr int kStages = 3;
+constexpr int kFew = 256;
 
 template <int D>
 struct BwdLayout {
@@ -126,7 +131,7 @@ __device__ __forceinline__ void drain_loads(BwdSmall& bs, int done) {
 // memory (K, V for dv and dk), or in tensor memory where that has room for it (Q, dO for dq): at
 // N = 64 a product with both operands in shared memory takes 49 cycles, bound by its reads, one
 // with A in tensor memory 33.
-template <int D, bool DKV>
+template <int D, bool DKV, bool FINE>
 __device__ __forceinline__ void issue_steps(uint32_t sb, uint32_t tb, BwdSmall& bs, int n,
                                             const Waits& wait) {
   using L = BwdLayout<D>;
@@ -166,14 +171,14 @@ __device__ __forceinline__ void issue_steps(uint32_t sb, uint32_t tb, BwdSmall& 
       const uint32_t at = sb + L::ST + s * L::STAGE;
       if (DKV) {
 #pragma unroll
-        for (int ks = 0; ks < kS / 16; ++ks)
+        for (int ks = 0; ks < (FINE ? 2 : 1) * kS / 16; ++ks)
           mma_bf16_ta_w(tb + L::TG, tb + L::TS + 128 * w + 8 * ks,
-                        mnmajor(at + L::SMALL_T, kS, ks), id_g, z > 0 || ks > 0);
+                        mnmajor(at + L::SMALL_T, kS, ks % (kS / 16)), id_g, z > 0 || ks > 0);
       }
 #pragma unroll
-      for (int ks = 0; ks < kS / 16; ++ks)
+      for (int ks = 0; ks < (FINE ? 2 : 1) * kS / 16; ++ks)
         mma_bf16_ta_w(tb + L::TG + (DKV ? D : 0), tb + L::TS + 128 * w + 64 + 8 * ks,
-                      mnmajor(at, kS, ks), id_g, z > 0 || ks > 0);
+                      mnmajor(at, kS, ks % (kS / 16)), id_g, z > 0 || ks > 0);
       mma_commit_w(mb(bs.empty[s]));
     }
   }
@@ -181,6 +186,24 @@ __device__ __forceinline__ void issue_steps(uint32_t sb, uint32_t tb, BwdSmall& 
   // the products issued here complete before tensor memory is freed
   mma_commit_w(mb(bs.drained));
   mbar_wait(mb(bs.drained), 0, kDrain);
+}
+
+// 64 weights of a TMEM lane as bf16 pairs, with FINE what the rounding cut off in 32 more columns.
+template <bool FINE>
+__device__ __forceinline__ void put_weights(uint32_t taddr, const float (&x)[kS]) {
+  float pk[32];
+#pragma unroll
+  for (int e = 0; e < 32; ++e) pk[e] = pack2(x[2 * e], x[2 * e + 1]);
+  tmem_st32(taddr, pk);
+  if (FINE) {
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+      const uint32_t u = __float_as_uint(pk[e]);
+      pk[e] = pack2(x[2 * e] - __uint_as_float(u << 16),
+                    x[2 * e + 1] - __uint_as_float(u & 0xffff0000u));
+    }
+    tmem_st32(taddr + 32, pk);
+  }
 }
 
 // D columns of a TMEM lane times f, as bf16, to dst (16-byte aligned); zeros when !have.
@@ -209,7 +232,7 @@ __device__ __forceinline__ void store_row(uint32_t taddr, float f, bool have, bo
   }
 }
 
-template <int D>
+template <int D, bool FINE>
 __global__ void __launch_bounds__(kWarpsB * 32, 1)
 attn_dq_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
            const AttnGradArgs a, uint32_t spin) {
@@ -293,10 +316,7 @@ attn_dq_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
         for (int e = 0; e < kS; ++e)
           if (!rc.sees(e)) g[e] = 0.f;
       }
-      float pk[32];
-#pragma unroll
-      for (int e = 0; e < 32; ++e) pk[e] = pack2(g[2 * e], g[2 * e + 1]);
-      tmem_st32(tS + 64, pk);
+      put_weights<FINE>(tS + 64, g);
       tmem_wait_st();
       fence_before_sync();
       __syncwarp();
@@ -311,7 +331,7 @@ attn_dq_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
   } else {
     fewer_registers<80>();
     if (warp == 8) {
-      issue_steps<D, false>(sb, tb, bs, n, wait);
+      issue_steps<D, false, FINE>(sb, tb, bs, n, wait);
     } else if (warp == 9) {
       const int limit = m.len < f.Tk ? m.len : -1;
       uint32_t nraw = 0;
@@ -363,7 +383,7 @@ __device__ __forceinline__ void tile_steps(const Mask& m, int j0, int Tk, int Tq
   nt = hi > lo ? (hi + kS - 1) / kS - lo64 : 0;
 }
 
-template <int D>
+template <int D, bool FINE>
 __global__ void __launch_bounds__(kWarpsB * 32, 1)
 attn_dkv_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
             const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
@@ -434,12 +454,7 @@ attn_dkv_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         for (int e = 0; e < kS; ++e)
           if (e < first || e >= last) s[e] = 0.f;
       }
-      {
-        float pk[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) pk[e] = pack2(s[2 * e], s[2 * e + 1]);
-        tmem_st32(tS, pk);
-      }
+      put_weights<FINE>(tS, s);
       if (!(ok = wait(mb(bs.dp_full[w]), par))) break;
       fence_after_sync();
       tmem_ld32(tS + 64, reinterpret_cast<float(&)[32]>(g[0]));
@@ -462,10 +477,7 @@ attn_dkv_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         for (int e = 0; e < kS; ++e)
           if (e < first || e >= last) g[e] = 0.f;
       }
-      float pk[32];
-#pragma unroll
-      for (int e = 0; e < 32; ++e) pk[e] = pack2(g[2 * e], g[2 * e + 1]);
-      tmem_st32(tS + 64, pk);
+      put_weights<FINE>(tS + 64, g);
       tmem_wait_st();
       fence_before_sync();
       __syncwarp();
@@ -502,7 +514,7 @@ attn_dkv_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
   } else {
     fewer_registers<80>();
     if (warp == 8) {
-      issue_steps<D, true>(sb, tb, bs, n, wait);
+      issue_steps<D, true, FINE>(sb, tb, bs, n, wait);
     } else if (warp == 9 && n > 0) {
       if (lane == 0) {
         mbar_expect_tx(mb(bs.big_full), 2 * L::BIG);
@@ -619,7 +631,7 @@ Parts plan_parts(const AttnArgs& f) {
   return p;
 }
 
-template <int D>
+template <int D, bool FINE>
 cudaError_t launch_t(const AttnGradArgs& a, cudaStream_t st) {
   using L = BwdLayout<D>;
   const AttnArgs& f = a.f;
@@ -631,8 +643,8 @@ cudaError_t launch_t(const AttnGradArgs& a, cudaStream_t st) {
       !encode_bthd_bf16(&ks, f.k, f.B, f.Tk, f.Hkv, D, 64, kS, true) ||
       !encode_bthd_bf16(&vs, f.v, f.B, f.Tk, f.Hkv, D, 64, kS, true))
     return cudaErrorInvalidValue;
-  auto kq = attn_dq_tc<D>;
-  auto kk = attn_dkv_tc<D>;
+  auto kq = attn_dq_tc<D, FINE>;
+  auto kk = attn_dkv_tc<D, FINE>;
   static std::atomic<unsigned long long> done{0}, done2{0};
   cudaError_t e = allow_smem(kq, L::SMEM, done);
   if (e == cudaSuccess)
@@ -665,7 +677,9 @@ size_t attn_backward_tc_bytes(const AttnArgs& f) {
 }
 
 cudaError_t launch_attn_backward_tc(const AttnGradArgs& a, cudaStream_t st) {
-  return a.f.d == 64 ? launch_t<64>(a, st) : launch_t<128>(a, st);
+  const long seen = a.f.window ? (long)a.f.window + a.f.sinks : a.f.Tk;
+  if (seen <= kFew) return a.f.d == 64 ? launch_t<64, true>(a, st) : launch_t<128, true>(a, st);
+  return a.f.d == 64 ? launch_t<64, false>(a, st) : launch_t<128, false>(a, st);
 }
 
 }  // namespace gdr
