@@ -654,7 +654,8 @@ def attn_prefill(q, k, v, *, window=0, sinks=0, scale=None, lengths=None, o=None
     with _on(dev, stream):
         o = _out_like(o, "o", q)
         lse = None if lse is False else _out(lse, "lse", (B, Hq, Tq), torch.float32, dev)
-        ws, nws = _scratch(workspace, 256, dev, "attn_prefill")
+        ws, nws = _scratch(workspace, _attn_bytes(B, Tq, Tk, Hq, Hkv, d, w, n, code, 0), dev,
+                           "attn_prefill")
         _check(lib.attn_prefill(*ptrs, lens, o.data_ptr(), None if lse is None else lse.data_ptr(),
                                 B, Tq, Tk, Hq, Hkv, d, w, n, d ** -0.5 if scale is None else scale,
                                 code, ws.data_ptr(), nws, _raw(dev, stream)))

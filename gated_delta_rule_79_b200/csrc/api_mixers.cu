@@ -146,15 +146,16 @@ gdr_status attn_common(const char* fn, int B, int Tq, int Tk, int Hq, int Hkv, i
 
 bool attn_tc(int d, int dtype) { return dtype == GDR_BF16 && d >= 64; }
 
-// Status word, then (backward) do . o of every row, then the sums of cut key tiles.  The
-// window is normalised.
+// Status word, then the sums of cut keys, or (backward) do . o of every row and the sums of cut
+// key tiles.  The window is normalised.
 size_t attn_delta_bytes(const AttnArgs& a) {
   return ((size_t)a.B * a.Hq * a.Tq * sizeof(float) + 255) / 256 * 256;
 }
 size_t attn_need(const AttnArgs& a, bool backward) {
-  if (!backward || a.Tq == 0 || a.Tk == 0 || a.Hq == 0) return kStatusBytes;
-  return kStatusBytes + attn_delta_bytes(a) +
-         (attn_tc(a.d, a.dtype) ? attn_backward_tc_bytes(a) : 0);
+  if (a.B == 0 || a.Tq == 0 || a.Tk == 0 || a.Hq == 0) return kStatusBytes;
+  const bool tc = attn_tc(a.d, a.dtype);
+  if (!backward) return kStatusBytes + (tc ? attn_forward_tc_bytes(a) : 0);
+  return kStatusBytes + attn_delta_bytes(a) + (tc ? attn_backward_tc_bytes(a) : 0);
 }
 
 int page_shift_of(int page) {
@@ -309,10 +310,10 @@ gdr_status attn_prefill(const void* q, const void* k, const void* v, const int* 
   const Arg args[] = {{q, "q", true, 16}, {k, "k", Tk > 0, 16}, {v, "v", Tk > 0, 16},
                       {o, "o", true, 16}, {lse, "lse", false, 16}, {lengths, "lengths", false, 4}};
   if ((s = check_pointers(fn, args)) != GDR_OK) return s;
-  if ((s = check_workspace(fn, workspace, ws_bytes, kStatusBytes)) != GDR_OK) return s;
   normalise_window(Tk, window, sinks);
   AttnArgs a{q, k, v, lengths, o, lse, (unsigned int*)workspace, B, Tq, Tk, Hq, Hkv, d,
-             window, sinks, scale, dtype};
+             window, sinks, scale, dtype, (float*)((unsigned char*)workspace + kStatusBytes)};
+  if ((s = check_workspace(fn, workspace, ws_bytes, attn_need(a, false))) != GDR_OK) return s;
   const bool tc = attn_tc(d, dtype) && Tk > 0;
   return done(fn, tc ? launch_attn_forward_tc(a, (cudaStream_t)stream)
                      : launch_attn_forward_simt(a, (cudaStream_t)stream));
@@ -335,7 +336,7 @@ gdr_status attn_backward(const void* q, const void* k, const void* v, const int*
   normalise_window(Tk, window, sinks);
   AttnGradArgs a{};
   a.f = AttnArgs{q, k, v, lengths, const_cast<void*>(o), const_cast<float*>(lse),
-                 (unsigned int*)workspace, B, Tq, Tk, Hq, Hkv, d, window, sinks, scale, dtype};
+                 (unsigned int*)workspace, B, Tq, Tk, Hq, Hkv, d, window, sinks, scale, dtype, nullptr};
   a.dO = dO, a.dq = dq, a.dk = dk, a.dv = dv;
   if ((s = check_workspace(fn, workspace, ws_bytes, attn_need(a.f, true))) != GDR_OK) return s;
   cudaStream_t st = (cudaStream_t)stream;

@@ -76,12 +76,6 @@ template <int N>
 __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory");
 }
-__device__ __forceinline__ void dependents_may_launch() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void wait_for_prior_grid() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -177,7 +171,7 @@ attn_decode_tc(const PagedArgs a) {
   using S = TcSmem<D>;
   using bf16 = __nv_bfloat16;
   extern __shared__ __align__(128) unsigned char sm[];
-  dependents_may_launch();
+  let_next_start();
   const int G = a.Hq / a.Hkv, nhb = (G + 15) / 16;
   int x = blockIdx.x;
   const int part = x % a.nsplit;
@@ -383,7 +377,7 @@ __global__ void __launch_bounds__(kWarps * 32)
 attn_decode_simt(const PagedArgs a) {
   extern __shared__ __align__(128) unsigned char raw[];
   SimtSmem<T, D>& sm = *reinterpret_cast<SimtSmem<T, D>*>(raw);
-  dependents_may_launch();
+  let_next_start();
   const int G = a.Hq / a.Hkv, nhb = (G + kSHeads - 1) / kSHeads;
   int x = blockIdx.x;
   const int part = x % a.nsplit;
@@ -506,7 +500,7 @@ __global__ void __launch_bounds__(128)
 attn_decode_join(const PagedArgs a) {
   __shared__ float wt[kMaxSplit], acc[4][D], red[2][4];
   const int nh = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  wait_for_prior_grid();
+  wait_for_previous();
   const Visible vis = visible(a, nh / a.Hq, false);
   const int per = part_tokens(vis.count, a.nsplit);
   const int parts = (vis.count + per - 1) / per;
@@ -608,16 +602,7 @@ cudaError_t launch_t(const PagedArgs& a, cudaStream_t st) {
                     done);
   }
   if (e != cudaSuccess || a.nsplit == 1) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(a.N * a.Hq), 1, 1);
-  cfg.blockDim = dim3(128, 1, 1);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_decode_join<T, D>, a);
+  return launch_after(attn_decode_join<T, D>, dim3((unsigned)(a.N * a.Hq)), 128, 0, st, a);
 }
 
 template <typename T>
@@ -634,7 +619,7 @@ cudaError_t launch_d(const PagedArgs& a, cudaStream_t st) {
 
 // How many parts a sequence's tokens may be cut into.  The grid is the same for every
 // length (the lengths are on the device), and parts past a short sequence's end leave at
-// once, so it is chosen from what the page table can hold: enough CTAs for eight on each
+// once, so it is chosen from what the page table can hold: enough CTAs for sixteen on each
 // SM, which also evens out sequences of different lengths, and no part below 64 tokens.
 int attn_decode_splits(int N, int Hq, int Hkv, int d, int dtype, long capacity, int window,
                        int sinks) {
@@ -644,7 +629,7 @@ int attn_decode_splits(int N, int Hq, int Hkv, int d, int dtype, long capacity, 
   long most = capacity;
   if (window && most > (long)window + sinks) most = (long)window + sinks;
   const long by_tokens = (most + kWarps * kTile - 1) / (kWarps * kTile);
-  const long by_ctas = (148L * 8 + base - 1) / base;
+  const long by_ctas = (148L * 16 + base - 1) / base;
   long s = by_tokens < by_ctas ? by_tokens : by_ctas;
   if (s < 1) s = 1;
   return (int)(s > kMaxSplit ? kMaxSplit : s);

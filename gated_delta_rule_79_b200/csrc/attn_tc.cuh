@@ -72,35 +72,36 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
       : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
   return d;
 }
-// 2^x for two x in [-126, 127] on the multiply-add pipes: x = n + f with n the nearest integer
-// (left in the low bits of x + 1.5 2^23) and f in [-1/2, 1/2]; 2^f by a polynomial of degree 4,
-// fitted for the least relative error, 2.6e-6; n added to the exponent field.  Below -126 it
-// stays at 2^-126.
-__device__ __forceinline__ float2 ex2_fma(float2 x) {
-  const float2 magic = make_float2(12582912.f, 12582912.f), one = make_float2(-1.f, -1.f);
-  x.x = fmaxf(x.x, -126.f);
-  x.y = fmaxf(x.y, -126.f);
-  const float2 t = add2(x, magic);
-  const float2 f = fma2(add2(t, make_float2(-12582912.f, -12582912.f)), one, x);
-  float2 p = make_float2(0.009570102207362652f, 0.009570102207362652f);
-  p = fma2(p, f, make_float2(0.05591785907745361f, 0.05591785907745361f));
-  p = fma2(p, f, make_float2(0.240247443318367f, 0.240247443318367f));
-  p = fma2(p, f, make_float2(0.6931217908859253f, 0.6931217908859253f));
-  p = fma2(p, f, make_float2(0.9999992847442627f, 0.9999992847442627f));
-  return make_float2(__int_as_float(__float_as_int(p.x) + (__float_as_int(t.x) << 23)),
-                     __int_as_float(__float_as_int(p.y) + (__float_as_int(t.y) << 23)));
-}
 __device__ __forceinline__ float pack2(float lo, float hi) {
   __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<float*>(&p);
 }
 
+// Bits 0 .. h.
+__device__ __forceinline__ uint32_t columns_to(int h) {
+  return h < 0 ? 0u : 0xffffffffu >> (31 - min(h, 31));
+}
 // A query's visible keys as column thresholds of a tile that starts at key j0: column c is
 // visible when c <= hi and (c >= lo or c < sink).  hi < 0 hides everything.
 struct RowCols {
   int hi, lo, sink;
-  __device__ __forceinline__ bool sees(int c) const { return c <= hi && (c >= lo || c < sink); }
+  // columns c0 .. c0 + 31 as bits
+  __device__ __forceinline__ uint32_t bits(int c0) const {
+    return columns_to(hi - c0) & (~columns_to(lo - 1 - c0) | columns_to(sink - 1 - c0));
+  }
 };
+// The elements of x, a row's columns, that are not visible become `hidden`: a test of one bit and
+// a select each.  (Three comparisons an element made masked tiles two to four times as long.)
+template <int N>
+__device__ __forceinline__ void hide(float (&x)[N], const RowCols& rc, float hidden) {
+#pragma unroll
+  for (int q = 0; q < N / 32; ++q) {
+    const uint32_t see = rc.bits(32 * q);
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      if (!(see & (1u << e))) x[32 * q + e] = hidden;
+  }
+}
 __device__ __forceinline__ RowCols row_cols(const Mask& m, int p, int j0) {
   RowCols r;
   r.hi = p < m.len ? p - j0 : -1;      // p < len covers j < len as well

@@ -311,12 +311,8 @@ attn_dq_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
         g[e] = x.x;
         g[e + 1] = x.y;
       }
-      if (!all_visible(m, m.off + i0, m.off + i0 + kA - 1, j0, j0 + kS - 1)) {
-        const RowCols rc = row_cols(m, p, j0);
-#pragma unroll
-        for (int e = 0; e < kS; ++e)
-          if (!rc.sees(e)) g[e] = 0.f;
-      }
+      if (!all_visible(m, m.off + i0, m.off + i0 + kA - 1, j0, j0 + kS - 1))
+        hide(g, row_cols(m, p, j0), 0.f);
       put_weights<FINE>(tS + 64, g);
       tmem_wait_st();
       fence_before_sync();
@@ -353,7 +349,7 @@ attn_dq_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
   if (warp == 0) tmem_dealloc(tb, 512);
   // its blocks start as those of the kernel before (dk, dv: nothing they need) leave their SMs;
   // this one is not over before that one
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_previous();
 }
 
 // How key tiles are cut: tiles [0, nfirst) into up to pfirst parts, the others into up to
@@ -405,7 +401,7 @@ attn_dkv_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
   int lo64, nt;
   tile_steps(m, j0, f.Tk, f.Tq, lo64, nt);
   const int used = parts.used(G * nt, most);
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  let_next_start();
   if (part >= used) return;
   const int per = (G * nt + used - 1) / used;
   const int y0 = part * per, n = max(0, min(per, G * nt - y0));
@@ -446,14 +442,13 @@ attn_dkv_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
       }
       // this key's queries as a range of columns
       const bool whole = all_visible(m, p0, p0 + kS - 1, j0, j0 + kA - 1);
-      int first = 0, last = kS;
+      RowCols rc;
       if (!whole) {
-        first = j - p0;
-        last = m.len - p0;
-        if (m.window && j >= m.sinks) last = min(last, j - p0 + m.window);
-#pragma unroll
-        for (int e = 0; e < kS; ++e)
-          if (e < first || e >= last) s[e] = 0.f;
+        rc.lo = j - p0;
+        rc.hi = m.len - 1 - p0;
+        if (m.window && j >= m.sinks) rc.hi = min(rc.hi, j - p0 + m.window - 1);
+        rc.sink = 0;
+        hide(s, rc, 0.f);
       }
       put_weights<FINE>(tS, s);
       if (!(ok = wait(mb(bs.dp_full[w]), par))) break;
@@ -473,11 +468,7 @@ attn_dkv_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         g[e + 2] = z.x;
         g[e + 3] = z.y;
       }
-      if (!whole) {      // 0 times what a hidden query holds is not always 0
-#pragma unroll
-        for (int e = 0; e < kS; ++e)
-          if (e < first || e >= last) g[e] = 0.f;
-      }
+      if (!whole) hide(g, rc, 0.f);     // 0 times what a hidden query holds is not always 0
       put_weights<FINE>(tS + 64, g);
       tmem_wait_st();
       fence_before_sync();

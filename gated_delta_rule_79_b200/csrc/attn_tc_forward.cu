@@ -18,6 +18,15 @@
 // weights then stay below 2^8, far from bf16's range), which after the first key tiles is rare.
 // P is rounded to bf16, as the values it weighs are; l adds the unrounded weights.
 //
+// Few queries over many keys (a short piece of a long prompt) leave SMs without a pair of tiles.
+// There the key tiles of a pair are cut into parts, one CTA each, which leave their O, m and l
+// in the workspace in fp32, and a second kernel joins them:
+//
+//     m = max m_p,   l = sum 2^(m_p - m) l_p,   o = sum 2^(m_p - m) O_p / l
+//
+// (16 queries over 8192 keys, 32 heads of d = 128: 38 us, 127 with one CTA to a pair; 3 x 500
+// queries at a window of 1000, 12 heads of d = 64: 22 us and 30.)
+//
 // Waits are bounded: a give-up sets the status word, drains what is in flight and ends the CTA.
 
 #include "attn_tc.cuh"
@@ -32,6 +41,7 @@ using namespace attn;
 constexpr int kT = 128;                     // queries and keys of a tile
 // three warpgroups: 384 threads of 168 registers at launch, then 2 x 128 x 208 + 128 x 80
 constexpr int kWarpsF = 12;
+constexpr int kSMs = 148, kLeast = 3;       // key tiles of a part
 constexpr float kGrow = 8.f;                // log2 of how far a row's weights may grow
 
 template <int D>
@@ -54,13 +64,17 @@ struct FwdSmall {
   int abort;
 };
 
-// The key tiles of the pair, and which of them each tile of queries sees.
+// The key tiles of the pair (of one of `parts` equal parts of them), and which of them each tile
+// of queries sees.
 struct PairTiles {
   KeyTiles t[2];
-  int nsink, lo, n;
-  __device__ __forceinline__ int tile(int x) const { return x < nsink ? x : lo + x - nsink; }
+  int nsink, lo, first, n;
+  __device__ __forceinline__ int tile(int x) const {
+    return x + first < nsink ? x + first : lo + x + first - nsink;
+  }
 };
-__device__ __forceinline__ PairTiles pair_tiles(const Mask& m, int i0, int Tq) {
+__device__ __forceinline__ PairTiles pair_tiles(const Mask& m, int i0, int Tq, int part,
+                                                int parts) {
   PairTiles p;
   p.t[0] = key_tiles<kT>(m, i0, min(i0 + kT, Tq) - 1);
   p.t[1] = i0 + kT < Tq ? key_tiles<kT>(m, i0 + kT, min(i0 + 2 * kT, Tq) - 1) : KeyTiles{0, 0, 0};
@@ -69,14 +83,18 @@ __device__ __forceinline__ PairTiles pair_tiles(const Mask& m, int i0, int Tq) {
   p.nsink = f.nsink;
   const int hi = max(p.t[0].nwin ? p.t[0].lo + p.t[0].nwin : 0,
                      p.t[1].nwin ? p.t[1].lo + p.t[1].nwin : 0);
-  p.n = hi > 0 ? p.nsink + hi - p.lo : 0;
+  const int all = hi > 0 ? p.nsink + hi - p.lo : 0;
+  const int per = (all + parts - 1) / parts;
+  p.first = part * per;
+  p.n = max(0, min(per, all - p.first));
   return p;
 }
 
-template <int D>
+template <int D, bool PARTS>
 __global__ void __launch_bounds__(kWarpsF * 32, 1)
 attn_forward_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                const __grid_constant__ CUtensorMap tm_v, const AttnArgs a, uint32_t spin) {
+                const __grid_constant__ CUtensorMap tm_v, const AttnArgs a,
+                int nparts, uint32_t spin) {
   using L = FwdLayout<D>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -87,11 +105,14 @@ attn_forward_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
   const int npair = (a.Tq + 2 * kT - 1) / (2 * kT);
   const int h = blockIdx.x % a.Hq;
   const int b = (blockIdx.x / a.Hq) % a.B;
-  const int pr = npair - 1 - (int)(blockIdx.x / ((unsigned)a.Hq * a.B));
+  const int parts = PARTS ? nparts : 1;
+  const unsigned rest = blockIdx.x / ((unsigned)a.Hq * a.B);
+  const int part = PARTS ? rest % parts : 0;
+  const int pr = npair - 1 - (int)(rest / parts);
   const int hk = h / (a.Hq / a.Hkv);
   const int i0 = pr * 2 * kT;
   const Mask m = make_mask(a.lengths, b, a.Tq, a.Tk, a.window, a.sinks);
-  const PairTiles pt = pair_tiles(m, i0, a.Tq);
+  const PairTiles pt = pair_tiles(m, i0, a.Tq, part, parts);
 
   auto bar = [](unsigned long long& x) { return reinterpret_cast<uint64_t*>(&x); };
   if (tid == 0) {
@@ -143,12 +164,8 @@ attn_forward_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
       for (int q = 0; q < 4; ++q)
         tmem_ld32(tS + 32 * q, reinterpret_cast<float(&)[32]>(s[32 * q]));
       tmem_wait_ld();
-      if (!all_visible(m, m.off + iw, m.off + iw + kT - 1, j0, j0 + kT - 1)) {
-        const RowCols rc = row_cols(m, p, j0);
-#pragma unroll
-        for (int q = 0; q < kT; ++q)
-          if (!rc.sees(q)) s[q] = -INFINITY;
-      }
+      if (!all_visible(m, m.off + iw, m.off + iw + kT - 1, j0, j0 + kT - 1))
+        hide(s, row_cols(m, p, j0), -INFINITY);
       float t0 = s[0], t1 = s[1], t2 = s[2], t3 = s[3];
 #pragma unroll
       for (int q = 4; q < kT - 4; q += 8) {
@@ -206,6 +223,7 @@ attn_forward_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     if (ok && ns > 0) ok = wait(bar(fs.o_done[w]), (ns - 1) & 1u);
     ok = __all_sync(0xffffffffu, ok);
     const float l = l2.x + l2.y;
+    const size_t row_at = ((size_t)b * a.Hq + h) * a.Tq + i, rows = (size_t)a.B * a.Hq * a.Tq;
     // l is 0 only where nothing is visible; a NaN passes on
     const float inv = l == 0.f ? 0.f : 1.f / l;
     if (ok) {
@@ -218,7 +236,14 @@ attn_forward_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
           tmem_ld32(tO + 32 * q, o);
           tmem_wait_ld();
         }
-        if (i < a.Tq) {
+        if (PARTS && i < a.Tq && ns > 0) {           // O as it stands
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            reinterpret_cast<float4*>(
+                a.part + (((size_t)part * (D / 8) + 4 * q + (e >> 1)) * rows + row_at) * 8)[e & 1] =
+                make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        }
+        if (!PARTS && i < a.Tq) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -231,9 +256,11 @@ attn_forward_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
           }
         }
       }
-      if (a.lse && i < a.Tq)
-        a.lse[((size_t)b * a.Hq + h) * a.Tq + i] =
-            l == 0.f ? -INFINITY : (mref * c + log2f(l)) * kLn2;
+      if (PARTS && i < a.Tq)
+        reinterpret_cast<float2*>(a.part + rows * parts * D)[part * rows + row_at] =
+            make_float2(mref * c, ns > 0 ? l : 0.f);
+      else if (!PARTS && a.lse && i < a.Tq)
+        a.lse[row_at] = l == 0.f ? -INFINITY : (mref * c + log2f(l)) * kLn2;
     }
   } else {
     fewer_registers<80>();
@@ -333,27 +360,97 @@ attn_forward_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
   if (warp == 0) tmem_dealloc(tb, 512);
 }
 
+// The parts' sums joined: 8 channels of a row a thread (they lie [part][channels / 8][row][8], so
+// that both sides touch whole lines).
 template <int D>
+__global__ void __launch_bounds__(256)
+attn_forward_join(const AttnArgs a, int parts) {
+  constexpr int C8 = D / 8;
+  const size_t rows = (size_t)a.B * a.Hq * a.Tq;
+  const size_t row = (size_t)blockIdx.x * (256 / C8) + threadIdx.x % (256 / C8);   // (b, h, i)
+  const int c8 = threadIdx.x / (256 / C8);
+  wait_for_previous();
+  if (row >= rows) return;
+  const float2* ml = reinterpret_cast<const float2*>(a.part + rows * parts * D);
+  float top = -INFINITY;
+  for (int p = 0; p < parts; ++p) {
+    const float2 s = ml[p * rows + row];
+    if (s.y != 0.f) top = fmaxf(top, s.x);
+  }
+  float l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f), u = o;
+  for (int p = 0; p < parts; ++p) {
+    const float2 s = ml[p * rows + row];
+    if (s.y == 0.f) continue;                     // saw nothing, and may have left nothing
+    const float4* src =
+        reinterpret_cast<const float4*>(a.part + (((size_t)p * C8 + c8) * rows + row) * 8);
+    const float4 x = src[0], y = src[1];
+    const float f = ex2(s.x - top);
+    l = fmaf(f, s.y, l);
+    o.x = fmaf(f, x.x, o.x);
+    o.y = fmaf(f, x.y, o.y);
+    o.z = fmaf(f, x.z, o.z);
+    o.w = fmaf(f, x.w, o.w);
+    u.x = fmaf(f, y.x, u.x);
+    u.y = fmaf(f, y.y, u.y);
+    u.z = fmaf(f, y.z, u.z);
+    u.w = fmaf(f, y.w, u.w);
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const size_t bh = row / a.Tq, i = row % a.Tq;
+  __nv_bfloat16* dst =
+      (__nv_bfloat16*)a.o + ((bh / a.Hq * a.Tq + i) * a.Hq + bh % a.Hq) * D + 8 * c8;
+  *reinterpret_cast<float4*>(dst) =
+      make_float4(pack2(o.x * inv, o.y * inv), pack2(o.z * inv, o.w * inv),
+                  pack2(u.x * inv, u.y * inv), pack2(u.z * inv, u.w * inv));
+  if (a.lse && c8 == 0) a.lse[row] = l == 0.f ? -INFINITY : (top + log2f(l)) * kLn2;
+}
+
+// Into how many parts the key tiles of a pair are cut: as many as there are SMs for, of at
+// least kLeast tiles each (2 and 4 measured within 5 % of 3 on lengths from 500 to 32768).
+int parts_of(const AttnArgs& a) {
+  const long ctas = (a.Tq + 2L * kT - 1) / (2 * kT) * a.Hq * a.B;
+  long keys = a.Tk;
+  if (a.window && keys > (long)a.window + 2 * kT + a.sinks)
+    keys = (long)a.window + 2 * kT + a.sinks;
+  long p = ctas > 0 ? kSMs / ctas : 1;
+  const long most = (keys + kT - 1) / kT / kLeast;
+  if (p > most) p = most;
+  return p < 1 ? 1 : (int)p;
+}
+
+template <int D, bool PARTS>
 cudaError_t launch_t(const AttnArgs& a, cudaStream_t st) {
   CUtensorMap mq, mk, mv;
   if (!encode_bthd_bf16(&mq, a.q, a.B, a.Tq, a.Hq, D, 64, kT, true) ||
       !encode_bthd_bf16(&mk, a.k, a.B, a.Tk, a.Hkv, D, 64, kT, true) ||
       !encode_bthd_bf16(&mv, a.v, a.B, a.Tk, a.Hkv, D, 64, kT, true))
     return cudaErrorInvalidValue;
-  auto kern = attn_forward_tc<D>;
+  auto kern = attn_forward_tc<D, PARTS>;
   constexpr int smem = FwdLayout<D>::SMEM;
   static std::atomic<unsigned long long> done{0};
   cudaError_t e = allow_smem(kern, smem, done);
   if (e != cudaSuccess) return e;
-  const unsigned grid = (unsigned)((a.Tq + 2 * kT - 1) / (2 * kT) * a.Hq * a.B);
-  kern<<<grid, kWarpsF * 32, smem, st>>>(mq, mk, mv, a, attn_spin_limit());
-  return cudaGetLastError();
+  const int parts = PARTS ? parts_of(a) : 1;
+  const unsigned grid = (unsigned)((a.Tq + 2 * kT - 1) / (2 * kT) * a.Hq * a.B * parts);
+  kern<<<grid, kWarpsF * 32, smem, st>>>(mq, mk, mv, a, parts, attn_spin_limit());
+  if ((e = cudaGetLastError()) != cudaSuccess || !PARTS) return e;
+  const size_t rows = (size_t)a.B * a.Hq * a.Tq;
+  return launch_after(attn_forward_join<D>, dim3((unsigned)((rows + 2048 / D - 1) / (2048 / D))),
+                      256, 0, st, a, parts);
 }
 
 }  // namespace
 
+// Workspace of the parts' sums (0 when no pair is cut).
+size_t attn_forward_tc_bytes(const AttnArgs& a) {
+  const int parts = parts_of(a);
+  return parts == 1 ? 0 : (size_t)parts * a.B * a.Hq * a.Tq * (a.d + 2) * sizeof(float);
+}
+
 cudaError_t launch_attn_forward_tc(const AttnArgs& a, cudaStream_t st) {
-  return a.d == 64 ? launch_t<64>(a, st) : launch_t<128>(a, st);
+  if (parts_of(a) > 1) return a.d == 64 ? launch_t<64, true>(a, st) : launch_t<128, true>(a, st);
+  return a.d == 64 ? launch_t<64, false>(a, st) : launch_t<128, false>(a, st);
 }
 
 }  // namespace gdr

@@ -154,6 +154,7 @@ struct AttnArgs {
   int window, sinks;    // window 0: none (and then no sinks)
   float scale;
   int dtype;
+  float* part;          // workspace of attn_forward_tc_bytes: sums of parts of the keys
 };
 struct AttnGradArgs {
   AttnArgs f;           // the forward's arguments and results
@@ -167,6 +168,7 @@ struct AttnGradArgs {
 cudaError_t launch_attn_forward_simt(const AttnArgs& a, cudaStream_t stream);
 cudaError_t launch_attn_forward_tc(const AttnArgs& a, cudaStream_t stream);   // bf16, d >= 64
 cudaError_t launch_attn_delta(const AttnGradArgs& a, cudaStream_t stream);
+size_t attn_forward_tc_bytes(const AttnArgs& a);
 size_t attn_backward_tc_bytes(const AttnArgs& f);
 cudaError_t launch_attn_backward_tc(const AttnGradArgs& a, cudaStream_t stream);  // bf16, d >= 64
 cudaError_t launch_attn_backward_simt(const AttnGradArgs& a, cudaStream_t stream);

@@ -62,15 +62,5 @@ __host__ __device__ __forceinline__ int part_at(int dv, int r, int c) {
   return ((c >> 2) * dv + r) * 4 + (c & 3);
 }
 
-// The kernels of a call follow one another by programmatic launch: the next one's blocks may
-// start (and form their decays) once every block has called the first, and wait in the second
-// for all of the one before to have finished.
-__device__ __forceinline__ void let_next_start() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void wait_for_previous() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
 }  // namespace lin
 }  // namespace gdr

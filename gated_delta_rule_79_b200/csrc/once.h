@@ -1,5 +1,6 @@
-// Host-side: a kernel's shared-memory limit is raised once per device, not at every launch (a
-// one-token call lasts about as long as the two driver calls this saves).
+// Launches.  A kernel's shared-memory limit is raised once per device, not at every launch (a
+// one-token call lasts about as long as the two driver calls this saves); the kernels of a call
+// follow one another by programmatic launch.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -22,7 +23,7 @@ inline cudaError_t allow_smem(K kern, int bytes, std::atomic<unsigned long long>
 }
 
 // Launches `kern` so that its blocks may start before the kernel before it in the stream has
-// finished; the kernel itself waits (griddepcontrol.wait) before it reads what that one wrote.
+// finished (once every block of it has called let_next_start, if it does).
 template <typename... P, typename... A>
 inline cudaError_t launch_after(void (*kern)(P...), dim3 grid, int threads, int smem,
                                 cudaStream_t st, const A&... args) {
@@ -37,6 +38,13 @@ inline cudaError_t launch_after(void (*kern)(P...), dim3 grid, int threads, int 
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+__device__ __forceinline__ void let_next_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+// All of the kernel before has finished, and what it wrote can be read.
+__device__ __forceinline__ void wait_for_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 }  // namespace gdr

@@ -152,6 +152,10 @@ def test_workspace_sizes(g):
         g.lin_workspace_bytes(1, 4096, 4, 64, 64, bf)
     assert g.attn_workspace_bytes(2, 100, 100, 4, 2, 64, bf) >= 256
     assert g.attn_workspace_bytes(2, 100, 100, 4, 2, 64, bf, True) >= 256 + 4 * 2 * 4 * 100
+    # few queries over many keys: sums of two parts at least
+    assert g.attn_workspace_bytes(1, 100, 9000, 4, 2, 64, bf) >= 256 + 2 * 4 * 100 * 66 * 4
+    assert g.attn_workspace_bytes(1, 100, 9000, 4, 2, 64, bf, window=100) == 256
+    assert g.attn_workspace_bytes(1, 100, 9000, 4, 2, 64, torch.float32) == 256
     assert g.attn_workspace_bytes(2, 100, 100, 4, 3, 64, bf) == 0
     assert g.attn_decode_workspace_bytes(1, 8, 1, 128, 64, 1024, bf) > 256
     assert g.attn_decode_workspace_bytes(1, 8, 1, 128, 48, 1024, bf) == 0

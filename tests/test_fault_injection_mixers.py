@@ -21,6 +21,7 @@ def _calls(g):
     long = _lin(1500)              # several segments
     q = randn((2, 300, 4, 128), 1, "bf16").cuda()
     k, v = (randn((2, 300, 2, 128), s, "bf16").cuda() for s in (2, 3))
+    kl = randn((1, 1800, 2, 128), 4, "bf16").cuda()
     lens = torch.tensor([300, 170], dtype=torch.int32, device="cuda")
     kw = dict(window=90, sinks=3, lengths=lens)
     o, lse = g.attn_prefill(q, k, v, **kw)
@@ -33,13 +34,15 @@ def _calls(g):
                          g.lin_workspace_bytes(1, 1500, 2, 128, 128, bf, True)),
         "attn_prefill": (lambda ws: g.attn_prefill(q, k, v, workspace=ws, **kw)[0],
                          g.attn_workspace_bytes(2, 300, 300, 4, 2, 128, bf)),
+        "attn_prefill in parts": (lambda ws: g.attn_prefill(kl[:, :90], kl, kl, workspace=ws)[0],
+                                  g.attn_workspace_bytes(1, 90, 1800, 2, 2, 128, bf)),
         "attn_backward": (lambda ws: g.attn_backward(q, k, v, o, lse, q, workspace=ws, **kw)[1],
                           g.attn_workspace_bytes(2, 300, 300, 4, 2, 128, bf, True, 90, 3)),
     }
 
 
 @pytest.mark.parametrize("name", ["lin_prefill", "lin_prefill in segments", "lin_backward",
-                                  "attn_prefill", "attn_backward"])
+                                  "attn_prefill", "attn_prefill in parts", "attn_backward"])
 def test_bounded_waits_report_and_recover(name, monkeypatch):
     import gated_delta_rule_79_b200 as g
     call, size = _calls(g)[name]

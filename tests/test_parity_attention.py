@@ -122,6 +122,34 @@ def test_part_of_a_padded_batch(dtype, Tq, Tk, lens):
     _check_padded(q, k, v, dtype, lens, window=70, sinks=5)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Tq,Tk,Hq,Hkv,lens,window,sinks", [
+    (1, 2000, 2, 1, None, 0, 0),                     # 15 tiles of keys for a single query
+    (129, 1900, 4, 2, [1900, 1771, 1772, 0, 1, 1850], 0, 0),
+    (129, 1900, 4, 2, [1900, 1771, 1772, 0, 1, 1850], 1000, 140),
+    (300, 1300, 6, 2, [1300, 1290], 900, 3),         # parts of the second pair of tiles only
+    (2000, 1000, 3, 1, None, 0, 0),                  # queries that see nothing, in every part
+])
+def test_few_queries_over_many_keys(d, Tq, Tk, Hq, Hkv, lens, window, sinks):
+    """Where there are fewer query tiles than SMs their keys are cut into parts and joined."""
+    q, k, v = _inputs(len(lens or [0]), Tq, Tk, Hq, Hkv, d, "bf16", 21)
+    if lens is None:
+        _forward(q, k, v, "bf16", window=window, sinks=sinks)
+        return
+    for x, off in ((q, Tk - Tq), (k, 0), (v, 0)):
+        for b, n in enumerate(lens):
+            x[b, max(0, n - off):] = float("nan")
+    _forward(q, k, v, "bf16", lens, window=window, sinks=sinks)
+
+
+def test_scores_that_lie_far_apart_in_the_parts():
+    """One key far above all others, in one part: the others' weights vanish, none overflows."""
+    q, k, v = _inputs(1, 40, 1800, 2, 1, 64, "bf16", 31)
+    q[...] = 0.5
+    k[0, 70], k[0, 1000] = 40.0, 44.0
+    _forward(q, k, v, "bf16")
+
+
 def test_lengths_outside_the_tensor_are_clamped():
     import gated_delta_rule_79_b200 as g
     q, k, v = (x.cuda() for x in _inputs(2, 70, 70, 2, 2, 64, "bf16"))
