@@ -179,12 +179,11 @@ gdr_status paged_common(const char* fn, int N, int Hq, int Hkv, int d, int npage
   return GDR_OK;
 }
 
-size_t decode_need(int N, int Hq, int Hkv, int d, int page, int max_pages, int window, int sinks,
-                   int dtype) {
-  const long cap = (long)max_pages * page;
-  normalise_window(cap, window, sinks);
-  const int s = attn_decode_splits(N, Hq, Hkv, d, dtype, cap, window, sinks);
-  return kStatusBytes + (s > 1 ? (size_t)N * Hq * s * (d + 2) * sizeof(float) : 0);
+// Status word, then (for a batch that is cut) where each sequence's parts lie, and their sums.
+size_t first_bytes(int N) { return ((size_t)N * sizeof(int2) + 255) / 256 * 256; }
+size_t decode_need(const PagedArgs& a) {
+  if (a.nparts == 0) return kStatusBytes;
+  return kStatusBytes + first_bytes(a.N) + (size_t)a.nparts * a.Hq * (a.d + 2) * sizeof(float);
 }
 
 }  // namespace
@@ -362,7 +361,12 @@ size_t gdr_attn_decode_workspace_bytes(int N, int Hq, int Hkv, int d, int page, 
   const char* fn = "gdr_attn_decode_workspace_bytes";
   if (paged_common(fn, N, Hq, Hkv, d, 0, page, max_pages, dtype) != GDR_OK) return 0;
   if (N == 0 || Hq == 0 || Hkv == 0 || Hq % Hkv != 0) return kStatusBytes;
-  return decode_need(N, Hq, Hkv, d, page, max_pages, window, sinks, dtype);
+  const long cap = (long)max_pages * page;
+  normalise_window(cap, window, sinks);
+  PagedArgs a{};
+  a.N = N, a.Hq = Hq, a.Hkv = Hkv, a.d = d, a.window = window, a.sinks = sinks, a.dtype = dtype;
+  attn_decode_plan(a, cap);
+  return decode_need(a);
 }
 
 gdr_status attn_decode(const void* q, const void* k, const void* v, void* k_cache, void* v_cache,
@@ -386,15 +390,15 @@ gdr_status attn_decode(const void* q, const void* k, const void* v, void* k_cach
                       {page_table, "page_table", max_pages > 0, 4},
                       {lengths, "lengths", true, 4}, {o, "o", true, 16}};
   if ((s = check_pointers(fn, args)) != GDR_OK) return s;
-  s = check_workspace(fn, workspace, ws_bytes,
-                      decode_need(N, Hq, Hkv, d, page, max_pages, window, sinks, dtype));
-  if (s != GDR_OK) return s;
   const long cap = (long)max_pages * page;
   normalise_window(cap, window, sinks);
   PagedArgs a{q, k, v, k_cache, v_cache, page_table, lengths, o,
-              (float*)((unsigned char*)workspace + kStatusBytes), (unsigned int*)workspace,
-              N, Hq, Hkv, d, npages, page_shift_of(page), max_pages, window, sinks,
-              attn_decode_splits(N, Hq, Hkv, d, dtype, cap, window, sinks), scale, dtype};
+              (int2*)((unsigned char*)workspace + kStatusBytes),
+              (float*)((unsigned char*)workspace + kStatusBytes + first_bytes(N)),
+              (unsigned int*)workspace, N, Hq, Hkv, d, npages, page_shift_of(page), max_pages, window, sinks, scale, dtype,
+              0, 0, 0, 0.f, 0, false};
+  attn_decode_plan(a, cap);
+  if ((s = check_workspace(fn, workspace, ws_bytes, decode_need(a))) != GDR_OK) return s;
   return done(fn, launch_attn_decode(a, (cudaStream_t)stream));
 }
 

@@ -4,12 +4,18 @@
 //
 // Bound by HBM: every visible token's key and value are read once for all the query heads
 // of their group, 2 d e bytes a token and key head (e bytes an element) against 4 d flops a
-// query head.  A sequence's visible tokens (the sinks, then the window) are cut into up to
-// `nsplit` equal parts, each a CTA of four warps; a warp streams its own tiles of 16 tokens
-// through a private ring of shared-memory stages with 16-byte asynchronous copies, so no
-// barrier stands between the loads and the products, and keeps its own running maximum, sum
-// and output.  The warps of a CTA join in shared memory, the parts of a sequence in a second
-// small kernel that starts while the first one drains.
+// query head.  A sequence's visible tokens (the sinks, then the window) are cut into equal
+// parts, each a CTA of four or two warps; a warp streams its own tiles of 16 tokens through a private
+// ring of shared-memory stages with 16-byte asynchronous copies, so no barrier stands between
+// the loads and the products, and keeps its own running maximum, sum and output.  The warps of
+// a CTA join in shared memory, the parts of a sequence in a second small kernel that starts
+// while the first one drains.
+//
+// The lengths are on the device, so the cut is made there: every CTA adds up the batch's visible
+// tokens, takes parts of as many tokens as give each CTA that the GPU holds one part (few
+// sequences), or a quarter of its share but no less than 1024 (many), and looks up which part is
+// its own.  Many parts follow one another on an SM, so there a CTA has two warps, and an SM holds
+// twice as many: while one of them starts, which takes it about 3 us, the others read.
 //
 // bf16 with d = 64 or 128: the products run as m16n8k16 warp matrix instructions, 16 query
 // heads as the 16 rows (fewer heads leave rows unused, which costs nothing at this ratio of
@@ -27,7 +33,6 @@ namespace {
 
 using namespace attn;
 
-constexpr int kWarps = 4;
 constexpr int kTile = 16;           // tokens of a warp's tile
 
 // Records a length or page outside the cache (gdr_workspace_status: GDR_ERR_INVALID_ARG).
@@ -60,10 +65,65 @@ __device__ __forceinline__ Visible visible(const PagedArgs& a, int n, bool note)
   }
   return v;
 }
-// tokens of each part: whole tiles for all four warps, so that short sequences use few parts
-__device__ __forceinline__ int part_tokens(int count, int nsplit) {
-  const int per = (count + nsplit - 1) / nsplit;
-  return max(kWarps * kTile, (per + kTile - 1) / kTile * kTile);
+constexpr int kMaxSplit = 256;      // parts of a sequence
+constexpr int kLeast = 64;          // tokens of a part, where a sequence is cut at all
+
+// One part: `tokens` visible tokens from part * tokens on (fewer at the end, none in a part behind
+// it); `slot` is its place among all parts, -1 for a place behind the last one.
+struct Part {
+  int n, part, parts, tokens, slot;
+};
+// The part in place `slot`.  Each warp finds it by itself (no barrier): its lanes count the parts
+// of a run of sequences each.
+__device__ __forceinline__ Part find_part(const PagedArgs& a, int slot) {
+  if (a.nparts == 0) return Part{slot, 0, 1, 0x7fffffff, 0};
+  auto cut = [&](int n, int at, int parts, int count) {
+    // where the join finds the sequence's parts
+    if (slot == at && threadIdx.x == 0) a.first[n] = make_int2(at, parts);
+    const int tokens = (count + parts - 1) / parts;
+    return Part{n, slot - at, parts, max(kLeast, (tokens + kTile - 1) / kTile * kTile), slot};
+  };
+  if (a.stride) {
+    const int n = slot / a.stride, at = n * a.stride;
+    const int count = visible(a, n, false).count;
+    const int parts = min(kMaxSplit, max(1, (count + kLeast - 1) / kLeast));
+    if (slot - at >= parts) return Part{0, 0, 0, 0, -1};
+    return cut(n, at, parts, count);
+  }
+  const int lane = threadIdx.x & 31;
+  const int run = (a.N + 31) >> 5;
+  const int n0 = min(a.N, lane * run), n1 = min(a.N, n0 + run);
+  const int count0 = n0 < n1 ? visible(a, n0, false).count : 0;
+  auto count = [&](int n) { return n == n0 ? count0 : visible(a, n, false).count; };
+  long long all = count0;
+  for (int n = n0 + 1; n < n1; ++n) all += count(n);
+#pragma unroll
+  for (int f = 16; f; f >>= 1) all += __shfl_xor_sync(0xffffffffu, all, f);
+  // no less than all / places (the factor is rounded up), the same in every CTA
+  const unsigned per =
+      max((unsigned)a.least, (unsigned)fminf(__ll2float_ru(all) * a.per_place, 0x1p30f) + 1u);
+  auto parts_of = [&](int n) {
+    return (int)min((unsigned)kMaxSplit, max(1u, (count(n) + per - 1) / per));
+  };
+  const int parts0 = n0 < n1 ? parts_of(n0) : 0;
+  int mine = parts0;
+  for (int n = n0 + 1; n < n1; ++n) mine += parts_of(n);
+  int upto = mine;
+#pragma unroll
+  for (int f = 1; f < 32; f <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, upto, f);
+    if (lane >= f) upto += x;
+  }
+  const unsigned who = __ballot_sync(0xffffffffu, slot < upto);
+  if (who == 0) return Part{0, 0, 0, 0, -1};
+  const int src = __ffs(who) - 1;
+  int n = n0, c = parts0, at = upto - mine;
+  if (lane == src)
+    while (slot >= at + c) at += c, c = parts_of(++n);
+  n = __shfl_sync(0xffffffffu, n, src);
+  at = __shfl_sync(0xffffffffu, at, src);
+  c = __shfl_sync(0xffffffffu, c, src);
+  return cut(n, at, c, __shfl_sync(0xffffffffu, lane == src ? count(n) : 0, src));
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take) {
@@ -119,7 +179,7 @@ struct Rows {
 // The part that holds the last token stores the new key and value into their page (each key
 // head's by the CTA of the group's first 16 heads).  No other CTA touches that row: the
 // tokens of a sequence lie in different rows, and sequences do not share their last page.
-template <typename T, int D>
+template <typename T, int D, int W>
 __device__ __forceinline__ void store_new(const PagedArgs& a, const Visible& v, int n, int hk) {
   const int t = v.len - 1;
   const int pg = a.table[(size_t)n * a.max_pages + (t >> a.page_shift)];
@@ -129,7 +189,7 @@ __device__ __forceinline__ void store_new(const PagedArgs& a, const Visible& v, 
   }
   const size_t row = ((size_t)pg << a.page_shift) + (t & ((1 << a.page_shift) - 1));
   constexpr int V = 16 / sizeof(T);
-  for (int c = threadIdx.x * V; c < 2 * D; c += kWarps * 32 * V) {
+  for (int c = threadIdx.x * V; c < 2 * D; c += W * 32 * V) {
     const bool key = c < D;
     const T* src = (const T*)(key ? a.k_new : a.v_new) + ((size_t)n * a.Hkv + hk) * D + c % D;
     T* dst = (T*)(key ? a.kc : a.vc) + (row * a.Hkv + hk) * D + c % D;
@@ -140,53 +200,50 @@ __device__ __forceinline__ void store_new(const PagedArgs& a, const Visible& v, 
 // Writes one part's result: the output itself when there is only one part, else (o, m, l) of
 // the part for the join, with o not yet divided by the sum.
 template <typename T>
-__device__ __forceinline__ void emit(const PagedArgs& a, int n, int h, int part, int parts, int D,
-                                     int c, float o, float m, float l) {
-  if (parts == 1) {
-    Elem<T>::store((T*)a.o + ((size_t)n * a.Hq + h) * D + c, l != 0.f ? o / l : 0.f);
+__device__ __forceinline__ void emit(const PagedArgs& a, const Part& pt, int h, int D, int c,
+                                     float o, float m, float l) {
+  if (pt.parts == 1) {
+    Elem<T>::store((T*)a.o + ((size_t)pt.n * a.Hq + h) * D + c, l != 0.f ? o / l : 0.f);
     return;
   }
-  float* p = a.part + ((size_t)n * a.Hq + h) * a.nsplit * (D + 2);
-  p[(size_t)part * D + c] = o;
-  if (c == 0) {
-    p[(size_t)a.nsplit * D + 2 * part] = m;
-    p[(size_t)a.nsplit * D + 2 * part + 1] = l;
-  }
+  const size_t at = (size_t)pt.slot * a.Hq + h;
+  a.part[at * D + c] = o;
+  if (c == 0)
+    reinterpret_cast<float2*>(a.part + (size_t)a.nparts * a.Hq * D)[at] = make_float2(m, l);
 }
 
-template <int D>
+template <int D, int W>
 struct TcSmem {
   static constexpr int STAGES = 3;
   static constexpr int ROW = D * 2;                       // bytes of a token's key or value
   static constexpr int HALF = kTile * ROW;                // a tile's keys
-  static constexpr int WARP = STAGES * 2 * HALF;
-  static constexpr int RING = kWarps * WARP;
+  static constexpr int PER = STAGES * 2 * HALF;
+  static constexpr int RING = W * PER;
   static constexpr int BYTES = RING;                      // the join of the warps reuses it
-  static_assert(kWarps * 16 * (D + 4) * 4 + kWarps * 16 * 8 <= RING, "join area");
+  static_assert(W * 16 * (D + 4) * 4 + W * 16 * 8 <= RING, "join area");
 };
 
-template <int D>
-__global__ void __launch_bounds__(kWarps * 32)
+template <int D, int W>
+__global__ void __launch_bounds__(W * 32)
 attn_decode_tc(const PagedArgs a) {
-  using S = TcSmem<D>;
+  using S = TcSmem<D, W>;
   using bf16 = __nv_bfloat16;
   extern __shared__ __align__(128) unsigned char sm[];
   let_next_start();
   const int G = a.Hq / a.Hkv, nhb = (G + 15) / 16;
+  // the heads of a part run next to each other: their rows are neighbours in the pages
   int x = blockIdx.x;
-  const int part = x % a.nsplit;
-  x /= a.nsplit;
   const int hb = x % nhb;
   x /= nhb;
-  const int hk = x % a.Hkv, n = x / a.Hkv;
+  const int hk = x % a.Hkv;
+  const Part pt = find_part(a, x / a.Hkv);
+  if (pt.slot < 0) return;
+  const int n = pt.n, part = pt.part, parts = pt.parts;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const Visible vis = visible(a, n, tid == 0 && part == 0);
-  const int per = part_tokens(vis.count, a.nsplit);
-  const int parts = max(1, (vis.count + per - 1) / per);
-  if (part >= parts) return;
   const int h0 = hk * G + hb * 16, nh = min(16, G - hb * 16);
-  const int x0 = part * per, x1 = min(vis.count, x0 + per);
-  if (vis.fresh && hb == 0 && part == parts - 1) store_new<bf16, D>(a, vis, n, hk);
+  const int x0 = part * pt.tokens, x1 = x0 + max(0, min(vis.count - x0, pt.tokens));
+  if (vis.fresh && hb == 0 && part == parts - 1) store_new<bf16, D, W>(a, vis, n, hk);
 
   // query fragments, with the scale and log2 e applied to the scores later
   const int g = lane >> 2, t4 = lane & 3;
@@ -203,14 +260,14 @@ attn_decode_tc(const PagedArgs a) {
 
   // this warp's tiles: warp, warp + 4, ...
   const int ntile = (x1 - x0 + kTile - 1) / kTile;
-  const int mine = ntile > warp ? (ntile - warp + kWarps - 1) / kWarps : 0;
-  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(sm) + warp * S::WARP;
+  const int mine = ntile > warp ? (ntile - warp + W - 1) / W : 0;
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(sm) + warp * S::PER;
   constexpr int CH = D / 8;                 // 16-byte pieces of a row
   constexpr int RPI = 32 / CH;              // rows a warp instruction copies
   const Rows rows{a, vis, n};
   // lane l < 16 looks up row l of a tile; one tile ahead of the copies
   auto look = [&](int i) -> long {
-    return i < mine && lane < kTile ? rows.find(x0 + (warp + i * kWarps) * kTile + lane, x1) : -1;
+    return i < mine && lane < kTile ? rows.find(x0 + (warp + i * W) * kTile + lane, x1) : -1;
   };
   auto issue = [&](int i, long mrow) {
     const uint32_t st = ring + (i % S::STAGES) * 2 * S::HALF;
@@ -329,7 +386,7 @@ attn_decode_tc(const PagedArgs a) {
   }
   __syncthreads();
   float* jo = reinterpret_cast<float*>(sm);                 // [warp][16][D + 4]
-  float* jm = jo + kWarps * 16 * (D + 4);                   // [warp][16] m, then l
+  float* jm = jo + W * 16 * (D + 4);                   // [warp][16] m, then l
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
     const int row = g + 8 * w;
@@ -340,60 +397,59 @@ attn_decode_tc(const PagedArgs a) {
     }
     if (t4 == 0) {
       jm[warp * 16 + row] = mx[w];
-      jm[kWarps * 16 + warp * 16 + row] = sum[w];
+      jm[W * 16 + warp * 16 + row] = sum[w];
     }
   }
   __syncthreads();
-  for (int e = tid; e < nh * D; e += kWarps * 32) {
+  for (int e = tid; e < nh * D; e += W * 32) {
     const int row = e / D, ch = e % D;
     float m = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, jm[w * 16 + row]);
+    for (int w = 0; w < W; ++w) m = fmaxf(m, jm[w * 16 + row]);
     const float base = m == -INFINITY ? 0.f : m;
     float l = 0.f, v = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < W; ++w) {
       const float f = exp2f(jm[w * 16 + row] - base);
-      l = fmaf(f, jm[kWarps * 16 + w * 16 + row], l);
+      l = fmaf(f, jm[W * 16 + w * 16 + row], l);
       v = fmaf(f, jo[(w * 16 + row) * (D + 4) + ch], v);
     }
-    emit<bf16>(a, n, h0 + row, part, parts, D, ch, v, m, l);
+    emit<bf16>(a, pt, h0 + row, D, ch, v, m, l);
   }
 }
 
 // fp32 arithmetic: a warp's tile is 32 tokens; 8 query heads at a time.
-constexpr int kSTile = 32, kSHeads = 8;
+constexpr int kSWarps = 4, kSTile = 32, kSHeads = 8;
 
 template <typename T, int D>
 struct SimtSmem {
-  float kv[kWarps][kSTile][D + 4];     // keys, then values; then the warps' outputs
+  float kv[kSWarps][kSTile][D + 4];     // keys, then values; then the warps' outputs
   float q[kSHeads][D];
-  float p[kWarps][kSHeads][kSTile];
-  float m[kWarps][kSHeads], l[kWarps][kSHeads];
+  float p[kSWarps][kSHeads][kSTile];
+  float m[kSWarps][kSHeads], l[kSWarps][kSHeads];
 };
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(kSWarps * 32)
 attn_decode_simt(const PagedArgs a) {
   extern __shared__ __align__(128) unsigned char raw[];
   SimtSmem<T, D>& sm = *reinterpret_cast<SimtSmem<T, D>*>(raw);
   let_next_start();
   const int G = a.Hq / a.Hkv, nhb = (G + kSHeads - 1) / kSHeads;
+  // the heads of a part run next to each other: their rows are neighbours in the pages
   int x = blockIdx.x;
-  const int part = x % a.nsplit;
-  x /= a.nsplit;
   const int hb = x % nhb;
   x /= nhb;
-  const int hk = x % a.Hkv, n = x / a.Hkv;
+  const int hk = x % a.Hkv;
+  const Part pt = find_part(a, x / a.Hkv);
+  if (pt.slot < 0) return;
+  const int n = pt.n, part = pt.part, parts = pt.parts;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const Visible vis = visible(a, n, tid == 0 && part == 0);
-  const int per = part_tokens(vis.count, a.nsplit);
-  const int parts = max(1, (vis.count + per - 1) / per);
-  if (part >= parts) return;
   const int h0 = hk * G + hb * kSHeads, nh = min(kSHeads, G - hb * kSHeads);
-  const int x0 = part * per, x1 = min(vis.count, x0 + per);
-  if (vis.fresh && hb == 0 && part == parts - 1) store_new<T, D>(a, vis, n, hk);
-  for (int e = tid; e < kSHeads * D; e += kWarps * 32)
+  const int x0 = part * pt.tokens, x1 = x0 + max(0, min(vis.count - x0, pt.tokens));
+  if (vis.fresh && hb == 0 && part == parts - 1) store_new<T, D, kSWarps>(a, vis, n, hk);
+  for (int e = tid; e < kSHeads * D; e += kSWarps * 32)
     sm.q[e / D][e % D] =
         e / D < nh ? Elem<T>::load((const T*)a.q + ((size_t)n * a.Hq + h0 + e / D) * D + e % D)
                    : 0.f;
@@ -405,7 +461,7 @@ attn_decode_simt(const PagedArgs a) {
   const float c = a.scale * kLog2e;
   const Rows rows{a, vis, n};
   float (*kv)[D + 4] = sm.kv[warp];
-  for (int b = x0 + warp * kSTile; b < x1; b += kWarps * kSTile) {
+  for (int b = x0 + warp * kSTile; b < x1; b += kSWarps * kSTile) {
     const long mrow = rows.find(b + lane, x1);
     auto load = [&](const void* cache, const void* fresh) {
       constexpr int CH = D / 4;
@@ -473,27 +529,26 @@ attn_decode_simt(const PagedArgs a) {
     }
   }
   __syncthreads();
-  for (int e = tid; e < nh * D; e += kWarps * 32) {
+  for (int e = tid; e < nh * D; e += kSWarps * 32) {
     const int h = e / D, ch = e % D;
     float m = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sm.m[w][h]);
+    for (int w = 0; w < kSWarps; ++w) m = fmaxf(m, sm.m[w][h]);
     const float base = m == -INFINITY ? 0.f : m;
     float l = 0.f, v = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < kSWarps; ++w) {
       const float f = exp2f(sm.m[w][h] - base);
       l = fmaf(f, sm.l[w][h], l);
       v = fmaf(f, sm.kv[w][h][ch], v);
     }
-    emit<T>(a, n, h0 + h, part, parts, D, ch, v, m, l);
+    emit<T>(a, pt, h0 + h, D, ch, v, m, l);
   }
 }
 
 // Joins the parts of each (sequence, query head): four warps take the parts in turn, their
 // weights formed by all lanes beforehand, so that the loads of the outputs do not wait for one
 // another (a warp alone, a part at a time, took 23 us over 32 parts).
-constexpr int kMaxSplit = 256;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(128)
@@ -501,18 +556,20 @@ attn_decode_join(const PagedArgs a) {
   __shared__ float wt[kMaxSplit], acc[4][D], red[2][4];
   const int nh = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   wait_for_previous();
-  const Visible vis = visible(a, nh / a.Hq, false);
-  const int per = part_tokens(vis.count, a.nsplit);
-  const int parts = (vis.count + per - 1) / per;
+  const int2 of = a.first[nh / a.Hq];
+  const int parts = of.y;
   if (parts <= 1) return;
-  const float* p = a.part + (size_t)nh * a.nsplit * (D + 2);
-  const float2* ml = reinterpret_cast<const float2*>(p + (size_t)a.nsplit * D);
+  // part s of this head lies s * Hq further on
+  const size_t at = (size_t)of.x * a.Hq + nh % a.Hq;
+  const float* p = a.part + at * D;
+  const float2* ml = reinterpret_cast<const float2*>(a.part + (size_t)a.nparts * a.Hq * D) + at;
+  const size_t step = a.Hq;
   constexpr int PT = kMaxSplit / 128;
   float2 x[PT];
   float m = -INFINITY;
 #pragma unroll
   for (int e = 0; e < PT; ++e) {
-    x[e] = tid + 128 * e < parts ? ml[tid + 128 * e] : make_float2(-INFINITY, 0.f);
+    x[e] = tid + 128 * e < parts ? ml[(tid + 128 * e) * step] : make_float2(-INFINITY, 0.f);
     m = fmaxf(m, x[e].x);
   }
 #pragma unroll
@@ -538,7 +595,7 @@ attn_decode_join(const PagedArgs a) {
   for (int s = warp; s < parts; s += 4) {
     const float f = wt[s];
 #pragma unroll
-    for (int e = 0; e < CPL; ++e) o[e] = fmaf(f, p[(size_t)s * D + lane + 32 * e], o[e]);
+    for (int e = 0; e < CPL; ++e) o[e] = fmaf(f, p[s * step * D + lane + 32 * e], o[e]);
   }
 #pragma unroll
   for (int e = 0; e < CPL; ++e) acc[warp][lane + 32 * e] = o[e];
@@ -579,30 +636,63 @@ kv_append_kernel(const AppendArgs a) {
 }
 
 template <typename K>
-cudaError_t launch_main(K kern, int smem, const PagedArgs& a, unsigned grid, cudaStream_t st,
-                        std::atomic<unsigned long long>& done) {
+cudaError_t launch_main(K kern, int threads, int smem, const PagedArgs& a, int heads,
+                        cudaStream_t st, std::atomic<unsigned long long>& done) {
   cudaError_t e = allow_smem(kern, smem, done);
   if (e != cudaSuccess) return e;
-  kern<<<grid, kWarps * 32, smem, st>>>(a);
+  const int blocks = (a.Hq / a.Hkv + heads - 1) / heads;
+  const unsigned grid = (unsigned)((size_t)(a.nparts ? a.nparts : a.N) * a.Hkv * blocks);
+  kern<<<grid, threads, smem, st>>>(a);
   return cudaGetLastError();
 }
 
 template <typename T, int D>
 cudaError_t launch_t(const PagedArgs& a, cudaStream_t st) {
-  const int G = a.Hq / a.Hkv;
-  static std::atomic<unsigned long long> done{0};
+  static std::atomic<unsigned long long> done{0}, done2{0};
   cudaError_t e;
   if constexpr (sizeof(T) == 2 && D >= 64) {
-    const unsigned grid = (unsigned)((size_t)a.N * a.Hkv * ((G + 15) / 16) * a.nsplit);
-    e = launch_main(attn_decode_tc<D>, TcSmem<D>::BYTES, a, grid, st, done);
+    e = a.four_warps
+            ? launch_main(attn_decode_tc<D, 4>, 128, TcSmem<D, 4>::BYTES, a, 16, st, done)
+            : launch_main(attn_decode_tc<D, 2>, 64, TcSmem<D, 2>::BYTES, a, 16, st, done2);
   } else {
-    const unsigned grid =
-        (unsigned)((size_t)a.N * a.Hkv * ((G + kSHeads - 1) / kSHeads) * a.nsplit);
-    e = launch_main(attn_decode_simt<T, D>, (int)sizeof(SimtSmem<T, D>), a, grid, st,
-                    done);
+    e = launch_main(attn_decode_simt<T, D>, kSWarps * 32, (int)sizeof(SimtSmem<T, D>), a, kSHeads,
+                    st, done);
   }
-  if (e != cudaSuccess || a.nsplit == 1) return e;
+  if (e != cudaSuccess || a.nparts == 0) return e;
   return launch_after(attn_decode_join<T, D>, dim3((unsigned)(a.N * a.Hq)), 128, 0, st, a);
+}
+
+// CTAs of `bytes` of shared memory and `threads` of 128 registers that an SM holds.
+constexpr int held(int bytes, int threads) {
+  const int by_smem = 227 * 1024 / (bytes + 1024), by_regs = 512 / threads;
+  return by_smem < by_regs ? by_smem : by_regs;
+}
+
+// How the visible tokens are cut (the comment at the top).  The number of places for parts
+// follows from the sizes alone; CTAs of places without a part leave after the count.  Few tokens
+// need no count: when parts of kLeast have a place each in one round, each sequence has `stride`
+// places.  With more than 1024 sequences counting would take too long, and balance is good
+// without a cut.  Measured, four warps against two in a single round: 16 sequences of 4096 (8 key
+// heads, d = 128) 54 us and 50, 32 with a window of 1024 (2 key heads) 15.0 and 16.7; parts of
+// 1024 against 512 in several rounds: 64 sequences of 1000 46 us and 54.
+template <typename T, int D>
+void plan_t(PagedArgs& a, long most) {
+  constexpr bool tc = sizeof(T) == 2 && D >= 64;
+  constexpr int heads = tc ? 16 : kSHeads;
+  const long chains = (long)a.Hkv * ((a.Hq / a.Hkv + heads - 1) / heads);
+  constexpr int held4 = tc ? held(TcSmem<D, 4>::BYTES, 128) : held(sizeof(SimtSmem<T, D>), 128);
+  constexpr int held2 = tc ? held(TcSmem<D, 2>::BYTES, 64) : held4;
+  const long round4 = 148L * held4 / chains, round2 = 148L * held2 / chains;
+  const bool one = 2L * a.N <= round2;        // (a part of each sequence may be a short one)
+  a.four_warps = 3L * a.N <= round4;
+  a.least = one ? kLeast : 1024;
+  const long places = a.four_warps ? round4 - a.N : one ? round2 - a.N : 4 * round2;
+  a.places = places < 1 ? 1 : (int)places;
+  a.per_place = 1.0f / (float)a.places * 1.000001f;
+  const long each = (most + a.least - 1) / a.least, by_tokens = a.N * each;
+  a.stride = a.four_warps && by_tokens <= round4 ? (int)each : 0;
+  const long n = a.places + a.N < by_tokens && !a.stride ? a.places + (long)a.N : by_tokens;
+  a.nparts = a.N > 1024 || n <= a.N ? 0 : (int)n;
 }
 
 template <typename T>
@@ -614,25 +704,20 @@ cudaError_t launch_d(const PagedArgs& a, cudaStream_t st) {
   }
   return cudaErrorInvalidValue;
 }
+template <typename T>
+void plan_d(PagedArgs& a, long most) {
+  if (a.d == 32) plan_t<T, 32>(a, most);
+  if (a.d == 64) plan_t<T, 64>(a, most);
+  if (a.d == 128) plan_t<T, 128>(a, most);
+}
 
 }  // namespace
 
-// How many parts a sequence's tokens may be cut into.  The grid is the same for every
-// length (the lengths are on the device), and parts past a short sequence's end leave at
-// once, so it is chosen from what the page table can hold: enough CTAs for sixteen on each
-// SM, which also evens out sequences of different lengths, and no part below 64 tokens.
-int attn_decode_splits(int N, int Hq, int Hkv, int d, int dtype, long capacity, int window,
-                       int sinks) {
-  const int G = Hq / Hkv;
-  const int hb = dtype == GDR_BF16 && d >= 64 ? (G + 15) / 16 : (G + kSHeads - 1) / kSHeads;
-  const long base = (long)N * Hkv * hb;
+void attn_decode_plan(PagedArgs& a, long capacity) {
   long most = capacity;
-  if (window && most > (long)window + sinks) most = (long)window + sinks;
-  const long by_tokens = (most + kWarps * kTile - 1) / (kWarps * kTile);
-  const long by_ctas = (148L * 16 + base - 1) / base;
-  long s = by_tokens < by_ctas ? by_tokens : by_ctas;
-  if (s < 1) s = 1;
-  return (int)(s > kMaxSplit ? kMaxSplit : s);
+  if (a.window && most > (long)a.window + a.sinks) most = (long)a.window + a.sinks;
+  if (a.dtype == GDR_F32) plan_d<float>(a, most);
+  else plan_d<__nv_bfloat16>(a, most);
 }
 
 cudaError_t launch_attn_decode(const PagedArgs& a, cudaStream_t st) {

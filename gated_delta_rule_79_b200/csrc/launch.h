@@ -182,14 +182,19 @@ struct PagedArgs {
   const int* table;     // [N, max_pages]
   const int* lengths;   // [N]
   void* o;              // [N, Hq, d]
-  float* part;          // [N, Hq] x (nsplit x d outputs, nsplit x (max, sum))
+  int2* first;          // [N] a sequence's first part and their number
+  float* part;          // [nparts, Hq] x d outputs, then [nparts, Hq] x (max, sum)
   unsigned int* status;
-  int N, Hq, Hkv, d, npages, page_shift, max_pages, window, sinks, nsplit;
+  int N, Hq, Hkv, d, npages, page_shift, max_pages, window, sinks;
   float scale;
   int dtype;
+  // parts hold tokens / places of them, but no less than `least`; room for `nparts` (0: uncut)
+  int places, least, nparts;
+  float per_place;      // 1 / places, rounded up
+  int stride;           // places of each sequence, or 0: as the tokens fall
+  bool four_warps;      // of a CTA, or two
 };
-int attn_decode_splits(int N, int Hq, int Hkv, int d, int dtype, long capacity, int window,
-                       int sinks);
+void attn_decode_plan(PagedArgs& a, long capacity);   // sets the last six
 cudaError_t launch_attn_decode(const PagedArgs& a, cudaStream_t stream);
 
 struct AppendArgs {

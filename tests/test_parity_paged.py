@@ -116,6 +116,34 @@ def test_stores_the_new_token(dtype, d, Hq, Hkv):
     assert torch.equal(kc.view(bits), full_k.view(bits)) and torch.equal(vc.view(bits), full_v.view(bits))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens,Hq,Hkv,d,extra", [
+    ([1500, 3, 700], 4, 2, 128, 200),                        # a table far larger than its contents
+    ([900] + [13 * i % 41 for i in range(69)], 2, 1, 64, 20),     # more sequences than lanes
+    ([600, 0, 470] + [9 * i + 1 for i in range(17)], 8, 8, 128, 10),
+    ([2100, 1500, 0, 7, 1024], 1184, 1, 128, 1),             # several rounds of CTAs: large parts
+    ([i % 23 for i in range(1030)], 1, 1, 64, 0),            # too many sequences to be cut
+])
+def test_batches_that_are_cut_unevenly(dtype, lens, Hq, Hkv, d, extra):
+    import gated_delta_rule_79_b200 as g
+    c = Cache(lens, Hkv, d, 64, dtype, extra=extra, seed=6)
+    N = len(lens)
+    q, knew, vnew = randn((N, Hq, d), 9, dtype), randn((N, Hkv, d), 1, dtype), randn((N, Hkv, d), 2, dtype)
+    for i, n in enumerate(lens):
+        if n:
+            p, r = int(c.table[i, (n - 1) // 64]), (n - 1) % 64
+            knew[i], vnew[i] = c.k[i][n - 1], c.v[i][n - 1]
+            c.kc[p, r], c.vc[p, r] = float("nan"), float("nan")
+    kc, vc, table, t = c.cuda()
+    ws = torch.zeros(g.attn_decode_workspace_bytes(N, Hq, Hkv, d, 64, c.per, DT[dtype]),
+                     dtype=torch.uint8, device="cuda")
+    o = g.attn_decode(q.cuda(), kc, vc, table, t, k=knew.cuda(), v=vnew.cuda(), workspace=ws)
+    g.workspace_status(ws)
+    _check(c, q, o, dtype)
+    again = g.attn_decode(q.cuda(), kc, vc, table, t)           # the new tokens were stored
+    assert torch.equal(o, again)
+
+
 def test_pages_and_lengths_outside_the_cache_are_left_out_and_reported():
     import gated_delta_rule_79_b200 as g
     c = Cache([100, 100, 100], 2, 128, 16, "bf16")
