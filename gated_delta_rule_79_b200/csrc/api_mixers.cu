@@ -155,7 +155,7 @@ size_t attn_need(const AttnArgs& a, bool backward) {
   if (a.B == 0 || a.Tq == 0 || a.Tk == 0 || a.Hq == 0) return kStatusBytes;
   const bool tc = attn_tc(a.d, a.dtype);
   if (!backward) return kStatusBytes + (tc ? attn_forward_tc_bytes(a) : 0);
-  return kStatusBytes + attn_delta_bytes(a) + (tc ? attn_backward_tc_bytes(a) : 0);
+  return kStatusBytes + attn_delta_bytes(a) + (tc ? attn_backward_tc_bytes(a) : attn_backward_simt_bytes(a));
 }
 
 int page_shift_of(int page) {

@@ -14,7 +14,7 @@
 // x 6 heads x 3 sequences (d = 64, forward + dk, dv + dq): tiles of 64 rows by 256 threads took
 // 129 + 204 + 162 us, of 32 rows by one group 92 + 155 + 119.
 
-#include "attn_common.cuh"
+#include "attn_parts.cuh"
 #include "once.h"
 
 namespace gdr {
@@ -130,6 +130,22 @@ __device__ __forceinline__ void store_rows(T* x, size_t row_stride, int r0, int 
                          acc[a][g * C::W + e]);
     }
   }
+}
+
+// a part's sums as part_at places them
+template <int D>
+__device__ __forceinline__ void store_part(float* x, int ty, int tx,
+                                           const float (&acc)[4][Cols<D>::N]) {
+  using C = Cols<D>;
+#pragma unroll
+  for (int a = 0; a < 4; ++a)
+#pragma unroll
+    for (int g = 0; g < C::G; ++g)
+#pragma unroll
+      for (int e = 0; e < C::W; ++e) {
+        const int c = tx * C::W + 16 * C::W * g + e;
+        x[((c >> 3) * kA + 4 * ty + a) * 8 + (c & 7)] = acc[a][g * C::W + e];
+      }
 }
 
 __device__ __forceinline__ float row_max(float x) {   // over the 16 lanes of a tile row
@@ -346,28 +362,33 @@ struct DkvSmem {
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads)
-attn_dkv_simt(const AttnGradArgs a) {
+attn_dkv_simt(const AttnGradArgs a, const Parts parts) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   DkvSmem<D>& sm = *reinterpret_cast<DkvSmem<D>*>(smem_raw);
   const AttnArgs& f = a.f;
   // the first keys, which the most queries see without a window, start first
   const int bh = blockIdx.x % (f.B * f.Hkv), hk = bh % f.Hkv, b = bh / f.Hkv;
-  const int j0 = (int)(blockIdx.x / (unsigned)(f.B * f.Hkv)) * kA;
+  const int item = blockIdx.x / (unsigned)(f.B * f.Hkv);
+  int tile, part, most;
+  parts.locate(item, tile, part, most);
+  const int j0 = tile * kA;
   const int G = f.Hq / f.Hkv;
   const int grp = threadIdx.x / kGroup, tid = threadIdx.x % kGroup, ty = tid >> 4, tx = tid & 15;
   const Mask m = make_mask(f.lengths, b, f.Tq, f.Tk, f.window, f.sinks);
+  int first, nt;
+  tile_steps<kA, kB>(m, j0, f.Tk, f.Tq, first, nt);
+  const int used = parts.used(G * nt, most);
+  if (part >= used) return;
+  const int per = (G * nt + used - 1) / used, x1 = min(G * nt, (part + 1) * per);
   const size_t qs = (size_t)f.Hq * D, ks = (size_t)f.Hkv * D;
   const size_t kat = (size_t)b * f.Tk * ks + (size_t)hk * D;
   load_tile<T, D, kA, kThreads>(sm.k, (const T*)f.k + kat, ks, j0, m.len, threadIdx.x);
   load_tile<T, D, kA, kThreads>(sm.v, (const T*)f.v + kat, ks, j0, m.len, threadIdx.x);
   __syncthreads();
   auto& st = sm.g[grp];
-  int lo, hi;
-  query_range(m, j0, min(j0 + kA, f.Tk) - 1, f.Tq, lo, hi);
   const int end = min(f.Tq, m.len - m.off);
   float dk[4][Cols<D>::N] = {}, dv[4][Cols<D>::N] = {};
-  const int first = lo / kB, nt = hi > lo ? (hi + kB - 1) / kB - first : 0;
-  for (int x = grp; x < G * nt; x += 2) {
+  for (int x = part * per + grp; x < x1; x += 2) {
     const int h = hk * G + x / nt, i0 = (first + x % nt) * kB;
     const size_t qat = (size_t)b * f.Tq * qs + (size_t)h * D;
     group_sync(grp);
@@ -398,7 +419,11 @@ attn_dkv_simt(const AttnGradArgs a) {
   }
   const bool mine = join_groups(sm.g[1].q, grp, ty, tx, dk);
   join_groups(sm.g[1].d, grp, ty, tx, dv);
-  if (mine) {
+  if (mine && used > 1) {
+    float* pv = a.part + part_at(f, kA, D, item, bh, 0, 0, 0);
+    store_part<D>(pv, ty, tx, dv);
+    store_part<D>(pv + kA * D, ty, tx, dk);
+  } else if (mine) {
     store_rows<T, D>((T*)a.dk + kat, ks, j0, f.Tk, ty, tx, dk);
     store_rows<T, D>((T*)a.dv + kat, ks, j0, f.Tk, ty, tx, dv);
   }
@@ -463,6 +488,9 @@ cudaError_t delta_t(const AttnGradArgs& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
+// (two CTAs on an SM)
+Parts plan_simt(const AttnArgs& f) { return plan_parts<kA, kB>(f, 2 * 148); }
+
 template <typename T, int D>
 cudaError_t backward_t(const AttnGradArgs& a, cudaStream_t st) {
   auto kq = attn_dq_simt<T, D>;
@@ -473,8 +501,10 @@ cudaError_t backward_t(const AttnGradArgs& a, cudaStream_t st) {
   if (e == cudaSuccess)
     e = allow_smem(kk, sk, done2);
   if (e != cudaSuccess) return e;
-  kk<<<(unsigned)((a.f.Tk + kA - 1) / kA) * (unsigned)(a.f.Hkv * a.f.B), kThreads, sk, st>>>(a);
+  const Parts p = plan_simt(a.f);
+  kk<<<(unsigned)p.items() * (unsigned)(a.f.Hkv * a.f.B), kThreads, sk, st>>>(a, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if ((e = launch_dkv_join<T, D, kA, kB>(a, p, st)) != cudaSuccess) return e;
   kq<<<(unsigned)((a.f.Tq + kA - 1) / kA) * (unsigned)(a.f.Hq * a.f.B), kThreads, sq, st>>>(a);
   return cudaGetLastError();
 }
@@ -495,6 +525,7 @@ cudaError_t backward_t(const AttnGradArgs& a, cudaStream_t st) {
     return cudaErrorInvalidValue;                                                   \
   } while (0)
 
+size_t attn_backward_simt_bytes(const AttnArgs& f) { return part_bytes(f, kA, plan_simt(f)); }
 cudaError_t launch_attn_forward_simt(const AttnArgs& a, cudaStream_t st) {
   GDR_BY_TYPE(forward_t, a.dtype, a.d, a, st);
 }

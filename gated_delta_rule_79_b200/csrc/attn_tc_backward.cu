@@ -23,10 +23,9 @@
 // free: four or eight more products a step (15 % of the time at a window of 1024, where it is not
 // done; the error of dq is 1.1 times the rounding of the result with it, 1.5 without).
 //
-// A key tile that many queries see (one with sinks, or an early one without a window) would keep
-// its CTA busy after the others have finished: its queries are cut into parts of about the mean
-// load of an SM, whose fp32 sums a small kernel adds in order.
+// Key tiles that many queries see are cut (attn_parts.cuh).
 
+#include "attn_parts.cuh"
 #include "attn_tc.cuh"
 #include "once.h"
 #include "tma_host.h"
@@ -352,34 +351,6 @@ attn_dq_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
   wait_for_previous();
 }
 
-// How key tiles are cut: tiles [0, nfirst) into up to pfirst parts, the others into up to
-// prest, so that a part has about `cap` steps (a step: 64 queries of one head).
-struct Parts {
-  int nfirst, pfirst, prest, cap, ntiles;
-  __host__ __device__ int items() const { return nfirst * pfirst + (ntiles - nfirst) * prest; }
-  __host__ __device__ void locate(int item, int& tile, int& part, int& most) const {
-    if (item < nfirst * pfirst) {
-      tile = item / pfirst, part = item % pfirst, most = pfirst;
-    } else {
-      const int r = item - nfirst * pfirst;
-      tile = nfirst + r / prest, part = r % prest, most = prest;
-    }
-  }
-  __host__ __device__ int used(int steps, int most) const {
-    const int p = (steps + cap - 1) / cap;
-    return p < 1 ? 1 : p > most ? most : p;
-  }
-};
-
-// The steps of a key tile: tiles of 64 queries from lo64, nt of them for each head.
-__device__ __forceinline__ void tile_steps(const Mask& m, int j0, int Tk, int Tq, int& lo64,
-                                           int& nt) {
-  int lo, hi;
-  query_range(m, j0, min(j0 + kA, Tk) - 1, Tq, lo, hi);
-  lo64 = lo / kS;
-  nt = hi > lo ? (hi + kS - 1) / kS - lo64 : 0;
-}
-
 template <int D, bool FINE>
 __global__ void __launch_bounds__(kWarpsB * 32, 1)
 attn_dkv_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -399,7 +370,7 @@ attn_dkv_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
   const int j0 = tile * kA;
   const Mask m = make_mask(f.lengths, b, f.Tq, f.Tk, f.window, f.sinks);
   int lo64, nt;
-  tile_steps(m, j0, f.Tk, f.Tq, lo64, nt);
+  tile_steps<kA, kS>(m, j0, f.Tk, f.Tq, lo64, nt);
   const int used = parts.used(G * nt, most);
   let_next_start();
   if (part >= used) return;
@@ -486,7 +457,7 @@ attn_dkv_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                      (__nv_bfloat16*)(w ? a.dk : a.dv) +
                          (((size_t)b * f.Tk + j) * f.Hkv + hk) * D);
       } else {
-        float* dst = a.part + ((((size_t)item * f.B * f.Hkv + bh) * 2 + w) * kA + row) * D;
+        float* dst = a.part + part_at(f, kA, D, item, bh, w, row, 0);
 #pragma unroll
         for (int q = 0; q < D / 32; ++q) {
           float o[32];
@@ -496,7 +467,7 @@ attn_dkv_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
           }
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            reinterpret_cast<float4*>(dst + 32 * q)[e] =
+            reinterpret_cast<float4*>(dst + (size_t)(4 * q + (e >> 1)) * kA * 8)[e & 1] =
                 n > 0 ? make_float4(o[4 * e] * scale, o[4 * e + 1] * scale, o[4 * e + 2] * scale,
                                     o[4 * e + 3] * scale)
                       : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -549,80 +520,6 @@ attn_dkv_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
   if (warp == 0) tmem_dealloc(tb, 512);
 }
 
-// Adds the parts of a key tile in order: a thread for eight channels of a row of dv or dk.
-template <int D>
-__global__ void __launch_bounds__(256)
-attn_dkv_join(const AttnGradArgs a, const Parts parts) {
-  const AttnArgs& f = a.f;
-  constexpr int BLOCKS = kA * (D / 8) * 2 / 256;         // a piece a thread
-  const int at = blockIdx.x / BLOCKS;
-  const int bh = at % (f.B * f.Hkv), tile = at / (f.B * f.Hkv);
-  const int b = bh / f.Hkv, hk = bh % f.Hkv;
-  const int j0 = tile * kA;
-  const Mask m = make_mask(f.lengths, b, f.Tq, f.Tk, f.window, f.sinks);
-  int lo64, nt;
-  tile_steps(m, j0, f.Tk, f.Tq, lo64, nt);
-  const bool head = tile < parts.nfirst;
-  const int most = head ? parts.pfirst : parts.prest;
-  const int used = parts.used(f.Hq / f.Hkv * nt, most);
-  if (used == 1) return;
-  const int item = head ? tile * parts.pfirst
-                        : parts.nfirst * parts.pfirst + (tile - parts.nfirst) * parts.prest;
-  const size_t step = (size_t)f.B * f.Hkv * 2 * kA * D;      // from a part to the next
-  const int e = blockIdx.x % BLOCKS * 256 + threadIdx.x;
-  const int w = e / (kA * (D / 8)), row = e / (D / 8) % kA, c = e % (D / 8) * 8;
-  if (j0 + row >= f.Tk) return;
-  const float* src = a.part + ((((size_t)item * f.B * f.Hkv + bh) * 2 + w) * kA + row) * D + c;
-  float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-#pragma unroll 4
-  for (int p = 0; p < used; ++p) {
-    const float4 u = *reinterpret_cast<const float4*>(src + p * step);
-    const float4 v = *reinterpret_cast<const float4*>(src + p * step + 4);
-    x.x += u.x, x.y += u.y, x.z += u.z, x.w += u.w;
-    y.x += v.x, y.y += v.y, y.z += v.z, y.w += v.w;
-  }
-  *reinterpret_cast<float4*>((__nv_bfloat16*)(w ? a.dk : a.dv) +
-                             (((size_t)b * f.Tk + j0 + row) * f.Hkv + hk) * D + c) =
-      make_float4(pack2(x.x, x.y), pack2(x.z, x.w), pack2(y.x, y.y), pack2(y.z, y.w));
-}
-
-// Steps of a key tile when every sequence is whole (the host's tile_steps).
-long host_steps(const AttnArgs& f, int tile) {
-  const long off = (long)f.Tk - f.Tq, j0 = (long)tile * kA;
-  const long j1 = (j0 + kA < f.Tk ? j0 + kA : f.Tk) - 1;
-  const long lo = j0 - off > 0 ? j0 - off : 0;
-  long last = f.Tk - 1;
-  if (f.window && j0 >= f.sinks && j1 + f.window - 1 < last) last = j1 + f.window - 1;
-  const long hi = f.Tq < last - off + 1 ? f.Tq : last - off + 1;
-  return hi > lo ? ((hi + kS - 1) / kS - lo / kS) * (f.Hq / f.Hkv) : 0;
-}
-
-// The cap is the mean number of steps an SM gets with a quarter on top (parts cost a pass of
-// fp32 sums through memory, so a little imbalance is cheaper), and no part is below 64 steps.
-Parts plan_parts(const AttnArgs& f) {
-  Parts p;
-  p.ntiles = (f.Tk + kA - 1) / kA;
-  p.nfirst = f.window ? (f.sinks + kA - 1) / kA : 0;
-  if (p.nfirst > p.ntiles) p.nfirst = p.ntiles;
-  long total = 0, mfirst = 0, mrest = 0;
-  for (int t = 0; t < p.ntiles; ++t) {
-    const long s = host_steps(f, t);
-    total += s;
-    long& most = t < p.nfirst ? mfirst : mrest;
-    if (s > most) most = s;
-  }
-  total *= (long)f.B * f.Hkv;
-  long cap = total * 5 / (4 * 148) + 1;
-  if (cap < 64) cap = 64;
-  if (cap > (1 << 28)) cap = 1 << 28;
-  p.cap = (int)cap;
-  p.pfirst = (int)((mfirst + cap - 1) / cap);
-  p.prest = (int)((mrest + cap - 1) / cap);
-  if (p.pfirst < 1) p.pfirst = 1;
-  if (p.prest < 1) p.prest = 1;
-  return p;
-}
-
 template <int D, bool FINE>
 cudaError_t launch_t(const AttnGradArgs& a, cudaStream_t st) {
   using L = BwdLayout<D>;
@@ -643,29 +540,21 @@ cudaError_t launch_t(const AttnGradArgs& a, cudaStream_t st) {
     e = allow_smem(kk, L::SMEM, done2);
   if (e != cudaSuccess) return e;
   const uint32_t spin = attn_spin_limit();
-  const Parts p = plan_parts(f);
+  const Parts p = plan_parts<kA, kS>(f, 148);
   const unsigned bh = (unsigned)(f.B * f.Hkv);
   kk<<<(unsigned)p.items() * bh, kWarpsB * 32, L::SMEM, st>>>(kb, vb, qs, ds, a, p, spin);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   e = launch_after(kq, dim3((unsigned)((f.Tq + kA - 1) / kA * f.Hq * f.B)), kWarpsB * 32, L::SMEM,
                    st, ks, vs, a, spin);
   if (e != cudaSuccess) return e;
-  if (p.pfirst > 1 || p.prest > 1) {
-    const unsigned tiles = (unsigned)(p.prest > 1 ? p.ntiles : p.nfirst);
-    attn_dkv_join<D><<<tiles * bh * (kA * (D / 8) * 2 / 256), 256, 0, st>>>(a, p);
-    e = cudaGetLastError();
-  }
-  return e;
+  return launch_dkv_join<__nv_bfloat16, D, kA, kS>(a, p, st);
 }
 
 }  // namespace
 
 // Workspace of the parts' sums (0 when no tile is cut).
 size_t attn_backward_tc_bytes(const AttnArgs& f) {
-  const Parts p = plan_parts(f);
-  if (p.pfirst == 1 && p.prest == 1) return 0;
-  const size_t items = p.prest > 1 ? p.items() : p.nfirst * p.pfirst;
-  return items * f.B * f.Hkv * 2 * kA * f.d * sizeof(float);
+  return part_bytes(f, kA, plan_parts<kA, kS>(f, 148));
 }
 
 cudaError_t launch_attn_backward_tc(const AttnGradArgs& a, cudaStream_t st) {

@@ -160,7 +160,7 @@ struct AttnGradArgs {
   AttnArgs f;           // the forward's arguments and results
   const void* dO;
   float* delta;         // [B, Hq, Tq] workspace: do . o of every row
-  float* part;          // workspace of attn_backward_tc_bytes(f): sums of parts of key tiles
+  float* part;          // workspace of attn_backward_.._bytes(f): sums of parts of key tiles
   void* dq;
   void* dk;
   void* dv;
@@ -170,6 +170,7 @@ cudaError_t launch_attn_forward_tc(const AttnArgs& a, cudaStream_t stream);   //
 cudaError_t launch_attn_delta(const AttnGradArgs& a, cudaStream_t stream);
 size_t attn_forward_tc_bytes(const AttnArgs& a);
 size_t attn_backward_tc_bytes(const AttnArgs& f);
+size_t attn_backward_simt_bytes(const AttnArgs& f);
 cudaError_t launch_attn_backward_tc(const AttnGradArgs& a, cudaStream_t stream);  // bf16, d >= 64
 cudaError_t launch_attn_backward_simt(const AttnGradArgs& a, cudaStream_t stream);
 
