@@ -22,15 +22,16 @@ namespace attn {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 // The mask of one sequence.  window > 0, or 0 for none; sinks is 0 without a window.
 struct Mask {
   int off;      // position of query 0
   int len;      // keys and queries at and past this position do not count
   int window, sinks;
-
-  __device__ __forceinline__ bool sees(int p, int j) const {
-    return j <= p && j < len && p < len && (window == 0 || p - j < window || j < sinks);
-  }
 };
 
 __device__ __forceinline__ Mask make_mask(const int* lengths, int b, int Tq, int Tk, int window,
@@ -41,6 +42,56 @@ __device__ __forceinline__ Mask make_mask(const int* lengths, int b, int Tq, int
   m.window = window;
   m.sinks = sinks;
   return m;
+}
+
+// Bits 0 .. h.
+__device__ __forceinline__ uint32_t columns_to(int h) {
+  return h < 0 ? 0u : 0xffffffffu >> (31 - min(h, 31));
+}
+// A query's visible keys as column thresholds of a tile that starts at key j0: column c is
+// visible when c <= hi and (c >= lo or c < sink).  hi < 0 hides everything.
+struct RowCols {
+  int hi, lo, sink;
+  __device__ __forceinline__ bool sees(int c) const {
+    return (c <= hi) & ((c >= lo) | (c < sink));
+  }
+  // columns c0 .. c0 + 31 as bits
+  __device__ __forceinline__ uint32_t bits(int c0) const {
+    return columns_to(hi - c0) & (~columns_to(lo - 1 - c0) | columns_to(sink - 1 - c0));
+  }
+};
+// The elements of x, a row's columns, that are not visible become `hidden`: a test of one bit and
+// a select each.  (Three comparisons an element made masked tiles two to four times as long.)
+template <int N>
+__device__ __forceinline__ void hide(float (&x)[N], const RowCols& rc, float hidden) {
+#pragma unroll
+  for (int q = 0; q < N / 32; ++q) {
+    const uint32_t see = rc.bits(32 * q);
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      if (!(see & (1u << e))) x[32 * q + e] = hidden;
+  }
+}
+__device__ __forceinline__ RowCols row_cols(const Mask& m, int p, int j0) {
+  RowCols r;
+  r.hi = p < m.len ? p - j0 : -1;      // p < len covers j < len as well
+  r.lo = m.window ? p - m.window + 1 - j0 : -0x40000000;
+  r.sink = m.sinks - j0;
+  return r;
+}
+// The other way round: the queries that see key j, as thresholds of columns that start at
+// position p0.
+__device__ __forceinline__ RowCols col_rows(const Mask& m, int j, int p0) {
+  RowCols r;
+  r.lo = j - p0;
+  r.hi = m.len - 1 - p0;
+  if (m.window && j >= m.sinks) r.hi = min(r.hi, j - p0 + m.window - 1);
+  r.sink = 0;
+  return r;
+}
+// Whether the queries p0 .. p1 all see all of the keys j0 .. j1.
+__device__ __forceinline__ bool all_visible(const Mask& m, int p0, int p1, int j0, int j1) {
+  return j1 <= p0 && p1 < m.len && (m.window == 0 || p1 - j0 < m.window || j1 < m.sinks);
 }
 
 // Key tiles of BN keys that the queries i0 .. i1 see: tiles 0 .. nsink-1 hold sinks that lie

@@ -11,22 +11,22 @@
 namespace gdr {
 namespace attn {
 
-// Tiles [0, nfirst) are cut into up to pfirst parts, the others into up to prest, so that a part
-// has about `cap` steps.
+// Tiles [0, nfirst), those with sinks, are cut into up to pfirst parts of up to `cfirst` steps, the
+// others into up to prest of up to `crest`.
 struct Parts {
-  int nfirst, pfirst, prest, cap, ntiles;
+  int nfirst, pfirst, prest, cfirst, crest, ntiles;
   __host__ __device__ int items() const { return nfirst * pfirst + (ntiles - nfirst) * prest; }
-  __host__ __device__ void locate(int item, int& tile, int& part, int& most) const {
+  __device__ void locate(int item, int& tile, int& part) const {
     if (item < nfirst * pfirst) {
-      tile = item / pfirst, part = item % pfirst, most = pfirst;
+      tile = item / pfirst, part = item % pfirst;
     } else {
       const int r = item - nfirst * pfirst;
-      tile = nfirst + r / prest, part = r % prest, most = prest;
+      tile = nfirst + r / prest, part = r % prest;
     }
   }
-  __host__ __device__ int used(int steps, int most) const {
-    const int p = (steps + cap - 1) / cap;
-    return p < 1 ? 1 : p > most ? most : p;
+  __device__ int used(int steps, int tile) const {
+    const int cap = tile < nfirst ? cfirst : crest, most = tile < nfirst ? pfirst : prest;
+    return max(1, min(most, (steps + cap - 1) / cap));
   }
   bool cut() const { return pfirst > 1 || prest > 1; }
 };
@@ -63,7 +63,7 @@ attn_dkv_join(const AttnGradArgs a, const Parts parts) {
   int lo, nt;
   tile_steps<A, S>(m, j0, f.Tk, f.Tq, lo, nt);
   const bool head = tile < parts.nfirst;
-  const int used = parts.used(f.Hq / f.Hkv * nt, head ? parts.pfirst : parts.prest);
+  const int used = parts.used(f.Hq / f.Hkv * nt, tile);
   if (used == 1) return;
   const int item = head ? tile * parts.pfirst
                         : parts.nfirst * parts.pfirst + (tile - parts.nfirst) * parts.prest;
@@ -114,7 +114,8 @@ long host_steps(const AttnArgs& f, int tile) {
 // number of steps that each gets: dq runs beside or after the last ones, and parts cost a pass of
 // fp32 sums through memory.  Measured with 128-key tiles (32 heads, 8 key heads, d = 128): 256
 // tokens 22 us against 31 uncut, 1024 tokens 69 and 107; factors of 1.25 and 2.5 were up to 25 %
-// slower with windows of 512 and 1024.
+// slower with windows of 512 and 1024.  Parts of tiles with sinks are no longer than the longest
+// other tile.
 template <int A, int S>
 Parts plan_parts(const AttnArgs& f, long ctas) {
   Parts p;
@@ -132,8 +133,9 @@ Parts plan_parts(const AttnArgs& f, long ctas) {
   long cap = total * 3 / (2 * ctas) + 1;
   if (cap < 4) cap = 4;
   if (cap > (1 << 28)) cap = 1 << 28;
-  p.cap = (int)cap;
-  p.pfirst = (int)((mfirst + cap - 1) / cap);
+  p.crest = (int)cap;
+  p.cfirst = (int)(mrest >= 4 && mrest < cap ? mrest : cap);
+  p.pfirst = (int)((mfirst + p.cfirst - 1) / p.cfirst);
   p.prest = (int)((mrest + cap - 1) / cap);
   if (p.pfirst < 1) p.pfirst = 1;
   if (p.prest < 1) p.prest = 1;

@@ -201,23 +201,24 @@ attn_forward_simt(const AttnArgs a) {
     group_sync(grp);
     float g[4][4];
     tile_dot<D>(sm.q, st.k, ty, tx, g);
+    const bool whole = all_visible(m, m.off + i0, m.off + i0 + kA - 1, j0, j0 + kB - 1);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int pos = m.off + i0 + 4 * ty + r;
       float top = -INFINITY;
+      const RowCols rc = row_cols(m, m.off + i0 + 4 * ty + r, j0);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        g[r][e] = m.sees(pos, j0 + tx + 16 * e) ? g[r][e] * c : -INFINITY;
+        g[r][e] = whole | rc.sees(tx + 16 * e) ? g[r][e] * c : -INFINITY;
         top = fmaxf(top, g[r][e]);
       }
       const float now = fmaxf(mx[r], row_max(top));
       const float base = now == -INFINITY ? 0.f : now;
-      const float f = exp2f(mx[r] - base);
+      const float f = ex2(mx[r] - base);
       mx[r] = now;
       float part = 0.f;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float w = exp2f(g[r][e] - base);
+        const float w = ex2(g[r][e] - base);
         st.p[(4 * ty + r) * kLd + tx + 16 * e] = w;
         part += w;
       }
@@ -249,7 +250,7 @@ attn_forward_simt(const AttnArgs a) {
     const int i = i0 + 4 * ty + r;
     const float m2 = sm.mx[4 * ty + r], now = fmaxf(mx[r], m2);
     const float base = now == -INFINITY ? 0.f : now;
-    const float f1 = exp2f(mx[r] - base), f2 = exp2f(m2 - base);
+    const float f1 = ex2(mx[r] - base), f2 = ex2(m2 - base);
     mx[r] = now;
     sum[r] = fmaf(sum[r], f1, sm.sum[4 * ty + r] * f2);
 #pragma unroll
@@ -334,15 +335,18 @@ attn_dq_simt(const AttnGradArgs a) {
     float g[4][4], dp[4][4];
     tile_dot<D>(sm.q, st.k, ty, tx, g);
     tile_dot<D>(sm.d, st.v, ty, tx, dp);
+    const bool whole = all_visible(m, m.off + i0, m.off + i0 + kA - 1, j0, j0 + kB - 1);
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
+    for (int r = 0; r < 4; ++r) {
+      const RowCols rc = row_cols(m, m.off + i0 + 4 * ty + r, j0);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int j = tx + 16 * e;
-        const float w = exp2f((g[r][e] * f.scale - lse[r]) * kLog2e);
-        st.s[(4 * ty + r) * kLd + j] = m.sees(m.off + i0 + 4 * ty + r, j0 + j)
-                                           ? f.scale * w * (dp[r][e] - delta[r]) : 0.f;
+        const float w = ex2((g[r][e] * f.scale - lse[r]) * kLog2e);
+        st.s[(4 * ty + r) * kLd + j] =
+            whole | rc.sees(j) ? f.scale * w * (dp[r][e] - delta[r]) : 0.f;
       }
+    }
     __syncwarp();
     tile_acc<D>(st.s, st.k, ty, tx, acc);
   }
@@ -369,15 +373,15 @@ attn_dkv_simt(const AttnGradArgs a, const Parts parts) {
   // the first keys, which the most queries see without a window, start first
   const int bh = blockIdx.x % (f.B * f.Hkv), hk = bh % f.Hkv, b = bh / f.Hkv;
   const int item = blockIdx.x / (unsigned)(f.B * f.Hkv);
-  int tile, part, most;
-  parts.locate(item, tile, part, most);
+  int tile, part;
+  parts.locate(item, tile, part);
   const int j0 = tile * kA;
   const int G = f.Hq / f.Hkv;
   const int grp = threadIdx.x / kGroup, tid = threadIdx.x % kGroup, ty = tid >> 4, tx = tid & 15;
   const Mask m = make_mask(f.lengths, b, f.Tq, f.Tk, f.window, f.sinks);
   int first, nt;
   tile_steps<kA, kB>(m, j0, f.Tk, f.Tq, first, nt);
-  const int used = parts.used(G * nt, most);
+  const int used = parts.used(G * nt, tile);
   if (part >= used) return;
   const int per = (G * nt + used - 1) / used, x1 = min(G * nt, (part + 1) * per);
   const size_t qs = (size_t)f.Hq * D, ks = (size_t)f.Hkv * D;
@@ -403,16 +407,20 @@ attn_dkv_simt(const AttnGradArgs a, const Parts parts) {
     float g[4][4], dp[4][4];
     tile_dot<D>(sm.k, st.q, ty, tx, g);
     tile_dot<D>(sm.v, st.d, ty, tx, dp);
+    const int p0 = m.off + i0;
+    const bool whole = all_visible(m, p0, p0 + kB - 1, j0, j0 + kA - 1);
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
+    for (int r = 0; r < 4; ++r) {
+      const RowCols rc = col_rows(m, j0 + 4 * ty + r, p0);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int i = tx + 16 * e, at = (4 * ty + r) * kLd + i;
-        const bool sees = m.sees(m.off + i0 + i, j0 + 4 * ty + r);
-        const float w = sees ? exp2f((g[r][e] * f.scale - st.lse[i]) * kLog2e) : 0.f;
+        const bool sees = whole | rc.sees(i);
+        const float w = sees ? ex2((g[r][e] * f.scale - st.lse[i]) * kLog2e) : 0.f;
         st.p[at] = w;
         st.s[at] = sees ? f.scale * w * (dp[r][e] - st.delta[i]) : 0.f;
       }
+    }
     __syncwarp();
     tile_acc<D>(st.p, st.d, ty, tx, dv);
     tile_acc<D>(st.s, st.q, ty, tx, dk);

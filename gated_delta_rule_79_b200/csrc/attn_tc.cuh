@@ -39,11 +39,6 @@ __host__ __device__ constexpr uint32_t idesc_bf16_mn(int M, int N) {   // B is M
   return idesc_bf16(M, N) | (1u << 16);
 }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float y;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
@@ -75,43 +70,6 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
 __device__ __forceinline__ float pack2(float lo, float hi) {
   __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<float*>(&p);
-}
-
-// Bits 0 .. h.
-__device__ __forceinline__ uint32_t columns_to(int h) {
-  return h < 0 ? 0u : 0xffffffffu >> (31 - min(h, 31));
-}
-// A query's visible keys as column thresholds of a tile that starts at key j0: column c is
-// visible when c <= hi and (c >= lo or c < sink).  hi < 0 hides everything.
-struct RowCols {
-  int hi, lo, sink;
-  // columns c0 .. c0 + 31 as bits
-  __device__ __forceinline__ uint32_t bits(int c0) const {
-    return columns_to(hi - c0) & (~columns_to(lo - 1 - c0) | columns_to(sink - 1 - c0));
-  }
-};
-// The elements of x, a row's columns, that are not visible become `hidden`: a test of one bit and
-// a select each.  (Three comparisons an element made masked tiles two to four times as long.)
-template <int N>
-__device__ __forceinline__ void hide(float (&x)[N], const RowCols& rc, float hidden) {
-#pragma unroll
-  for (int q = 0; q < N / 32; ++q) {
-    const uint32_t see = rc.bits(32 * q);
-#pragma unroll
-    for (int e = 0; e < 32; ++e)
-      if (!(see & (1u << e))) x[32 * q + e] = hidden;
-  }
-}
-__device__ __forceinline__ RowCols row_cols(const Mask& m, int p, int j0) {
-  RowCols r;
-  r.hi = p < m.len ? p - j0 : -1;      // p < len covers j < len as well
-  r.lo = m.window ? p - m.window + 1 - j0 : -0x40000000;
-  r.sink = m.sinks - j0;
-  return r;
-}
-// Whether the queries p0 .. p1 all see all of the keys j0 .. j1.
-__device__ __forceinline__ bool all_visible(const Mask& m, int p0, int p1, int j0, int j1) {
-  return j1 <= p0 && p1 < m.len && (m.window == 0 || p1 - j0 < m.window || j1 < m.sinks);
 }
 
 // Bounded waits of one CTA, made by whole warps: every lane gets the same answer.  The first

@@ -365,13 +365,13 @@ attn_dkv_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
   // the first key tiles, which the most queries see, start first
   const int bh = blockIdx.x % (f.B * f.Hkv), item = blockIdx.x / (f.B * f.Hkv);
   const int b = bh / f.Hkv, hk = bh % f.Hkv, G = f.Hq / f.Hkv;
-  int tile, part, most;
-  parts.locate(item, tile, part, most);
+  int tile, part;
+  parts.locate(item, tile, part);
   const int j0 = tile * kA;
   const Mask m = make_mask(f.lengths, b, f.Tq, f.Tk, f.window, f.sinks);
   int lo64, nt;
   tile_steps<kA, kS>(m, j0, f.Tk, f.Tq, lo64, nt);
-  const int used = parts.used(G * nt, most);
+  const int used = parts.used(G * nt, tile);
   let_next_start();
   if (part >= used) return;
   const int per = (G * nt + used - 1) / used;
@@ -415,10 +415,7 @@ attn_dkv_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
       const bool whole = all_visible(m, p0, p0 + kS - 1, j0, j0 + kA - 1);
       RowCols rc;
       if (!whole) {
-        rc.lo = j - p0;
-        rc.hi = m.len - 1 - p0;
-        if (m.window && j >= m.sinks) rc.hi = min(rc.hi, j - p0 + m.window - 1);
-        rc.sink = 0;
+        rc = col_rows(m, j, p0);
         hide(s, rc, 0.f);
       }
       put_weights<FINE>(tS, s);
