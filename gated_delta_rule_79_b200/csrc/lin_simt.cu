@@ -5,7 +5,10 @@
 // Chunks of 32 tokens.  A thread of the 16 x 16 grid keeps (d_v / 16) x (d_k / 16) elements
 // of the state in registers; the outputs' kernel mirrors the state in shared memory for S q.
 // Bound: fp32 multiply-adds, 2 (2 d_k d_v + 16 (d_k + d_v)) flops a token, with the reads of the
-// operands from shared memory close behind: four neighbours to a read.
+// operands from shared memory close behind: four neighbours to a read, the threads of a warp as
+// 4 x 8 where a product reads both operands there.  A CTA of d = 128 has an SM to itself, so its
+// loads do not hide behind another's work: they run a chunk ahead.  2 x 2048 tokens, 8 heads of
+// 128 x 128, fp32: 164 us; 216 with loads that the chunk waits for, 232 with 2 x 16 threads.
 
 #include "lin_common.cuh"
 #include "once.h"
@@ -26,6 +29,11 @@ struct Share {
   static __device__ __forceinline__ int col(int tx, int j) {
     return tx * W + 16 * W * (j / W) + j % W;
   }
+  // the W neighbours from column col(tx, j) on
+  static __device__ __forceinline__ void put(float* p, const float* x) {
+    if constexpr (W == 4) *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+    else *reinterpret_cast<float2*>(p) = make_float2(x[0], x[1]);
+  }
   static __device__ __forceinline__ void cols(const float* r, int tx, float (&x)[N]) {
 #pragma unroll
     for (int j = 0; j < N; j += W) read(r + col(tx, j), &x[j]);
@@ -43,6 +51,29 @@ struct Share {
     } else {
       const float2 f = *reinterpret_cast<const float2*>(p);
       x[0] = f.x, x[1] = f.y;
+    }
+  }
+};
+
+// A chunk's rows of one operand on their way from global to shared memory, in registers while
+// the chunk before it is worked on.  Rows from `end` on are zero.
+template <typename T, int D>
+struct Ahead {
+  static constexpr int N = kC * (D / 4) / kThreads;
+  float4 x[N];
+  __device__ __forceinline__ void load(const T* src, size_t stride, int r0, int end, int tid) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int e = tid + i * kThreads, r = r0 + e / (D / 4), c = e % (D / 4) * 4;
+      x[i] = r < end ? Elem<T>::load4(src + (size_t)r * stride + c)
+                     : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  }
+  __device__ __forceinline__ void put(float* dst, int tid) const {       // rows of D + 4
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int e = tid + i * kThreads;
+      *reinterpret_cast<float4*>(dst + e / (D / 4) * (D + 4) + e % (D / 4) * 4) = x[i];
     }
   }
 };
@@ -78,23 +109,19 @@ lin_segment_simt(const LinScan sc) {
   float acc[DV / 16][DK / 16] = {};
   const T* kb = (const T*)jb.k + (((size_t)b * sc.T + sg.a) * sc.H + h) * DK;
   const T* vb = (const T*)jb.v + (((size_t)b * sc.T + sg.a) * sc.H + h) * DV;
+  Ahead<T, DK> ka;
+  Ahead<T, DV> va;
+  ka.load(kb, (size_t)sc.H * DK, 0, sg.n, tid);
+  va.load(vb, (size_t)sc.H * DV, 0, sg.n, tid);
   for (int x0 = 0; x0 < sg.n; x0 += kC) {
     const int L = min(kC, sg.n - x0);
     const float far = (float)decay_pow(l2, jb.rev ? x0 : sg.n - x0 - L);
     __syncthreads();
-    for (int e = tid; e < kC * (DK / 4); e += kThreads) {
-      const int r = e / (DK / 4), c = (e % (DK / 4)) * 4;
-      float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (x0 + r < sg.n) f = Elem<T>::load4(kb + (size_t)(x0 + r) * sc.H * DK + c);
-      *reinterpret_cast<float4*>(&ks[r][c]) = f;
-    }
-    for (int e = tid; e < kC * (DV / 4); e += kThreads) {
-      const int r = e / (DV / 4), c = (e % (DV / 4)) * 4;
-      float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (x0 + r < sg.n) f = Elem<T>::load4(vb + (size_t)(x0 + r) * sc.H * DV + c);
-      *reinterpret_cast<float4*>(&vs[r][c]) = f;
-    }
+    ka.put(ks[0], tid);
+    va.put(vs[0], tid);
     __syncthreads();
+    ka.load(kb, (size_t)sc.H * DK, x0 + kC, sg.n, tid);
+    va.load(vb, (size_t)sc.H * DV, x0 + kC, sg.n, tid);
 #pragma unroll 4
     for (int r = 0; r < kC; ++r)
       add_token<DK, DV>(acc, ks[r], vs[r], near[jb.rev ? r : max(L - 1 - r, 0)] * far, ty, tx);
@@ -103,15 +130,15 @@ lin_segment_simt(const LinScan sc) {
 #pragma unroll
   for (int i = 0; i < DV / 16; ++i)
 #pragma unroll
-    for (int j = 0; j < DK / 16; ++j)
-      dst[(ty * (DV / 16) + i) * DK + Share<DK>::col(tx, j)] = acc[i][j];
+    for (int j = 0; j < DK / 16; j += Share<DK>::W)
+      Share<DK>::put(dst + (ty * (DV / 16) + i) * DK + Share<DK>::col(tx, j), &acc[i][j]);
 }
 
 template <int DK, int DV>
 struct OutSmem {
-  float st[DK][DV + 4];          // the state entering the chunk, transposed
+  float st[DV][DK + 4];          // the state entering the chunk
   float q[kC][DK + 4], k[kC][DK + 4], v[kC][DV + 4];
-  float p[kC][kC + 1];
+  float p[kC][kC + 4];
   float pw[kC + 1];              // a^n, n = 0 .. 32
 };
 
@@ -120,7 +147,6 @@ __global__ void __launch_bounds__(kThreads)
 lin_out_simt(const LinScan sc) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   OutSmem<DK, DV>& sm = *reinterpret_cast<OutSmem<DK, DV>*>(smem_raw);
-  constexpr int VPT = DV / 16;
   const LinJob& jb = sc.job[blockIdx.y];
   const int p = blockIdx.x % sc.nseg, bh = blockIdx.x / sc.nseg;
   const int b = bh / sc.H, h = bh % sc.H;
@@ -153,33 +179,31 @@ lin_out_simt(const LinScan sc) {
   const T* vb = (const T*)jb.v + row0 * DV;
   T* ob = (T*)jb.o + row0 * DV;
   const int nch = (sg.n + kC - 1) / kC;
+  Ahead<T, DK> qa, ka;
+  Ahead<T, DV> va;
+  auto ahead = [&](int ci) {
+    if (ci >= nch) return;             // (the chunk behind the last would start below row 0)
+    const int x = (jb.rev ? nch - 1 - ci : ci) * kC;
+    qa.load(qb, (size_t)sc.H * DK, x, sg.n, tid);
+    ka.load(kb, (size_t)sc.H * DK, x, sg.n, tid);
+    va.load(vb, (size_t)sc.H * DV, x, sg.n, tid);
+  };
+  ahead(0);
   for (int ci = 0; ci < nch; ++ci) {
     const int x0 = (jb.rev ? nch - 1 - ci : ci) * kC;
     const int L = min(kC, sg.n - x0);
     const int E = (p == 0 && ci == 0) ? jb.e0 : 1;
     __syncthreads();
-    for (int e = tid; e < kC * (DK / 4); e += kThreads) {
-      const int r = e / (DK / 4), c = (e % (DK / 4)) * 4;
-      float4 fq = make_float4(0.f, 0.f, 0.f, 0.f), fk = fq;
-      if (r < L) {
-        fq = Elem<T>::load4(qb + (size_t)(x0 + r) * sc.H * DK + c);
-        fk = Elem<T>::load4(kb + (size_t)(x0 + r) * sc.H * DK + c);
-      }
-      *reinterpret_cast<float4*>(&sm.q[r][c]) = fq;
-      *reinterpret_cast<float4*>(&sm.k[r][c]) = fk;
-    }
-    for (int e = tid; e < kC * (DV / 4); e += kThreads) {
-      const int r = e / (DV / 4), c = (e % (DV / 4)) * 4;
-      float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (r < L) f = Elem<T>::load4(vb + (size_t)(x0 + r) * sc.H * DV + c);
-      *reinterpret_cast<float4*>(&sm.v[r][c]) = f;
-    }
+    qa.put(sm.q[0], tid);
+    ka.put(sm.k[0], tid);
+    va.put(sm.v[0], tid);
 #pragma unroll
     for (int i = 0; i < DV / 16; ++i)
 #pragma unroll
-      for (int j = 0; j < DK / 16; ++j)
-        sm.st[Share<DK>::col(tx, j)][ty * (DV / 16) + i] = S[i][j];
+      for (int j = 0; j < DK / 16; j += Share<DK>::W)
+        Share<DK>::put(&sm.st[ty * (DV / 16) + i][Share<DK>::col(tx, j)], &S[i][j]);
     __syncthreads();
+    ahead(ci + 1);
     {
       const int t = tid >> 3, j0 = tid & 7;
       float g[4] = {};
@@ -200,49 +224,54 @@ lin_out_simt(const LinScan sc) {
     }
     __syncthreads();
     {
-      float o[2][VPT] = {};
-      const int t0 = 2 * ty;
+      // four rows and DV / 32 columns a thread: rows lr + 4 a of a warp's 16, columns lc + 8 b
+      // of its DV / 4, so that a read serves a warp from one line of banks
+      constexpr int NB = DV / 32;
+      const int warp = tid >> 5, lr = (tid >> 3) & 3, lc = tid & 7;
+      const int t0 = 16 * (warp & 1) + lr, c0 = (warp >> 1) * (DV / 4) + lc;
+      float o[4][NB] = {};
 #pragma unroll 4
       for (int c = 0; c < DK; c += 4) {
-        const float4 qa = *reinterpret_cast<const float4*>(&sm.q[t0][c]);
-        const float4 qc = *reinterpret_cast<const float4*>(&sm.q[t0 + 1][c]);
-        const float ua[4] = {qa.x, qa.y, qa.z, qa.w}, uc[4] = {qc.x, qc.y, qc.z, qc.w};
+        float4 u[4], w[NB];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float x[VPT];
-          Share<DV>::cols(sm.st[c + i], tx, x);
+        for (int x = 0; x < 4; ++x) u[x] = *reinterpret_cast<const float4*>(&sm.q[t0 + 4 * x][c]);
 #pragma unroll
-          for (int e = 0; e < VPT; ++e) {
-            o[0][e] = fmaf(ua[i], x[e], o[0][e]);
-            o[1][e] = fmaf(uc[i], x[e], o[1][e]);
+        for (int x = 0; x < NB; ++x) w[x] = *reinterpret_cast<const float4*>(&sm.st[c0 + 8 * x][c]);
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+          for (int y = 0; y < NB; ++y)
+            o[x][y] = fmaf(u[x].x, w[y].x,
+                           fmaf(u[x].y, w[y].y, fmaf(u[x].z, w[y].z, fmaf(u[x].w, w[y].w, o[x][y]))));
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int t = t0 + 4 * x, i = jb.rev ? L - 1 - t : t;
+        const float f = t < L ? sm.pw[i + E] : 0.f;
+#pragma unroll
+        for (int y = 0; y < NB; ++y) o[x][y] *= f;
+      }
+#pragma unroll 2
+      for (int j = 0; j < kC; j += 4) {          // rows past L are zero
+        float pp[4][4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          *reinterpret_cast<float4*>(pp[x]) = *reinterpret_cast<const float4*>(&sm.p[t0 + 4 * x][j]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int y = 0; y < NB; ++y) {
+            const float v = sm.v[j + e][c0 + 8 * y];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) o[x][y] = fmaf(pp[x][e], v, o[x][y]);
           }
-        }
       }
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int i = jb.rev ? L - 1 - (t0 + u) : t0 + u;
-        const float f = t0 + u < L ? sm.pw[i + E] : 0.f;
+      for (int x = 0; x < 4; ++x)
+        if (t0 + 4 * x < L) {
+          T* dst = ob + (size_t)(x0 + t0 + 4 * x) * sc.H * DV + c0;
 #pragma unroll
-        for (int e = 0; e < VPT; ++e) o[u][e] *= f;
-      }
-#pragma unroll 4
-      for (int j = 0; j < kC; ++j) {          // rows past L are zero
-        const float pa = sm.p[t0][j], pc = sm.p[t0 + 1][j];
-        float x[VPT];
-        Share<DV>::cols(sm.v[j], tx, x);
-#pragma unroll
-        for (int e = 0; e < VPT; ++e) {
-          o[0][e] = fmaf(pa, x[e], o[0][e]);
-          o[1][e] = fmaf(pc, x[e], o[1][e]);
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-        if (t0 + u < L) {
-          T* dst = ob + (size_t)(x0 + t0 + u) * sc.H * DV;
-#pragma unroll
-          for (int e = 0; e < VPT; ++e)
-            Elem<T>::store(dst + Share<DV>::col(tx, e), o[u][e]);
+          for (int y = 0; y < NB; ++y) Elem<T>::store(dst + 8 * y, o[x][y]);
         }
     }
     // the chunk's decay as a pair of floats: its rounding would otherwise be the same in
