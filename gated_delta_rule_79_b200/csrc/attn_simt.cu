@@ -46,14 +46,15 @@ __device__ __forceinline__ void load_tile(float* dst, const T* x, size_t row_str
   }
 }
 
-// g[a][b] = sum_c x[4 ty + a][c] y[tx + 16 b][c]
+// g[a][b] = sum_c x[4 ty + a][c] y[tx + 16 b][c], even and odd channels apart until the end
 template <int D>
 __device__ __forceinline__ void tile_dot(const float* x, const float* y, int ty, int tx,
                                          float (&g)[4][4]) {
+  float2 s[4][4];
 #pragma unroll
   for (int a = 0; a < 4; ++a)
 #pragma unroll
-    for (int b = 0; b < 4; ++b) g[a][b] = 0.f;
+    for (int b = 0; b < 4; ++b) s[a][b] = make_float2(0.f, 0.f);
 #pragma unroll 4
   for (int c = 0; c < D; c += 4) {
     float4 u[4], w[4];
@@ -65,10 +66,15 @@ __device__ __forceinline__ void tile_dot(const float* x, const float* y, int ty,
 #pragma unroll
     for (int a = 0; a < 4; ++a)
 #pragma unroll
-      for (int b = 0; b < 4; ++b)
-        g[a][b] = fmaf(u[a].x, w[b].x,
-                       fmaf(u[a].y, w[b].y, fmaf(u[a].z, w[b].z, fmaf(u[a].w, w[b].w, g[a][b]))));
+      for (int b = 0; b < 4; ++b) {
+        s[a][b] = fma2(make_float2(u[a].x, u[a].y), make_float2(w[b].x, w[b].y), s[a][b]);
+        s[a][b] = fma2(make_float2(u[a].z, u[a].w), make_float2(w[b].z, w[b].w), s[a][b]);
+      }
   }
+#pragma unroll
+  for (int a = 0; a < 4; ++a)
+#pragma unroll
+    for (int b = 0; b < 4; ++b) g[a][b] = s[a][b].x + s[a][b].y;
 }
 
 // The columns of thread tx: tx W + 16 W g + e, e < W, g < G; W consecutive ones per read.

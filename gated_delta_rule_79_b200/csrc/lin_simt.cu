@@ -7,9 +7,12 @@
 // Bound: fp32 multiply-adds, 2 (2 d_k d_v + 16 (d_k + d_v)) flops a token, with the reads of the
 // operands from shared memory close behind: four neighbours to a read, the threads of a warp as
 // 4 x 8 where a product reads both operands there.  A CTA of d = 128 has an SM to itself, so its
-// loads do not hide behind another's work: they run a chunk ahead.  2 x 2048 tokens, 8 heads of
-// 128 x 128, fp32: 164 us; 216 with loads that the chunk waits for, 232 with 2 x 16 threads.
+// loads do not hide behind another's work: they run a chunk ahead.  Multiply-adds go two to
+// an instruction, over neighbouring columns or over even and odd channels.  2 x 2048 tokens, 8
+// heads of 128 x 128, fp32: 154 us; one multiply-add an instruction 167, with loads that the chunk
+// waits for 216, with 2 x 16 threads 232 as well (6 heads of 64 x 128, gradients: 144 and 152).
 
+#include "attn_common.cuh"
 #include "lin_common.cuh"
 #include "once.h"
 
@@ -17,6 +20,8 @@ namespace gdr {
 namespace {
 
 using namespace lin;
+using attn::fma2;
+using attn::mul2;
 
 constexpr int kC = 32;
 constexpr int kThreads = 256;
@@ -78,19 +83,21 @@ struct Ahead {
   }
 };
 
-// S[i][j] += w sum over one token's v_i k_j
+// S[i][j] += w v_i k_j for one token; S holds pairs of neighbouring columns
 template <int DK, int DV>
-__device__ __forceinline__ void add_token(float (&S)[DV / 16][DK / 16], const float* k,
+__device__ __forceinline__ void add_token(float2 (&S)[DV / 16][DK / 32], const float* k,
                                           const float* v, float w, int ty, int tx) {
   float kk[DK / 16], vv[DV / 16];
   Share<DK>::cols(k, tx, kk);
   Share<DV>::rows(v, ty, vv);
+  float2 k2[DK / 32];
 #pragma unroll
-  for (int j = 0; j < DK / 16; ++j) kk[j] *= w;
+  for (int j = 0; j < DK / 32; ++j)
+    k2[j] = mul2(make_float2(kk[2 * j], kk[2 * j + 1]), make_float2(w, w));
 #pragma unroll
   for (int i = 0; i < DV / 16; ++i)
 #pragma unroll
-    for (int j = 0; j < DK / 16; ++j) S[i][j] = fmaf(vv[i], kk[j], S[i][j]);
+    for (int j = 0; j < DK / 32; ++j) S[i][j] = fma2(make_float2(vv[i], vv[i]), k2[j], S[i][j]);
 }
 
 // The sum over the segment's tokens of a^(n-1-i) v_i k_i^T.
@@ -106,7 +113,7 @@ lin_segment_simt(const LinScan sc) {
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
   let_next_start();
   if (tid < kC) near[tid] = (float)decay_pow(l2, tid);
-  float acc[DV / 16][DK / 16] = {};
+  float2 acc[DV / 16][DK / 32] = {};
   const T* kb = (const T*)jb.k + (((size_t)b * sc.T + sg.a) * sc.H + h) * DK;
   const T* vb = (const T*)jb.v + (((size_t)b * sc.T + sg.a) * sc.H + h) * DV;
   Ahead<T, DK> ka;
@@ -131,7 +138,7 @@ lin_segment_simt(const LinScan sc) {
   for (int i = 0; i < DV / 16; ++i)
 #pragma unroll
     for (int j = 0; j < DK / 16; j += Share<DK>::W)
-      Share<DK>::put(dst + (ty * (DV / 16) + i) * DK + Share<DK>::col(tx, j), &acc[i][j]);
+      Share<DK>::put(dst + (ty * (DV / 16) + i) * DK + Share<DK>::col(tx, j), &acc[i][j / 2].x);
 }
 
 template <int DK, int DV>
@@ -158,7 +165,7 @@ lin_out_simt(const LinScan sc) {
   // state entering the segment: what lin_carry.cu left for it, or the call's own if it is the
   // only one
   wait_for_previous();
-  float S[DV / 16][DK / 16] = {};
+  float2 S[DV / 16][DK / 32] = {};
   const bool parts = sc.nseg > 1;
   if (parts || jb.s_in) {
     const float* s =
@@ -167,9 +174,11 @@ lin_out_simt(const LinScan sc) {
 #pragma unroll
     for (int i = 0; i < DV / 16; ++i)
 #pragma unroll
-      for (int j = 0; j < DK / 16; ++j) {
-        const int r = ty * (DV / 16) + i, c = Share<DK>::col(tx, j);
-        S[i][j] = s[!parts && jb.s_trans ? c * DV + r : r * DK + c];
+      for (int j = 0; j < DK / 32; ++j) {
+        const int r = ty * (DV / 16) + i, c = Share<DK>::col(tx, 2 * j);
+        const bool turned = !parts && jb.s_trans;
+        S[i][j] = make_float2(s[turned ? c * DV + r : r * DK + c],
+                              s[turned ? (c + 1) * DV + r : r * DK + c + 1]);
       }
   }
 
@@ -201,25 +210,26 @@ lin_out_simt(const LinScan sc) {
     for (int i = 0; i < DV / 16; ++i)
 #pragma unroll
       for (int j = 0; j < DK / 16; j += Share<DK>::W)
-        Share<DK>::put(&sm.st[ty * (DV / 16) + i][Share<DK>::col(tx, j)], &S[i][j]);
+        Share<DK>::put(&sm.st[ty * (DV / 16) + i][Share<DK>::col(tx, j)], &S[i][j / 2].x);
     __syncthreads();
     ahead(ci + 1);
     {
       const int t = tid >> 3, j0 = tid & 7;
-      float g[4] = {};
+      float2 g[4] = {};          // even and odd channels
 #pragma unroll 4
       for (int c = 0; c < DK; c += 4) {
         const float4 a = *reinterpret_cast<const float4*>(&sm.q[t][c]);
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
           const float4 d = *reinterpret_cast<const float4*>(&sm.k[j0 + 8 * m][c]);
-          g[m] = fmaf(a.x, d.x, fmaf(a.y, d.y, fmaf(a.z, d.z, fmaf(a.w, d.w, g[m]))));
+          g[m] = fma2(make_float2(a.x, a.y), make_float2(d.x, d.y), g[m]);
+          g[m] = fma2(make_float2(a.z, a.w), make_float2(d.z, d.w), g[m]);
         }
       }
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
         const int gap = jb.rev ? j0 + 8 * m - t : t - (j0 + 8 * m);
-        sm.p[t][j0 + 8 * m] = gap >= 0 ? g[m] * sm.pw[gap] : 0.f;
+        sm.p[t][j0 + 8 * m] = gap >= 0 ? (g[m].x + g[m].y) * sm.pw[gap] : 0.f;
       }
     }
     __syncthreads();
@@ -229,7 +239,8 @@ lin_out_simt(const LinScan sc) {
       constexpr int NB = DV / 32;
       const int warp = tid >> 5, lr = (tid >> 3) & 3, lc = tid & 7;
       const int t0 = 16 * (warp & 1) + lr, c0 = (warp >> 1) * (DV / 4) + lc;
-      float o[4][NB] = {};
+      float o[4][NB];
+      float2 o2[4][NB] = {};
 #pragma unroll 4
       for (int c = 0; c < DK; c += 4) {
         float4 u[4], w[NB];
@@ -240,16 +251,17 @@ lin_out_simt(const LinScan sc) {
 #pragma unroll
         for (int x = 0; x < 4; ++x)
 #pragma unroll
-          for (int y = 0; y < NB; ++y)
-            o[x][y] = fmaf(u[x].x, w[y].x,
-                           fmaf(u[x].y, w[y].y, fmaf(u[x].z, w[y].z, fmaf(u[x].w, w[y].w, o[x][y]))));
+          for (int y = 0; y < NB; ++y) {
+            o2[x][y] = fma2(make_float2(u[x].x, u[x].y), make_float2(w[y].x, w[y].y), o2[x][y]);
+            o2[x][y] = fma2(make_float2(u[x].z, u[x].w), make_float2(w[y].z, w[y].w), o2[x][y]);
+          }
       }
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         const int t = t0 + 4 * x, i = jb.rev ? L - 1 - t : t;
         const float f = t < L ? sm.pw[i + E] : 0.f;
 #pragma unroll
-        for (int y = 0; y < NB; ++y) o[x][y] *= f;
+        for (int y = 0; y < NB; ++y) o[x][y] = f * (o2[x][y].x + o2[x][y].y);
       }
 #pragma unroll 2
       for (int j = 0; j < kC; j += 4) {          // rows past L are zero
@@ -281,7 +293,8 @@ lin_out_simt(const LinScan sc) {
 #pragma unroll
     for (int i = 0; i < DV / 16; ++i)
 #pragma unroll
-      for (int j = 0; j < DK / 16; ++j) S[i][j] = fmaf(fh, S[i][j], fl * S[i][j]);
+      for (int j = 0; j < DK / 32; ++j)
+        S[i][j] = fma2(make_float2(fh, fh), S[i][j], mul2(make_float2(fl, fl), S[i][j]));
 #pragma unroll 4
     for (int r = 0; r < kC; ++r)            // rows past L are zero
       add_token<DK, DV>(S, sm.k[r], sm.v[r], sm.pw[jb.rev ? r : max(L - 1 - r, 0)], ty, tx);
@@ -292,8 +305,11 @@ lin_out_simt(const LinScan sc) {
 #pragma unroll
     for (int i = 0; i < DV / 16; ++i)
 #pragma unroll
-      for (int j = 0; j < DK / 16; ++j)
-        s[(ty * (DV / 16) + i) * DK + Share<DK>::col(tx, j)] = f * S[i][j];
+      for (int j = 0; j < DK / 32; ++j) {
+        float* at = s + (ty * (DV / 16) + i) * DK + Share<DK>::col(tx, 2 * j);
+        at[0] = f * S[i][j].x;
+        at[1] = f * S[i][j].y;
+      }
   }
 }
 
