@@ -396,7 +396,7 @@ gdr_status attn_decode(const void* q, const void* k, const void* v, void* k_cach
               (int2*)((unsigned char*)workspace + kStatusBytes),
               (float*)((unsigned char*)workspace + kStatusBytes + first_bytes(N)),
               (unsigned int*)workspace, N, Hq, Hkv, d, npages, page_shift_of(page), max_pages, window, sinks, scale, dtype,
-              0, 0, 0, 0.f, 0, false};
+              0, 0, 0, 0.f, 0, false, false};
   attn_decode_plan(a, cap);
   if ((s = check_workspace(fn, workspace, ws_bytes, decode_need(a))) != GDR_OK) return s;
   return done(fn, launch_attn_decode(a, (cudaStream_t)stream));

@@ -25,6 +25,8 @@
 //
 // The join reads parts in order, so results do not depend on scheduling.
 
+#include <type_traits>
+
 #include "attn_common.cuh"
 #include "once.h"
 
@@ -74,7 +76,9 @@ struct Part {
   int n, part, parts, tokens, slot;
 };
 // The part in place `slot`.  Each warp finds it by itself (no barrier): its lanes count the parts
-// of a run of sequences each.
+// of a run of sequences each.  (TIGHT: with the search; its code alone cost the launches that do not
+// search 1 %.)
+template <bool TIGHT>
 __device__ __forceinline__ Part find_part(const PagedArgs& a, int slot) {
   if (a.nparts == 0) return Part{slot, 0, 1, 0x7fffffff, 0};
   auto cut = [&](int n, int at, int parts, int count) {
@@ -100,11 +104,25 @@ __device__ __forceinline__ Part find_part(const PagedArgs& a, int slot) {
 #pragma unroll
   for (int f = 16; f; f >>= 1) all += __shfl_xor_sync(0xffffffffu, all, f);
   // no less than all / places (the factor is rounded up), the same in every CTA
-  const unsigned per =
+  unsigned per =
       max((unsigned)a.least, (unsigned)fminf(__ll2float_ru(all) * a.per_place, 0x1p30f) + 1u);
   auto parts_of = [&](int n) {
     return (int)min((unsigned)kMaxSplit, max(1u, (count(n) + per - 1) / per));
   };
+  if (TIGHT && a.tight) {
+    // that leaves every sequence a place for a last part, however short; half of them on average
+    // stay empty, so halve what lies between it and an even share of all places
+    unsigned lo = max((unsigned)a.least, (unsigned)(all / a.nparts));
+    unsigned fits = per;
+    for (int i = 0; i < 6 && lo < fits; ++i) {
+      per = (lo + fits) / 2;
+      unsigned sum = 0;
+      for (int n = n0; n < n1; ++n) sum += parts_of(n);
+      if (__reduce_add_sync(0xffffffffu, sum) <= (unsigned)a.nparts) fits = per;
+      else lo = per + 1;
+    }
+    per = fits;
+  }
   const int parts0 = n0 < n1 ? parts_of(n0) : 0;
   int mine = parts0;
   for (int n = n0 + 1; n < n1; ++n) mine += parts_of(n);
@@ -223,7 +241,7 @@ struct TcSmem {
   static_assert(W * 16 * (D + 4) * 4 + W * 16 * 8 <= RING, "join area");
 };
 
-template <int D, int W>
+template <int D, int W, bool TIGHT>
 __global__ void __launch_bounds__(W * 32)
 attn_decode_tc(const PagedArgs a) {
   using S = TcSmem<D, W>;
@@ -236,7 +254,7 @@ attn_decode_tc(const PagedArgs a) {
   const int hb = x % nhb;
   x /= nhb;
   const int hk = x % a.Hkv;
-  const Part pt = find_part(a, x / a.Hkv);
+  const Part pt = find_part<TIGHT>(a, x / a.Hkv);
   if (pt.slot < 0) return;
   const int n = pt.n, part = pt.part, parts = pt.parts;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -441,7 +459,7 @@ attn_decode_simt(const PagedArgs a) {
   const int hb = x % nhb;
   x /= nhb;
   const int hk = x % a.Hkv;
-  const Part pt = find_part(a, x / a.Hkv);
+  const Part pt = find_part<true>(a, x / a.Hkv);
   if (pt.slot < 0) return;
   const int n = pt.n, part = pt.part, parts = pt.parts;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -648,13 +666,21 @@ cudaError_t launch_main(K kern, int threads, int smem, const PagedArgs& a, int h
 
 template <typename T, int D>
 cudaError_t launch_t(const PagedArgs& a, cudaStream_t st) {
-  static std::atomic<unsigned long long> done{0}, done2{0};
   cudaError_t e;
   if constexpr (sizeof(T) == 2 && D >= 64) {
-    e = a.four_warps
-            ? launch_main(attn_decode_tc<D, 4>, 128, TcSmem<D, 4>::BYTES, a, 16, st, done)
-            : launch_main(attn_decode_tc<D, 2>, 64, TcSmem<D, 2>::BYTES, a, 16, st, done2);
+    auto go = [&](auto w, auto tight) {
+      static std::atomic<unsigned long long> raised{0};
+      constexpr int W = decltype(w)::value;
+      return launch_main(attn_decode_tc<D, W, decltype(tight)::value>, W * 32, TcSmem<D, W>::BYTES,
+                         a, 16, st, raised);
+    };
+    using std::integral_constant;
+    const auto warps = [&](auto w) {
+      return a.tight ? go(w, std::true_type{}) : go(w, std::false_type{});
+    };
+    e = a.four_warps ? warps(integral_constant<int, 4>{}) : warps(integral_constant<int, 2>{});
   } else {
+    static std::atomic<unsigned long long> done{0};
     e = launch_main(attn_decode_simt<T, D>, kSWarps * 32, (int)sizeof(SimtSmem<T, D>), a, kSHeads,
                     st, done);
   }
@@ -674,7 +700,10 @@ constexpr int held(int bytes, int threads) {
 // places.  With more than 1024 sequences counting would take too long, and balance is good
 // without a cut.  Measured, four warps against two in a single round: 16 sequences of 4096 (8 key
 // heads, d = 128) 54 us and 50, 32 with a window of 1024 (2 key heads) 15.0 and 16.7; parts of
-// 1024 against 512 in several rounds: 64 sequences of 1000 46 us and 54.
+// 1024 against 512 in several rounds: 64 sequences of 1000 46 us and 54; the search for the
+// shortest parts against places kept for every sequence's last part (8 key heads, d = 128): 37
+// sequences of up to 6000 94 us and 112, 32 of up to 8192 105 and 119, 8 of up to 16384 62 and 64
+// (64 of up to 8192 with 4 key heads of d = 64: 60 and 58.5).
 template <typename T, int D>
 void plan_t(PagedArgs& a, long most) {
   constexpr bool tc = sizeof(T) == 2 && D >= 64;
@@ -693,6 +722,7 @@ void plan_t(PagedArgs& a, long most) {
   a.stride = a.four_warps && by_tokens <= round4 ? (int)each : 0;
   const long n = a.places + a.N < by_tokens && !a.stride ? a.places + (long)a.N : by_tokens;
   a.nparts = a.N > 1024 || n <= a.N ? 0 : (int)n;
+  a.tight = one && a.N <= 64;            // (at most two sequences a lane to add up again)
 }
 
 template <typename T>

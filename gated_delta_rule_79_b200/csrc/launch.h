@@ -194,8 +194,9 @@ struct PagedArgs {
   float per_place;      // 1 / places, rounded up
   int stride;           // places of each sequence, or 0: as the tokens fall
   bool four_warps;      // of a CTA, or two
+  bool tight;           // look for the shortest parts that fit `nparts` places
 };
-void attn_decode_plan(PagedArgs& a, long capacity);   // sets the last six
+void attn_decode_plan(PagedArgs& a, long capacity);   // sets the last seven
 cudaError_t launch_attn_decode(const PagedArgs& a, cudaStream_t stream);
 
 struct AppendArgs {

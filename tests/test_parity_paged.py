@@ -144,6 +144,25 @@ def test_batches_that_are_cut_unevenly(dtype, lens, Hq, Hkv, d, extra):
     assert torch.equal(o, again)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,Hq,Hkv,d,most", [(33, 8, 8, 128, 700), (37, 8, 8, 128, 331), (64, 4, 4, 64, 400),
+                                             (2, 16, 16, 128, 1500), (12, 8, 8, 32, 640)])
+def test_places_that_the_parts_fill(dtype, N, Hq, Hkv, d, most):
+    """Batches that take one round of CTAs: the parts are the shortest that the places hold."""
+    import gated_delta_rule_79_b200 as g
+    lens = [most] + [(i * 7919 + 13) % most for i in range(1, N)]
+    lens[-1] = 0
+    c = Cache(lens, Hkv, d, 16, dtype, extra=40, seed=8)
+    q = randn((N, Hq, d), 9, dtype)
+    kc, vc, table, t = c.cuda()
+    _check(c, q, g.attn_decode(q.cuda(), kc, vc, table, t), dtype)
+    # the same tables with every sequence but the empty one cut to one length
+    n = min(x for x in lens if x)
+    c.lens = [min(x, n) for x in lens]
+    c.k, c.v = [x[:n] for x in c.k], [x[:n] for x in c.v]
+    _check(c, q, g.attn_decode(q.cuda(), kc, vc, table, t.clamp(max=n)), dtype)
+
+
 def test_pages_and_lengths_outside_the_cache_are_left_out_and_reported():
     import gated_delta_rule_79_b200 as g
     c = Cache([100, 100, 100], 2, 128, 16, "bf16")
