@@ -184,12 +184,13 @@ struct Rows {
   __device__ __forceinline__ long find(int x, int end) const {
     if (x >= end) return -1;
     const int t = v.token(x);
-    if (v.fresh && t == v.len - 1) return -2;
     const int pg = a.table[(size_t)n * a.max_pages + (t >> a.page_shift)];
     if ((unsigned)pg >= (unsigned)a.npages) {
       report(a.status);
       return -1;
     }
+    // (also the new token is left out when its page, where it is to be kept, does not exist)
+    if (v.fresh && t == v.len - 1) return -2;
     return ((long)pg << a.page_shift) + (t & ((1 << a.page_shift) - 1));
   }
 };

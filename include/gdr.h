@@ -454,7 +454,7 @@ GDR_API gdr_status attn_backward(const void* q, const void* k, const void* v, co
  * hold visible tokens are read (those before a window may have been given away).  Lengths and
  * table entries are read on the device: lengths are clamped to 0 .. max_pages * page (a new
  * token past that is neither stored nor seen), tokens whose table entry is outside the pool are
- * left out, and either is recorded in the status word (GDR_ERR_INVALID_ARG from
+ * left out (so is a new token: neither stored nor seen), and either is recorded in the status word (GDR_ERR_INVALID_ARG from
  * gdr_workspace_status).  Sequences must not share the page of
  * their new token.  The workspace must hold gdr_attn_decode_workspace_bytes(...) bytes.
  *
