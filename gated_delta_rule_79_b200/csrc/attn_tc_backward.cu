@@ -17,11 +17,12 @@
 // overwrite S and dP as bf16 operands.
 //
 // P and dS are rounded to bf16, as what they multiply is; the scale is applied to the fp32 sums.
-// Where a query sees few keys (up to kFew) the rounded o inside D weighs as much as these
-// roundings (all three together passed one and a half times the rounding of the results), so
-// there P and dS enter as two bf16 terms each, the second in the columns that the first leaves
-// free: four or eight more products a step (15 % of the time at a window of 1024, where it is not
-// done; the error of dq is 1.1 times the rounding of the result with it, 1.5 without).
+// Where a query sees few keys (up to kFew, or in a prompt of up to 4 kFew + 3 tokens) the rounded o
+// inside D weighs as much as these roundings (all three together are 1.5 times the rounding of the
+// results), so there P and dS enter as two bf16 terms each, the second in the columns that the first
+// leaves free: four or eight more products a step (15 % of the time at a window of 1024 over 4096
+// tokens, where it is not done; the errors of dq and dk are 1.1 to 1.2 times the rounding of the
+// result with it, 1.5 without, those of dv 1.0 and 1.4).
 //
 // Key tiles that many queries see are cut (attn_parts.cuh).
 
@@ -555,9 +556,10 @@ size_t attn_backward_tc_bytes(const AttnArgs& f) {
 }
 
 cudaError_t launch_attn_backward_tc(const AttnGradArgs& a, cudaStream_t st) {
-  // (without a window the first queries see few keys however long the prompt is, which shows up
-  // to about 2048 tokens)
-  const long seen = a.f.window ? (long)a.f.window + a.f.sinks : a.f.Tk / 4;
+  // The window bounds what every query sees; however wide it is, the first queries of a prompt see
+  // few keys, which shows up to about 2048 tokens.  (Lengths lie on the device and do not count.)
+  long seen = a.f.Tk / 4;
+  if (a.f.window && seen > (long)a.f.window + a.f.sinks) seen = (long)a.f.window + a.f.sinks;
   if (seen <= kFew) return a.f.d == 64 ? launch_t<64, true>(a, st) : launch_t<128, true>(a, st);
   return a.f.d == 64 ? launch_t<64, false>(a, st) : launch_t<128, false>(a, st);
 }

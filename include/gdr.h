@@ -419,7 +419,12 @@ GDR_API gdr_status lin_backward(const void* q, const void* k, const void* v, con
  * nothing gets o = 0 and lse = -inf.  scale > 0.  Keys, values and queries at and past a
  * sequence's length may hold anything, NaN included; elsewhere they are finite.
  * With bf16 tensors the softmax weights (and, in the gradients, the weights' gradients) are
- * rounded to bf16 before they meet the values; sums and statistics are fp32.
+ * rounded to bf16 before they meet the values; sums and statistics are fp32.  For head sizes 64
+ * and 128 the gradients hold both as two bf16 terms (16 bits) where a query sees at most 512 keys
+ * (window + sinks) or Tk is at most 2051: lengths do not count, so short sequences in a long
+ * padded batch get one term.  Errors of dq, dk and dv against the norm of the result: at most
+ * 0.0020 with two terms, 0.0026 with one, where rounding the exact result gives 0.0017.  (Head
+ * size 32, and fp32 tensors, are computed in fp32.)
  *
  * attn_backward: the gradients of q, k, v in the tensors' type for dO [B, Tq, Hq, d], from
  * the forward's o and lse; zero for what no query sees.  Deterministic.  No output may
