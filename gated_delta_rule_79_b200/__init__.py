@@ -12,7 +12,7 @@ _PUBLIC = ("gdn_prefill", "kda_prefill", "gdn_decode", "kda_decode", "gdn_verify
            "gdn_prefill_varlen", "kda_prefill_varlen", "gdn_backward", "kda_backward",
            "lin_prefill", "lin_decode", "lin_backward", "lin_workspace_bytes",
            "attn_prefill", "attn_backward", "attn_workspace_bytes", "attn_decode",
-           "attn_decode_workspace_bytes", "kv_append",
+           "attn_decode_workspace_bytes", "kv_append", "mixer_workspace",
            "backward_workspace_bytes", "PROLOGUE_L2NORM_QK", "PROLOGUE_GATE_LOGIT",
            "VERIFY_MAX_TOKENS", "prefill_workspace",
            "workspace_status", "check_status", "noalloc_status", "prefill_path", "timing_start", "timing_stop", "GdrError", "lib", "LIB_PATH", "EXPORTS", "GDR_OK",

@@ -500,16 +500,52 @@ def _maybe(t, name, shape, dtype, device):
     return None if t is None else _same(t, name, shape, dtype, device)
 
 
-def _scratch(workspace, need, device, what):
-    """The call's workspace: the caller's, or one from torch's stream-ordered allocator (so a
-    captured graph owns what it uses).  Returns (tensor, nbytes)."""
+_kept = {}             # (device, stream): (workspace, its bytes, lock)
+
+
+def mixer_workspace(device=None, stream=None):
+    """The workspace of the linear- and softmax-attention calls on `stream` (None: the device's
+    current one) that are given none.  Its status word is kept from call to call until
+    workspace_status reads it, so that ``workspace_status(mixer_workspace())`` tells of a wait
+    that gave up, or of a length or page outside a paged cache, in any of them.  (A call that is
+    captured into a graph takes a workspace from the graph's own pool instead, which nothing
+    reads: give such a call a zero-filled one to be told.)"""
+    dev = torch.device("cuda" if device is None else device)
+    if dev.index is None:
+        dev = torch.device("cuda", torch.cuda.current_device())
+    with _on(dev, stream):
+        return _keep(256, dev, _raw(dev, stream))[0]
+
+
+def _keep(need, device, raw):
+    """A kept workspace of at least `need` bytes, inside _on(device, stream)."""
+    key = device.index, raw
+    got = _kept.get(key)
+    if got is None or got[1] < need:
+        with _ws_lock:
+            got = _kept.get(key)
+            if got is None or got[1] < need:
+                buf = torch.zeros(max(need, 1 << 12), dtype=torch.uint8, device=device)
+                if got is not None:              # what is on record stays so
+                    buf[:256].copy_(got[0][:256])
+                got = _kept[key] = (buf, buf.numel(), threading.Lock())
+    return got
+
+
+def _scratch(workspace, need, device, what, raw):
+    """The call's workspace, inside _on(device, stream): the caller's, or the one kept for this
+    stream, or in a capture one from torch's allocator (so a captured graph owns what it uses).
+    Returns (tensor, nbytes, what to hold while the call enqueues its kernels: those of two
+    threads on one stream must not mix in one workspace)."""
     if need == 0:
         raise GdrError(GDR_ERR_INVALID_ARG, f"invalid {what} sizes")
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=device), need
+        if torch.cuda.is_current_stream_capturing():
+            return torch.empty(need, dtype=torch.uint8, device=device), need, _HERE_ALREADY
+        return _keep(need, device, raw)
     if workspace.device != device or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the inputs' device")
-    return workspace, workspace.numel() * workspace.element_size()
+    return workspace, workspace.numel() * workspace.element_size(), _HERE_ALREADY
 
 
 def _cuda(t, name, dim, form):
@@ -549,7 +585,8 @@ def lin_prefill(q, k, v, decay, s0=None, *, o=None, s_final=None, stream=None, w
     q, k [B, T, H, d_k] and v [B, T, H, d_v], all float32 or all bfloat16; decay [H] float32 in
     [0, 1]; s0 [B, H, d_v, d_k] float32 or None.  Returns (o, s_final), o in the inputs' type;
     pass s_final=False to skip the final state, or s_final=s0 to carry in place.  workspace:
-    a zero-filled uint8 tensor of lin_workspace_bytes(...) to read with workspace_status.
+    a zero-filled uint8 tensor of lin_workspace_bytes(...) to read with workspace_status
+    (None: mixer_workspace()).
     """
     dev = _cuda(q, "q", 4, "[B, T, H, d_k]")
     B, T, H, dk = q.shape
@@ -563,9 +600,12 @@ def lin_prefill(q, k, v, decay, s0=None, *, o=None, s_final=None, stream=None, w
     with _on(dev, stream):
         o = _out_like(o, "o", v)
         sf = None if s_final is False else _out(s_final, "s_final", state, torch.float32, dev)
-        ws, nws = _scratch(workspace, _lin_bytes(B, T, H, dk, dv, code, 0), dev, "lin_prefill")
-        _check(lib.lin_prefill(*ptrs, o.data_ptr(), None if sf is None else sf.data_ptr(), B, T, H,
-                               dk, dv, code, ws.data_ptr(), nws, _raw(dev, stream)))
+        raw = _raw(dev, stream)
+        ws, nws, lock = _scratch(workspace, _lin_bytes(B, T, H, dk, dv, code, 0), dev,
+                                 "lin_prefill", raw)
+        with lock:
+            _check(lib.lin_prefill(*ptrs, o.data_ptr(), None if sf is None else sf.data_ptr(),
+                                   B, T, H, dk, dv, code, ws.data_ptr(), nws, raw))
     return o, sf
 
 
@@ -603,10 +643,13 @@ def lin_backward(q, k, v, decay, s0, do, ds_final=None, *, workspace=None, strea
     with _on(dev, stream):
         dq, dk_, dv_ = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
         ds0 = torch.empty(state, dtype=torch.float32, device=dev)
-        ws, nws = _scratch(workspace, _lin_bytes(B, T, H, dk, dv, code, 1), dev, "lin_backward")
-        _check(lib.lin_backward(*ptrs, dq.data_ptr(), dk_.data_ptr(), dv_.data_ptr(),
-                                ds0.data_ptr(), B, T, H, dk, dv, code, ws.data_ptr(), nws,
-                                _raw(dev, stream)))
+        raw = _raw(dev, stream)
+        ws, nws, lock = _scratch(workspace, _lin_bytes(B, T, H, dk, dv, code, 1), dev,
+                                 "lin_backward", raw)
+        with lock:
+            _check(lib.lin_backward(*ptrs, dq.data_ptr(), dk_.data_ptr(), dv_.data_ptr(),
+                                    ds0.data_ptr(), B, T, H, dk, dv, code, ws.data_ptr(), nws,
+                                    raw))
     return dq, dk_, dv_, ds0
 
 
@@ -645,7 +688,8 @@ def attn_prefill(q, k, v, *, window=0, sinks=0, scale=None, lengths=None, o=None
     and sees key j when j <= p, j and p < lengths[b] (int32 [B]; None: Tk), and
     p - j < window (0 or None: no window) or j < sinks.  scale: None for d ** -0.5.
     Returns (o in q's type, lse [B, Hq, Tq] float32); a query that sees nothing has o = 0 and
-    lse = -inf.  Pass lse=False to skip it.
+    lse = -inf.  Pass lse=False to skip it.  workspace: a zero-filled uint8 tensor of
+    attn_workspace_bytes(...) to read with workspace_status (None: mixer_workspace()).
     """
     dev, ptrs, B, Tq, Tk, Hq, Hkv, d = _attn_shapes(q, k, v)
     code = _code(q.dtype)
@@ -654,11 +698,14 @@ def attn_prefill(q, k, v, *, window=0, sinks=0, scale=None, lengths=None, o=None
     with _on(dev, stream):
         o = _out_like(o, "o", q)
         lse = None if lse is False else _out(lse, "lse", (B, Hq, Tq), torch.float32, dev)
-        ws, nws = _scratch(workspace, _attn_bytes(B, Tq, Tk, Hq, Hkv, d, w, n, code, 0), dev,
-                           "attn_prefill")
-        _check(lib.attn_prefill(*ptrs, lens, o.data_ptr(), None if lse is None else lse.data_ptr(),
-                                B, Tq, Tk, Hq, Hkv, d, w, n, d ** -0.5 if scale is None else scale,
-                                code, ws.data_ptr(), nws, _raw(dev, stream)))
+        raw = _raw(dev, stream)
+        ws, nws, lock = _scratch(workspace, _attn_bytes(B, Tq, Tk, Hq, Hkv, d, w, n, code, 0), dev,
+                                 "attn_prefill", raw)
+        with lock:
+            _check(lib.attn_prefill(*ptrs, lens, o.data_ptr(),
+                                    None if lse is None else lse.data_ptr(), B, Tq, Tk, Hq, Hkv, d,
+                                    w, n, d ** -0.5 if scale is None else scale, code,
+                                    ws.data_ptr(), nws, raw))
     return o, lse
 
 
@@ -675,12 +722,14 @@ def attn_backward(q, k, v, o, lse, do, *, window=0, sinks=0, scale=None, lengths
     w, n = _int32(window, "window"), _int32(sinks, "sinks")
     with _on(dev, stream):
         dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-        ws, nws = _scratch(workspace, _attn_bytes(B, Tq, Tk, Hq, Hkv, d, w, n, code, 1), dev,
-                           "attn_backward")
-        _check(lib.attn_backward(*ptrs, lens, *given, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
-                                 B, Tq, Tk, Hq, Hkv, d, w, n,
-                                 d ** -0.5 if scale is None else scale, code, ws.data_ptr(), nws,
-                                 _raw(dev, stream)))
+        raw = _raw(dev, stream)
+        ws, nws, lock = _scratch(workspace, _attn_bytes(B, Tq, Tk, Hq, Hkv, d, w, n, code, 1), dev,
+                                 "attn_backward", raw)
+        with lock:
+            _check(lib.attn_backward(*ptrs, lens, *given, dq.data_ptr(), dk.data_ptr(),
+                                     dv.data_ptr(), B, Tq, Tk, Hq, Hkv, d, w, n,
+                                     d ** -0.5 if scale is None else scale, code, ws.data_ptr(),
+                                     nws, raw))
     return dq, dk, dv
 
 
@@ -712,7 +761,8 @@ def attn_decode(q, k_cache, v_cache, page_table, lengths, *, k=None, v=None, win
     the new token's key and value are stored at position lengths[n] - 1 by the same launch.
     window, sinks, scale as in attn_prefill.  Returns o [N, Hq, d]; 0 for an empty sequence.
     Lengths and table entries outside the cache are left out and recorded in the workspace's
-    status word (pass a zero-filled workspace and read it with workspace_status).
+    status word: read it with workspace_status, of the zero-filled workspace given, or of
+    mixer_workspace() when there was none.
     """
     dev = _cuda(q, "q", 3, "[N, Hq, d]")
     N, Hq, d = q.shape
@@ -729,11 +779,13 @@ def attn_decode(q, k_cache, v_cache, page_table, lengths, *, k=None, v=None, win
     w, s = _int32(window, "window"), _int32(sinks, "sinks")
     with _on(dev, stream):
         o = _out_like(o, "o", q)
-        ws, nws = _scratch(workspace, _decode_bytes(N, Hq, Hkv, d, page, max_pages, w, s, code),
-                           dev, "attn_decode")
-        _check(lib.attn_decode(qp, kp, vp, *ptrs, lens, o.data_ptr(), N, Hq, Hkv, d, npages, page,
-                               max_pages, w, s, d ** -0.5 if scale is None else scale, code,
-                               ws.data_ptr(), nws, _raw(dev, stream)))
+        raw = _raw(dev, stream)
+        need = _decode_bytes(N, Hq, Hkv, d, page, max_pages, w, s, code)
+        ws, nws, lock = _scratch(workspace, need, dev, "attn_decode", raw)
+        with lock:
+            _check(lib.attn_decode(qp, kp, vp, *ptrs, lens, o.data_ptr(), N, Hq, Hkv, d, npages,
+                                   page, max_pages, w, s, d ** -0.5 if scale is None else scale,
+                                   code, ws.data_ptr(), nws, raw))
     return o
 
 
@@ -741,7 +793,8 @@ def kv_append(k, v, k_cache, v_cache, page_table, start, counts=None, *, stream=
               workspace=None):
     """Store K tokens of each of N sequences in a paged cache, in place: k, v [N, K, Hkv, d];
     token t < counts[n] (int32 [N]; None: K) goes to position start[n] + t (int32 [N]).
-    Positions and pages outside the cache are skipped (and recorded in ``workspace``)."""
+    Positions and pages outside the cache are skipped, and recorded in ``workspace`` (None:
+    mixer_workspace())."""
     dev = _cuda(k, "k", 4, "[N, K, Hkv, d]")
     N, K, Hkv, d = k.shape
     dt = k.dtype
@@ -752,10 +805,15 @@ def kv_append(k, v, k_cache, v_cache, page_table, start, counts=None, *, stream=
         raise ValueError(f"the caches hold heads {hc} x {dc}, k and v {Hkv} x {d}")
     sp = _same(start, "start", (N,), torch.int32, dev)
     cp = _maybe(counts, "counts", (N,), torch.int32, dev)
-    ws, nws = (None, 0) if workspace is None else _scratch(workspace, 256, dev, "kv_append")
     with _on(dev, stream):
+        raw = _raw(dev, stream)
+        if workspace is None and torch.cuda.is_current_stream_capturing():
+            ws, nws = None, 0
+        else:
+            w, nws, _ = _scratch(workspace, 256, dev, "kv_append", raw)
+            ws = w.data_ptr()
         _check(lib.kv_append(kp, vp, *ptrs, sp, cp, N, K, Hkv, d, npages, page, max_pages, code,
-                             None if ws is None else ws.data_ptr(), nws, _raw(dev, stream)))
+                             ws, nws, raw))
 
 
 def prefill_path(dk, dv, dtype, kda):
@@ -783,8 +841,9 @@ def noalloc_status(stream=None):
 
 
 def workspace_status(workspace, stream=None):
-    """Synchronise and read/clear the device status word of a prefill workspace;
-    raises GdrError(GDR_ERR_TIMEOUT) if a bounded device wait gave up."""
+    """Synchronise and read/clear the device status word of a workspace; raises
+    GdrError(GDR_ERR_TIMEOUT) if a bounded device wait gave up, and
+    GdrError(GDR_ERR_INVALID_ARG) if offsets, lengths or pages read on the device were wrong."""
     dev = workspace.device
     _check(lib.gdr_workspace_status(_ptr(workspace), workspace.numel(), _stream(dev, stream)))
 
