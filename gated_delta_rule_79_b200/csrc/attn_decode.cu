@@ -689,7 +689,9 @@ cudaError_t launch_t(const PagedArgs& a, cudaStream_t st) {
   return launch_after(attn_decode_join<T, D>, dim3((unsigned)(a.N * a.Hq)), 128, 0, st, a);
 }
 
-// CTAs of `bytes` of shared memory and `threads` of 128 registers that an SM holds.
+// CTAs of `bytes` of shared memory that an SM holds, if a thread takes 128 registers, as it does for
+// d = 32 and 64.  For d = 128 it takes up to 209 (bf16, two warps; 168 with four, 149 in fp32), but
+// there shared memory leaves room for 4 (2, 3) CTAs only, which still fit.
 constexpr int held(int bytes, int threads) {
   const int by_smem = 227 * 1024 / (bytes + 1024), by_regs = 512 / threads;
   return by_smem < by_regs ? by_smem : by_regs;

@@ -110,8 +110,8 @@ long host_steps(const AttnArgs& f, int tile) {
   return hi > lo ? ((hi + S - 1) / S - lo / S) * (f.Hq / f.Hkv) : 0;
 }
 
-// For a GPU that holds `ctas` of the kernel's CTAs.  The cap is one and a half times the mean
-// number of steps that each gets: dq runs beside or after the last ones, and parts cost a pass of
+// For a GPU with places for `ctas` of the kernel's CTAs.  The cap is one and a half times the mean
+// number of steps of a place: dq runs beside or after the last ones, and parts cost a pass of
 // fp32 sums through memory.  Measured with 128-key tiles (32 heads, 8 key heads, d = 128): 256
 // tokens 22 us against 31 uncut, 1024 tokens 69 and 107; factors of 1.25 and 2.5 were up to 25 %
 // slower with windows of 512 and 1024.  Parts of tiles with sinks are no longer than the longest

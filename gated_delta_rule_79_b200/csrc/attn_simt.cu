@@ -502,7 +502,12 @@ cudaError_t delta_t(const AttnGradArgs& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-// (two CTAs on an SM)
+// Two places on an SM.  attn_dkv_simt has two CTAs there at d = 32 (80 KB of shared memory each) but
+// one at 64 and 128 (120 and 200 KB), so there a part is at most three quarters of an SM's mean
+// share instead of one and a half.  That measured better on the whole than counting one (forward
+// and gradients, fp32): 2 x 600 tokens, 16 heads of 64 to 2, window 200: 192 us against 228; 1024
+// tokens, 8 heads of 128 to 2: 416 against 400; 1500 tokens, 4 heads of 64, and 3 x 777, 6 heads of
+// 64: equal.
 Parts plan_simt(const AttnArgs& f) { return plan_parts<kA, kB>(f, 2 * 148); }
 
 template <typename T, int D>
