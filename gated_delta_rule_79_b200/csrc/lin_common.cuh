@@ -1,8 +1,8 @@
 // Linear attention with one decay per head: what its kernels share.
 //
-// "Super Apriel: One Checkpoint, Many Speeds", §2A (Mixer Vocabulary) names token mixers
-// that carry a fixed-size state; this is the plainest of them, without the delta rule's
-// correction.  For every (sequence, head), with the decay a of that head,
+// A token mixer with a state of fixed size, like the two that "Super Apriel: One Checkpoint, Many
+// Speeds", §2A (Mixer Vocabulary) names (GDN and KDA), but without the delta rule's correction;
+// the paper does not name this one.  For every (sequence, head), with the decay a of that head,
 //
 //     S_t = a S_{t-1} + v_t k_t^T,      o_t = S_t q_t                       (S: d_v x d_k)
 //
@@ -42,17 +42,15 @@ __device__ __forceinline__ double log2_decay(float a) {
 // over the thousands of chunks that a decay near 1 reaches across.
 __device__ __forceinline__ double decay_pow(double l2, long n) { return exp2(l2 * (double)n); }
 
-// One segment in processing order: its first token, its length, and how many tokens were
-// processed before it.
+// One segment in processing order: its first token and its length.
 struct Segment {
-  int a, n, before;
+  int a, n;
 };
 __device__ __forceinline__ Segment segment(int p, int rev, int T, int seg_len, int nseg) {
   const int r = rev ? nseg - 1 - p : p;
   Segment s;
   s.a = r * seg_len;
   s.n = min(seg_len, T - s.a);
-  s.before = rev ? T - s.a - s.n : s.a;
   return s;
 }
 
