@@ -313,9 +313,10 @@ gdr_status attn_prefill(const void* q, const void* k, const void* v, const int* 
   AttnArgs a{q, k, v, lengths, o, lse, (unsigned int*)workspace, B, Tq, Tk, Hq, Hkv, d,
              window, sinks, scale, dtype, (float*)((unsigned char*)workspace + kStatusBytes)};
   if ((s = check_workspace(fn, workspace, ws_bytes, attn_need(a, false))) != GDR_OK) return s;
-  const bool tc = attn_tc(d, dtype) && Tk > 0;
-  return done(fn, tc ? launch_attn_forward_tc(a, (cudaStream_t)stream)
-                     : launch_attn_forward_simt(a, (cudaStream_t)stream));
+  cudaStream_t st = (cudaStream_t)stream;
+  if (Tk == 0) return done(fn, launch_attn_no_keys(a, st));
+  return done(fn, attn_tc(d, dtype) ? launch_attn_forward_tc(a, st)
+                                    : launch_attn_forward_simt(a, st));
 }
 
 gdr_status attn_backward(const void* q, const void* k, const void* v, const int* lengths,

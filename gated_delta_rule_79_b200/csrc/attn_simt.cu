@@ -482,6 +482,12 @@ attn_delta_kernel(const T* __restrict__ o, const T* __restrict__ dO, float* __re
   }
 }
 
+// Queries without any key: lse = -inf (and o = 0).
+__global__ void __launch_bounds__(256) attn_no_keys_kernel(float* lse, size_t n) {
+  const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
+  if (i < n) lse[i] = -INFINITY;
+}
+
 template <typename T, int D>
 cudaError_t forward_t(const AttnArgs& a, cudaStream_t st) {
   auto kern = attn_forward_simt<T, D>;
@@ -530,29 +536,37 @@ cudaError_t backward_t(const AttnGradArgs& a, cudaStream_t st) {
 
 }  // namespace
 
+// bf16 with d = 64 or 128 runs on the tensor cores, all but do . o.
 #define GDR_BY_TYPE(fn, dtype, d, ...)                                              \
   do {                                                                              \
     if ((dtype) == GDR_F32) {                                                       \
       if ((d) == 32) return fn<float, 32>(__VA_ARGS__);                             \
       if ((d) == 64) return fn<float, 64>(__VA_ARGS__);                             \
       if ((d) == 128) return fn<float, 128>(__VA_ARGS__);                           \
-    } else {                                                                        \
-      if ((d) == 32) return fn<__nv_bfloat16, 32>(__VA_ARGS__);                     \
-      if ((d) == 64) return fn<__nv_bfloat16, 64>(__VA_ARGS__);                     \
-      if ((d) == 128) return fn<__nv_bfloat16, 128>(__VA_ARGS__);                   \
+    } else if ((d) == 32) {                                                         \
+      return fn<__nv_bfloat16, 32>(__VA_ARGS__);                                    \
     }                                                                               \
-    return cudaErrorInvalidValue;                                                   \
   } while (0)
 
 size_t attn_backward_simt_bytes(const AttnArgs& f) { return part_bytes(f, kA, plan_simt(f)); }
 cudaError_t launch_attn_forward_simt(const AttnArgs& a, cudaStream_t st) {
   GDR_BY_TYPE(forward_t, a.dtype, a.d, a, st);
+  return cudaErrorInvalidValue;
 }
 cudaError_t launch_attn_delta(const AttnGradArgs& a, cudaStream_t st) {
   GDR_BY_TYPE(delta_t, a.f.dtype, a.f.d, a, st);
+  return a.f.d == 64 ? delta_t<__nv_bfloat16, 64>(a, st) : delta_t<__nv_bfloat16, 128>(a, st);
 }
 cudaError_t launch_attn_backward_simt(const AttnGradArgs& a, cudaStream_t st) {
   GDR_BY_TYPE(backward_t, a.f.dtype, a.f.d, a, st);
+  return cudaErrorInvalidValue;
+}
+cudaError_t launch_attn_no_keys(const AttnArgs& a, cudaStream_t st) {
+  const size_t rows = (size_t)a.B * a.Tq * a.Hq, e = a.dtype == GDR_F32 ? 4 : 2;
+  cudaError_t r = cudaMemsetAsync(a.o, 0, rows * a.d * e, st);
+  if (r != cudaSuccess || !a.lse) return r;
+  attn_no_keys_kernel<<<(unsigned)((rows + 255) / 256), 256, 0, st>>>(a.lse, rows);
+  return cudaGetLastError();
 }
 
 }  // namespace gdr

@@ -165,8 +165,9 @@ struct AttnGradArgs {
   void* dk;
   void* dv;
 };
-cudaError_t launch_attn_forward_simt(const AttnArgs& a, cudaStream_t stream);
+cudaError_t launch_attn_forward_simt(const AttnArgs& a, cudaStream_t stream);  // fp32, or d = 32
 cudaError_t launch_attn_forward_tc(const AttnArgs& a, cudaStream_t stream);   // bf16, d >= 64
+cudaError_t launch_attn_no_keys(const AttnArgs& a, cudaStream_t stream);      // Tk = 0
 cudaError_t launch_attn_delta(const AttnGradArgs& a, cudaStream_t stream);
 size_t attn_forward_tc_bytes(const AttnArgs& a);
 size_t attn_backward_tc_bytes(const AttnArgs& f);

@@ -333,12 +333,13 @@ cudaError_t launch_t(const LinScan& sc, cudaStream_t st) {
   return cudaGetLastError();
 }
 
+// (bf16 with both head sizes 64 or 128 runs on the tensor cores)
 template <typename T, int DK>
 cudaError_t launch_dv(const LinScan& sc, cudaStream_t st) {
-  switch (sc.dv) {
-    case 32: return launch_t<T, DK, 32>(sc, st);
-    case 64: return launch_t<T, DK, 64>(sc, st);
-    case 128: return launch_t<T, DK, 128>(sc, st);
+  if (sc.dv == 32) return launch_t<T, DK, 32>(sc, st);
+  if constexpr (sizeof(T) == 4 || DK == 32) {
+    if (sc.dv == 64) return launch_t<T, DK, 64>(sc, st);
+    if (sc.dv == 128) return launch_t<T, DK, 128>(sc, st);
   }
   return cudaErrorInvalidValue;
 }
