@@ -375,9 +375,13 @@ GDR_API gdr_status kda_backward(const void* q, const void* k, const void* v,
  * token only).  States are [B, H, d_v, d_k] fp32 as above; q, k, v, o and the gradients of
  * q, k, v all have the type `dtype`; head sizes {32, 64, 128}; q is used as given.
  *
+ * All of them are finite: a chunk of tokens is multiplied out whole before what lies ahead is
+ * weighed with 0, so a NaN or an infinity also reaches the tokens up to 63 before it (clear what
+ * lies behind the sequences of a padded batch).
+ *
  * lin_prefill: any T >= 0; s0 NULL for zeros; s_final NULL to skip, or s0 itself; otherwise no
  *   output may overlap an input.
- * lin_decode: one token for each of N sequences, the state updated in place.
+ * lin_decode: one token for each of N sequences, the state updated in place; o overlaps no input.
  * lin_backward: gradients of L = sum <dO, o> + <ds_final, S_T> with respect to q, k, v and
  *   s0 (ds0 is written whether s0 was given or not; the decay has none); ds_final NULL for
  *   zeros.  No output may overlap another argument.  Deterministic.
@@ -416,8 +420,9 @@ GDR_API gdr_status lin_backward(const void* q, const void* k, const void* v, con
  * window <= 0 means no window (every j <= p); lengths (int32 device array [B], clamped to
  * 0 .. Tk) may be NULL for Tk.  o_i = sum_j softmax_j(scale q_i.k_j) v_j and lse_i, the
  * natural logarithm of the softmax's sum ([B, Hq, Tq] fp32, may be NULL).  A query that sees
- * nothing gets o = 0 and lse = -inf.  scale > 0.  Keys, values and queries at and past a
- * sequence's length may hold anything, NaN included; elsewhere they are finite.
+ * nothing gets o = 0 and lse = -inf.  scale > 0.  No output may overlap an input.  Keys, values
+ * and queries at and past a sequence's length may hold anything, NaN included; elsewhere they are
+ * finite.
  * With bf16 tensors the softmax weights (and, in the gradients, the weights' gradients) are
  * rounded to bf16 before they meet the values; sums and statistics are fp32.  For head sizes 64
  * and 128 the gradients hold both as two bf16 terms (16 bits) where a query sees at most 512 keys
@@ -453,7 +458,7 @@ GDR_API gdr_status attn_backward(const void* q, const void* k, const void* v, co
  *   page_table   [N, max_pages] int32: token t of sequence n lies in row t % page of page
  *                page_table[n, t / page]
  *   lengths      [N] int32: tokens of each sequence, the new one included; 0 gives o = 0
- *   o            [N, Hq, d]
+ *   o            [N, Hq, d]; overlaps no input
  *
  * The query sits at position lengths[n] - 1; window, sinks, scale as above.  Only pages that
  * hold visible tokens are read (those before a window may have been given away).  Lengths and
