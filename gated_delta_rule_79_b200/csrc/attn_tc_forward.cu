@@ -43,6 +43,7 @@ constexpr int kT = 128;                     // queries and keys of a tile
 constexpr int kWarpsF = 12;
 constexpr int kSMs = 148, kLeast = 3;       // key tiles of a part
 constexpr float kGrow = 8.f;                // log2 of how far a row's weights may grow
+constexpr float kLarge = 16777216.f;        // 2^24: a base past it is rounded by more than 1
 
 template <int D>
 struct FwdLayout {
@@ -184,7 +185,9 @@ attn_forward_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         // O holds the sum up to the previous tile once its product has completed
         if (!(ok = wait(bar(fs.o_done[w]), (ns - 1) & 1u))) break;
         fence_after_sync();
-        const float f = grow ? ex2((mref - top) * c) : 1.f;   // from -inf: 0, and O is 0 too
+        // (the bases as they are rounded, which is what the weights refer to; from -inf: 0, and O
+        // is 0 too)
+        const float f = grow ? ex2(__fmul_rn(mref, c) - __fmul_rn(top, c)) : 1.f;
         if (grow) mref = top;
         l2.x *= f;
         l2.y *= f;
@@ -198,8 +201,17 @@ attn_forward_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
           tmem_st32(tO + 32 * q, o);
         }
       }
-      const float base = mref == -INFINITY ? 0.f : mref * c;
-      const float2 c2 = make_float2(c, c), nb = make_float2(-base, -base);
+      const float base = mref == -INFINITY ? 0.f : __fmul_rn(mref, c);
+      float2 c2 = make_float2(c, c), nb = make_float2(-base, -base);
+      // The exponents c S - base hold what the base's rounding cut off, alike in all of them; of a
+      // base past 2^24 that would leave the exponents' range, so it is taken off again.
+      if (__any_sync(0xffffffffu, fabsf(base) > kLarge)) {
+        const float cut = fabsf(base) > kLarge ? fmaf(mref, c, -base) : 0.f;
+#pragma unroll
+        for (int e = 0; e < kT; ++e) s[e] = fmaf(s[e], c, -base) - cut;
+        c2 = make_float2(1.f, 1.f);
+        nb = make_float2(0.f, 0.f);
+      }
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         float pk[32];

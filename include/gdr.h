@@ -432,7 +432,9 @@ GDR_API gdr_status lin_backward(const void* q, const void* k, const void* v, con
  * size 32, and fp32 tensors, are computed in fp32.)
  *
  * attn_backward: the gradients of q, k, v in the tensors' type for dO [B, Tq, Hq, d], from
- * the forward's o and lse; zero for what no query sees.  Deterministic.  No output may
+ * the forward's o and lse; zero for what no query sees.  It rebuilds each weight as e^(score - lse)
+ * from the fp32 lse, so scores of magnitude M leave the weights a relative error of up to about
+ * M 2^-22 (the forward has none of that size).  Deterministic.  No output may
  * overlap another argument.
  * Workspaces as for the linear mixer, with gdr_attn_workspace_bytes(...) bytes. */
 GDR_API size_t gdr_attn_workspace_bytes(int B, int Tq, int Tk, int Hq, int Hkv, int d, int window,
