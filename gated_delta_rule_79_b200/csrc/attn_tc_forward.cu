@@ -43,7 +43,7 @@ constexpr int kT = 128;                     // queries and keys of a tile
 constexpr int kWarpsF = 12;
 constexpr int kSMs = 148, kLeast = 3;       // key tiles of a part
 constexpr float kGrow = 8.f;                // log2 of how far a row's weights may grow
-constexpr float kLarge = 16777216.f;        // 2^24: a base past it is rounded by more than 1
+constexpr float kLarge = 268435456.f;       // 2^28: the rounding of a base past it may exceed 16
 
 template <int D>
 struct FwdLayout {
@@ -89,6 +89,81 @@ __device__ __forceinline__ PairTiles pair_tiles(const Mask& m, int i0, int Tq, i
   p.first = part * per;
   p.n = max(0, min(per, all - p.first));
   return p;
+}
+
+// A row whose scores are so large that the rounding of its base c m, which stays in its exponents,
+// may have taken the weights out of range: once more by the whole warp, in fp32 from global memory,
+// the differences of scores formed first.  That happens past scores of 2^28 / log2 e only.  (8192
+// tokens, 32 heads: 434 us, 428 without this code and NaN for such rows; 437 to 447 with the
+// rounding taken off in the loop.)
+// i: the query; thread `owner` has its lane of O at tO.  Returns (c m, l) to all.
+template <int D>
+__device__ __forceinline__ float2 redo_row(const AttnArgs& a, const Mask& m, const PairTiles& pt,
+                                           int w, int b, int h, int i, int owner, uint32_t tO) {
+  using T = __nv_bfloat16;
+  const int lane = threadIdx.x & 31;
+  const float c = a.scale * kLog2e;
+  const size_t step = (size_t)a.Hkv * D;
+  const size_t kv = (size_t)b * a.Tk * step + (size_t)(h / (a.Hq / a.Hkv)) * D;
+  const T* q = (const T*)a.q + (((size_t)b * a.Tq + i) * a.Hq + h) * D;
+  auto score = [&](int j, bool sees) {            // each lane its own key
+    float s = -INFINITY;
+    if (sees) {
+      const T* k = (const T*)a.k + kv + j * step;
+      s = 0.f;
+#pragma unroll 1
+      for (int e = 0; e < D; ++e) s = fmaf(Elem<T>::load(q + e), Elem<T>::load(k + e), s);
+    }
+    return s;
+  };
+  float top = -INFINITY, l = 0.f, o[D / 32] = {};
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll 1
+    for (int x = 0; x < pt.n; ++x) {
+      const int tl = pt.tile(x);
+      if (!(w ? pt.t[1] : pt.t[0]).has(tl)) continue;
+      const RowCols rc = row_cols(m, m.off + i, tl * kT);
+#pragma unroll 1
+      for (int j0 = 0; j0 < kT; j0 += 32) {
+        const float s = score(tl * kT + j0 + lane, rc.sees(j0 + lane));
+        if (pass == 0) {
+          top = fmaxf(top, s);
+          continue;
+        }
+        const float p = s == -INFINITY ? 0.f : ex2((s - top) * c);
+        l += p;
+#pragma unroll 1
+        for (int e = 0; e < 32; ++e) {
+          const float pe = __shfl_sync(0xffffffffu, p, e);
+          if (pe == 0.f) continue;                // (hidden keys are not read)
+          const T* v = (const T*)a.v + kv + (tl * kT + j0 + e) * step;
+#pragma unroll
+          for (int u = 0; u < D / 32; ++u) o[u] = fmaf(pe, Elem<T>::load(v + 32 * u + lane), o[u]);
+        }
+      }
+    }
+    if (pass == 0) {
+#pragma unroll
+      for (int f = 16; f; f >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, f));
+    }
+  }
+#pragma unroll
+  for (int f = 16; f; f >>= 1) l += __shfl_xor_sync(0xffffffffu, l, f);
+#pragma unroll
+  for (int u = 0; u < D / 32; ++u) {
+    float t[32];
+    tmem_ld32(tO + 32 * u, t);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+      const float y = __shfl_sync(0xffffffffu, o[u], e);
+      if (lane == owner) t[e] = y;
+    }
+    tmem_st32(tO + 32 * u, t);
+  }
+  tmem_wait_st();
+  return make_float2(top * c, l);
 }
 
 template <int D, bool PARTS>
@@ -185,8 +260,8 @@ attn_forward_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         // O holds the sum up to the previous tile once its product has completed
         if (!(ok = wait(bar(fs.o_done[w]), (ns - 1) & 1u))) break;
         fence_after_sync();
-        // (the bases as they are rounded, which is what the weights refer to; from -inf: 0, and O
-        // is 0 too)
+        // between the bases as they are rounded, which is what the weights refer to (from -inf: 0,
+        // and O is 0 too)
         const float f = grow ? ex2(__fmul_rn(mref, c) - __fmul_rn(top, c)) : 1.f;
         if (grow) mref = top;
         l2.x *= f;
@@ -201,17 +276,8 @@ attn_forward_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
           tmem_st32(tO + 32 * q, o);
         }
       }
-      const float base = mref == -INFINITY ? 0.f : __fmul_rn(mref, c);
-      float2 c2 = make_float2(c, c), nb = make_float2(-base, -base);
-      // The exponents c S - base hold what the base's rounding cut off, alike in all of them; of a
-      // base past 2^24 that would leave the exponents' range, so it is taken off again.
-      if (__any_sync(0xffffffffu, fabsf(base) > kLarge)) {
-        const float cut = fabsf(base) > kLarge ? fmaf(mref, c, -base) : 0.f;
-#pragma unroll
-        for (int e = 0; e < kT; ++e) s[e] = fmaf(s[e], c, -base) - cut;
-        c2 = make_float2(1.f, 1.f);
-        nb = make_float2(0.f, 0.f);
-      }
+      const float base = mref == -INFINITY ? 0.f : mref * c;
+      const float2 c2 = make_float2(c, c), nb = make_float2(-base, -base);
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         float pk[32];
@@ -234,7 +300,17 @@ attn_forward_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     // ---- result ---------------------------------------------------------------------------------
     if (ok && ns > 0) ok = wait(bar(fs.o_done[w]), (ns - 1) & 1u);
     ok = __all_sync(0xffffffffu, ok);
-    const float l = l2.x + l2.y;
+    float l = l2.x + l2.y, base = mref * c;
+    uint32_t redo = __ballot_sync(0xffffffffu, ok && ns > 0 && mref != -INFINITY &&
+                                                   !(fabsf(base) <= kLarge && l < INFINITY));
+    if (__builtin_expect(redo != 0, 0)) {
+      fence_after_sync();
+      for (; redo; redo &= redo - 1) {
+        const int r = __ffs(redo) - 1;
+        const float2 x = redo_row<D>(a, m, pt, w, b, h, iw + (warp & 3) * 32 + r, r, tO);
+        if (lane == r) base = x.x, l = x.y;
+      }
+    }
     const size_t row_at = ((size_t)b * a.Hq + h) * a.Tq + i, rows = (size_t)a.B * a.Hq * a.Tq;
     // l is 0 only where nothing is visible; a NaN passes on
     const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -270,9 +346,9 @@ attn_forward_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
       }
       if (PARTS && i < a.Tq)
         reinterpret_cast<float2*>(a.part + rows * parts * D)[part * rows + row_at] =
-            make_float2(mref * c, ns > 0 ? l : 0.f);
+            make_float2(base, ns > 0 ? l : 0.f);
       else if (!PARTS && a.lse && i < a.Tq)
-        a.lse[row_at] = l == 0.f ? -INFINITY : (mref * c + log2f(l)) * kLn2;
+        a.lse[row_at] = l == 0.f ? -INFINITY : (base + log2f(l)) * kLn2;
     }
   } else {
     fewer_registers<80>();

@@ -56,3 +56,23 @@ def test_decode(dtype, d, sign, power):
     o = g.attn_decode(q[:, 0].cuda().contiguous(), k.view(50, 16, 2, d).cuda(), v.view(50, 16, 2, d).cuda(),
                       table, torch.tensor([800], dtype=torch.int32, device="cuda"), scale=0.3)
     _compare(o[None], q, k, v, dtype, "o", scale=0.3)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Tq,Tk", [(300, 900), (40, 1800)])
+def test_small_differences_of_large_scores(d, Tq, Tk):
+    """Scores of 2^20 (exact in fp32) that rise by some units along the keys, so that weights of the
+    tiles before count still: what was summed is carried over between the rounded bases."""
+    import gated_delta_rule_79_b200 as g
+    gen = torch.Generator().manual_seed(d)
+    q = torch.zeros(1, Tq, 2, d)
+    k = torch.zeros(1, Tk, 1, d)
+    q[..., 0], k[..., 0] = 2.0 ** 10, 2.0 ** 10
+    # whole numbers of eighths, 12 more from one tile of 128 keys to the next
+    q[..., 1], q[..., 2] = 1.0, 1.0
+    k[..., 1] = torch.randint(-8, 9, (1, Tk, 1), generator=gen) / 8
+    k[..., 2] = (torch.arange(Tk) // 128 * 12).view(1, Tk, 1)
+    q, k, v = q.bfloat16(), k.bfloat16(), randn((1, Tk, 1, d), 5, "bf16")
+    o, lse = g.attn_prefill(q.cuda(), k.cuda(), v.cuda(), scale=0.7)
+    ref = _compare(o, q, k, v, "bf16", "o", scale=0.7)
+    close(to64(lse), ref, F32 * (1 + np.abs(ref)), "lse")
