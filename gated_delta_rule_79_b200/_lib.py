@@ -509,7 +509,8 @@ def mixer_workspace(device=None, stream=None):
     workspace_status reads it, so that ``workspace_status(mixer_workspace())`` tells of a wait
     that gave up, or of a length or page outside a paged cache, in any of them.  (A call that is
     captured into a graph takes a workspace from the graph's own pool instead, which nothing
-    reads: give such a call a zero-filled one to be told.)"""
+    reads: give such a call a zero-filled one to be told.)  It grows to what the largest call on
+    the stream needs (..._workspace_bytes) and is kept; calls given one leave it alone."""
     dev = torch.device("cuda" if device is None else device)
     if dev.index is None:
         dev = torch.device("cuda", torch.cuda.current_device())
